@@ -283,6 +283,164 @@ int pv_voxelize_static(const float* points, int64_t num_points, const float poin
                        int32_t* out_coords, int32_t* out_counts, int32_t* out_num_voxels,
                        pv_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Operators on voxel tokens.
+ *
+ * A batch of voxelized frames (pv_voxelize_batch, frames concatenated) is a
+ * ragged sequence of tokens: one row per voxel, frame b the rows
+ * offsets[b] .. offsets[b + 1], coordinates (batch, z, y, x).  The operators
+ * below work on such rows for networks that read them: queries and keys
+ * normalised and rotated by the coordinates, attention inside each frame, and
+ * a gated linear recurrence along each frame, each with its backward pass.
+ *
+ * All of them are asynchronous on `stream`, allocate nothing once their
+ * per-(device, stream) workspace is warm (a call that grows it synchronizes
+ * the stream once), give the same bits for the same inputs on every call, and
+ * check their arguments on the host as pv_voxelize does: a status is returned
+ * and nothing is enqueued.  Row offsets are HOST arrays, read before the call
+ * returns.  Sums, softmax statistics, norms and recurrent states are held in
+ * 32 bits; outputs are rounded once.  Outputs do not overlap inputs unless a
+ * call says so.
+ */
+typedef enum pv_dtype { PV_F32 = 0, PV_BF16 = 1, PV_F16 = 2 } pv_dtype;
+
+/* Rows of heads: element (row, head, d) is data[row * row_stride + head *
+ * head_stride + d], strides in elements.  data and both strides are multiples
+ * of 16 bytes, so slices of a fused projection can be passed as they are. */
+typedef struct pv_heads {
+  void* data;
+  int64_t row_stride;
+  int64_t head_stride;
+} pv_heads;
+
+/*
+ * Queries and keys normalised per head and rotated by position, in one pass:
+ *   n = x / sqrt(mean(x^2) + eps) * weight          (over head_dim)
+ *   (y[p], y[p + D/2]) = (n[p] c - n[p + D/2] s, n[p + D/2] c + n[p] s),
+ *   (c, s) = (cos, sin)(positions[row][p mod axes] * inv_freq[p]),
+ * the angle one binary32 product, as the tables of models hold it.  With one
+ * axis this is the usual rotation along a sequence; with two or three, pairs
+ * take turns on the axes, and voxel coordinates (..., y, x) are passed as they
+ * stand (position_stride = 3 or 4 int32 between rows).
+ *   rows          0 <= rows < 2^31.
+ *   q_heads       >= 1; k_heads >= 0 (0: k, out_k, k_weight unused).
+ *   head_dim      a multiple of 16, 16 .. 256.
+ *   q_weight, k_weight, inv_freq   device float32, [head_dim] and [head_dim / 2].
+ *   positions     device int32, row stride position_stride >= axes, axes 1..3.
+ * The outputs may be the inputs (in place).
+ */
+typedef struct pv_rope_params {
+  int64_t rows;
+  int q_heads, k_heads, head_dim, dtype;
+  const float* q_weight;
+  const float* k_weight;
+  const int32_t* positions;
+  int64_t position_stride;
+  int axes;
+  const float* inv_freq;
+  float eps;
+} pv_rope_params;
+
+int pv_qk_norm_rope(const pv_rope_params* params, const pv_heads* q, const pv_heads* k, const pv_heads* out_q,
+                    const pv_heads* out_k, pv_stream_t stream);
+
+/* Its backward pass: from the gradients of the outputs and the forward
+ * inputs, the gradients of q and k and, in float32, of the two weights
+ * (summed over rows and heads in a fixed order).  dq and dk may be the
+ * gradients' own buffers. */
+int pv_qk_norm_rope_backward(const pv_rope_params* params, const pv_heads* dout_q, const pv_heads* dout_k,
+                             const pv_heads* q, const pv_heads* k, const pv_heads* dq, const pv_heads* dk,
+                             float* dq_weight, float* dk_weight, pv_stream_t stream);
+
+/*
+ * Attention inside frames.  Query i and key j, counted from the start of
+ * their frame b (nq queries, nk keys), score
+ *   s = scale * q . k,  capped to cap * tanh(s / cap) if cap > 0, less
+ *   slopes[h] * (|dz| + |dy| + |dx|) of the two tokens' positions if slopes
+ * is given; j is visible to i if it is in the same frame and, with `causal`,
+ * j <= i + nk - nq or j < prefix[b].  out = softmax(s over visible keys) v;
+ * a query with no visible key gives 0 (its lse is -inf, its gradients 0).
+ * Query head h reads key head h / (q_heads / k_heads).
+ *   frames        1 .. PV_MAX_FRAMES; q_offsets and k_offsets HOST [frames + 1]:
+ *                 0, then never decreasing (empty frames allowed), below 2^31.
+ *   head_dim      a multiple of 8, 8 .. 128; dtype PV_BF16 or PV_F16.
+ *   scale, cap    finite, scale > 0, cap >= 0 (0: no cap).
+ *   slopes        device float32 [q_heads] or NULL; then q_positions and
+ *                 k_positions (device int32, axes 1..3 per row) are needed,
+ *                 |coordinate| < 2^23.  Slopes and positions get no gradient.
+ *   prefix        HOST [frames] or NULL, used with causal only.
+ *   lse           device float32 [q_heads, queries]: the logarithm of each
+ *                 query's softmax sum, or NULL if no backward pass follows.
+ * Rows of other frames never reach a result, whatever they hold; hidden keys of
+ * the same frame have to be finite.
+ */
+typedef struct pv_attention_params {
+  int frames;
+  const int64_t* q_offsets;
+  const int64_t* k_offsets;
+  int q_heads, k_heads, head_dim, dtype;
+  float scale, cap;
+  const float* slopes;
+  const int32_t* q_positions;
+  int64_t q_position_stride;
+  const int32_t* k_positions;
+  int64_t k_position_stride;
+  int axes;
+  int causal;
+  const int64_t* prefix;
+} pv_attention_params;
+
+int pv_attention(const pv_attention_params* params, const pv_heads* q, const pv_heads* k, const pv_heads* v,
+                 const pv_heads* out, float* lse, pv_stream_t stream);
+
+/* Its backward pass: dq, dk, dv from the gradient of out, the forward inputs,
+ * out and lse.  No atomics: sums over queries, keys and shared heads are taken
+ * in a fixed order. */
+int pv_attention_backward(const pv_attention_params* params, const pv_heads* dout, const pv_heads* q,
+                          const pv_heads* k, const pv_heads* v, const pv_heads* out, const float* lse,
+                          const pv_heads* dq, const pv_heads* dk, const pv_heads* dv, pv_stream_t stream);
+
+/*
+ * Gated linear recurrence along each frame, every channel by itself:
+ *   z = 1 / (1 + exp(-gate)),  h[t] = (1 - z[t]) h[t-1] + z[t] x[t],
+ * from h0[b], read from the frame's first row to its last, or from its last to
+ * its first if `reverse`.
+ *   x, gate, out_h  device [rows, channels] of dtype, row strides in elements
+ *                 (x_stride, gate_stride, h_stride >= channels); element aligned.
+ *   frames, offsets   as above (HOST).  channels 1 .. 2^20.
+ *   h0            device float32 [frames, channels], or NULL for zeros.
+ *   out_last      device float32 [frames, channels]: the state after each
+ *                 frame's last step (h0 for an empty frame), or NULL.
+ *   out_states    device float32 [pv_gated_scan_states(...), channels] or NULL:
+ *                 the state before each stretch of steps, for the backward pass.
+ */
+typedef struct pv_scan_params {
+  int frames;
+  const int64_t* offsets;
+  int64_t channels;
+  int dtype;
+  int reverse;
+  const void* x;
+  int64_t x_stride;
+  const void* gate;
+  int64_t gate_stride;
+} pv_scan_params;
+
+int pv_gated_scan(const pv_scan_params* params, const float* h0, void* out_h, int64_t h_stride, float* out_last,
+                  float* out_states, pv_stream_t stream);
+
+/* Rows of out_states for these offsets, channels, dtype (from params; strides
+ * matter too, the data pointers do not), or a negative status. */
+int64_t pv_gated_scan_states(const pv_scan_params* params);
+
+/* Its backward pass: from the gradients of h ([rows, channels], stride
+ * dh_stride) and of the last states (float32 [frames, channels], NULL: zeros)
+ * the gradients of x and gate (strides dx_stride, dgate_stride) and of h0
+ * (float32 [frames, channels] or NULL).  `states` is the forward call's. */
+int pv_gated_scan_backward(const pv_scan_params* params, const void* dh, int64_t dh_stride, const float* dlast,
+                           const float* states, void* dx, int64_t dx_stride, void* dgate, int64_t dgate_stride,
+                           float* dh0, pv_stream_t stream);
+
 /* Grid extents for a range and a cell size: PV_OK, PV_ERR_INVALID or
  * PV_ERR_UNSUPPORTED, with grid_out = {grid_x, grid_y, grid_z}. */
 int pv_grid_size(const float point_cloud_range[6], const float voxel_size[3], int64_t grid_out[3]);

@@ -32,7 +32,8 @@ STATUS = {
 EXPORTS = (
     "pv_voxelize", "pv_voxelize_ex", "pv_voxelize_host", "pv_voxelize_static", "pv_voxelize_batch",
     "pv_voxel_downsample", "pv_fps", "pv_grid_size", "pv_query_plan", "pv_release_workspace", "pv_status_string",
-    "pv_version",
+    "pv_version", "pv_qk_norm_rope", "pv_qk_norm_rope_backward", "pv_attention", "pv_attention_backward",
+    "pv_gated_scan", "pv_gated_scan_states", "pv_gated_scan_backward",
 )
 
 FPS_MAX_POINTS = 212992  # PV_FPS_MAX_POINTS
@@ -60,6 +61,34 @@ class Plan(ctypes.Structure):
                 ("table_slots", ctypes.c_int64), ("list_stride", ctypes.c_int),
                 ("ctas", ctypes.c_int), ("threads", ctypes.c_int),
                 ("points_per_cta", ctypes.c_int64), ("workspace_bytes", ctypes.c_int64)]
+
+
+class Heads(ctypes.Structure):
+    """pv_heads: rows of heads, strides in elements."""
+
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class RopeParams(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("q_heads", ctypes.c_int), ("k_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("position_stride", ctypes.c_int64),
+                ("axes", ctypes.c_int), ("inv_freq", ctypes.c_void_p), ("eps", ctypes.c_float)]
+
+
+class AttentionParams(ctypes.Structure):
+    _fields_ = [("frames", ctypes.c_int), ("q_offsets", ctypes.POINTER(ctypes.c_int64)),
+                ("k_offsets", ctypes.POINTER(ctypes.c_int64)), ("q_heads", ctypes.c_int), ("k_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int), ("scale", ctypes.c_float), ("cap", ctypes.c_float),
+                ("slopes", ctypes.c_void_p), ("q_positions", ctypes.c_void_p), ("q_position_stride", ctypes.c_int64),
+                ("k_positions", ctypes.c_void_p), ("k_position_stride", ctypes.c_int64), ("axes", ctypes.c_int),
+                ("causal", ctypes.c_int), ("prefix", ctypes.POINTER(ctypes.c_int64))]
+
+
+class ScanParams(ctypes.Structure):
+    _fields_ = [("frames", ctypes.c_int), ("offsets", ctypes.POINTER(ctypes.c_int64)), ("channels", ctypes.c_int64),
+                ("dtype", ctypes.c_int), ("reverse", ctypes.c_int), ("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64),
+                ("gate", ctypes.c_void_p), ("gate_stride", ctypes.c_int64)]
 
 
 _lock = threading.Lock()
@@ -100,6 +129,21 @@ def load(path: Optional[str] = None):
         lib.pv_voxel_downsample.restype = ci
         lib.pv_fps.argtypes = [vp, ci, i64, i64, i64, vp, vp, vp, vp]
         lib.pv_fps.restype = ci
+        h, rope, attn, scan = (ctypes.POINTER(t) for t in (Heads, RopeParams, AttentionParams, ScanParams))
+        lib.pv_qk_norm_rope.argtypes = [rope, h, h, h, h, vp]
+        lib.pv_qk_norm_rope.restype = ci
+        lib.pv_qk_norm_rope_backward.argtypes = [rope, h, h, h, h, h, h, vp, vp, vp]
+        lib.pv_qk_norm_rope_backward.restype = ci
+        lib.pv_attention.argtypes = [attn, h, h, h, h, vp, vp]
+        lib.pv_attention.restype = ci
+        lib.pv_attention_backward.argtypes = [attn, h, h, h, h, h, vp, h, h, h, vp]
+        lib.pv_attention_backward.restype = ci
+        lib.pv_gated_scan.argtypes = [scan, vp, vp, i64, vp, vp, vp]
+        lib.pv_gated_scan.restype = ci
+        lib.pv_gated_scan_states.argtypes = [scan]
+        lib.pv_gated_scan_states.restype = i64
+        lib.pv_gated_scan_backward.argtypes = [scan, vp, i64, vp, vp, vp, i64, vp, i64, vp, vp]
+        lib.pv_gated_scan_backward.restype = ci
         lib.pv_grid_size.argtypes = [f, f, ctypes.POINTER(ctypes.c_int64)]
         lib.pv_grid_size.restype = ci
         lib.pv_query_plan.argtypes = [i64, f, f, ci, ci, ctypes.POINTER(Options), ctypes.POINTER(Plan)]

@@ -11,10 +11,13 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 # Every translation unit of libpv.so: the block-tile voxelizer, the unordered
 # voxelizer, centroid downsampling, the host side with the C ABI, and farthest
-# point sampling (kernel and entry); pv_device.cuh is the kernels' shared code.
+# point sampling (kernel and entry), with pv_device.cuh shared; and the operators
+# on voxel tokens (rotation of queries and keys, the gated recurrence,
+# attention), with pv_seq.cuh, pv_seq.cu and pv_attn.cuh shared.
 SRCS = [os.path.join(CSRC, f) for f in ("pv_ordered.cu", "pv_ordered_half.cu", "pv_unordered.cu", "pv_downsample.cu",
-                                         "pv_downsample_half.cu", "pv_host.cu", "pv_fps.cu")]
-HEADERS = [os.path.join(CSRC, "pv_device.cuh")]
+                                         "pv_downsample_half.cu", "pv_host.cu", "pv_fps.cu", "pv_seq.cu", "pv_rope.cu",
+                                         "pv_scan.cu", "pv_attn.cu")]
+HEADERS = [os.path.join(CSRC, f) for f in ("pv_device.cuh", "pv_seq.cuh", "pv_attn.cuh")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libpv.so")
 

@@ -16,6 +16,10 @@
 #include <new>
 #include <utility>
 
+namespace pvs {
+int release_scratch();  // the token operators' workspaces (pv_seq.cu)
+}
+
 namespace {
 
 using namespace pvk;
@@ -838,7 +842,8 @@ int pv_release_workspace(void) {
     delete ws;
   }
   g_ws.clear();
-  return st;
+  const int seq = pvs::release_scratch();
+  return st == PV_OK ? seq : st;
 }
 
 const char* pv_status_string(int status) {

@@ -1,0 +1,399 @@
+// Queries and keys normalised per head and rotated by position, in one pass,
+// and the backward pass (pv_qk_norm_rope, pv_qk_norm_rope_backward in pv.h).
+//
+// A row (token, head) is D elements.  A group of `lanes` lanes (a power of
+// two) holds one: each lane 16 bytes of the first half and the same 16 bytes
+// of the second half, so both elements of a rotated pair are in one lane.
+// Consecutive groups take consecutive heads of a token, so a warp reads and
+// writes whole contiguous lines.  The cosines and sines of a tile of tokens
+// are worked out once for all heads, into shared memory.
+//
+// Bound by memory: each element is read once and written once (backward: two
+// reads and one write).
+
+#include "pv_seq.cuh"
+
+#include <algorithm>
+#include <cmath>
+
+namespace {
+
+using namespace pvs;
+
+constexpr int kThreads = 256;
+constexpr int kTableFloats = 8192;  // cosines and sines of a tile: 32 KB of shared memory
+constexpr int kMaxBlocks = 1216;    // blocks of the backward pass: one row of weight sums each
+
+struct View {
+  char* data;
+  long long row, head;  // strides in bytes
+};
+
+struct RopeArgs {
+  View q, k, oq, ok;    // forward: inputs and outputs; backward: forward inputs and their gradients
+  View gq, gk;          // backward: gradients of the outputs
+  const float* wq;
+  const float* wk;
+  const int32_t* pos;
+  long long pos_stride;
+  const float* freq;
+  int rows, hq, hk, D, axes;
+  int lanes_log2;       // lanes of a group
+  int tile;             // tokens of a tile
+  float eps;
+  float* partial;       // backward: [blocks, 2, D] weight sums
+  unsigned int* done;   // backward: blocks that have written theirs
+  float* dwq;
+  float* dwk;
+};
+
+__device__ __forceinline__ float group_sum(float v, int lanes) {
+  for (int o = lanes >> 1; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+
+// Cosines and sines of the tile's tokens, [token][pair].
+__device__ __forceinline__ void fill_table(const RopeArgs& a, int t0, int tokens, float2* table) {
+  const int half = a.D >> 1;
+  for (int i = threadIdx.x; i < tokens * half; i += kThreads) {
+    const int t = i / half, p = i - t * half;
+    const float at = static_cast<float>(a.pos[static_cast<long long>(t0 + t) * a.pos_stride + p % a.axes]);
+    float s, c;
+    sincosf(at * a.freq[p], &s, &c);
+    table[i] = make_float2(c, s);
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) pv_rope_kernel(const RopeArgs a) {
+  constexpr int V = Pack<T>::kN;
+  __shared__ __align__(16) float2 table[kTableFloats / 2];
+  const int half = a.D >> 1;
+  const int lanes = 1 << a.lanes_log2;
+  const int sub = threadIdx.x & (lanes - 1);
+  const int group = threadIdx.x >> a.lanes_log2, groups = kThreads >> a.lanes_log2;
+  const bool on = sub * V < half;
+  const int heads = a.hq + a.hk;
+  const float inv = 1.0f / static_cast<float>(a.D);
+  wait_prior_grid();
+  const int t0 = blockIdx.x * a.tile;
+  const int tokens = min(a.tile, a.rows - t0);
+  fill_table(a, t0, tokens, table);
+  __syncthreads();
+  for (int r0 = 0; r0 < tokens * heads; r0 += groups) {
+    const int r = r0 + group;
+    const bool live = on && r < tokens * heads;
+    const int t = r / heads, h = r - t * heads;
+    float x[2 * V];
+    const bool isq = h < a.hq;
+    const View& in = isq ? a.q : a.k;
+    const View& out = isq ? a.oq : a.ok;
+    const int hh = isq ? h : h - a.hq;
+    float ss = 0.0f;
+    if (live) {
+      const char* p = in.data + (t0 + t) * in.row + hh * in.head + sub * 16;
+      Pack<T>::load(p, x);
+      Pack<T>::load(p + half * sizeof(T), x + V);
+#pragma unroll
+      for (int i = 0; i < 2 * V; ++i) ss = fmaf(x[i], x[i], ss);
+    }
+    ss = group_sum(ss, lanes);
+    if (live) {
+      const float rs = rsqrtf(fmaf(ss, inv, a.eps));
+      const float* w = (isq ? a.wq : a.wk) + sub * V;
+      const float2* cs = table + t * half + sub * V;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float n0 = x[i] * rs * w[i], n1 = x[V + i] * rs * w[half + i];
+        const float2 c = cs[i];
+        x[i] = fmaf(n0, c.x, -(n1 * c.y));
+        x[V + i] = fmaf(n1, c.x, n0 * c.y);
+      }
+      char* p = out.data + (t0 + t) * out.row + hh * out.head + sub * 16;
+      Pack<T>::store(p, x);
+      Pack<T>::store(p + half * sizeof(T), x + V);
+    }
+  }
+  allow_next_grid();
+}
+
+// Backward.  With g the gradient turned back, n = x r, r = 1 / sqrt(mean(x^2) + eps):
+// dx = r (g w - n mean(g w n)), dw = sum of g n over rows.  A lane keeps the
+// weight sums of its own columns in registers over all of the block's tiles;
+// a block's lanes are joined in shared memory, the blocks by the last one to
+// finish, both in a fixed order.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) pv_rope_backward_kernel(const RopeArgs a) {
+  constexpr int V = Pack<T>::kN;
+  __shared__ __align__(16) float2 table[kTableFloats / 2];
+  __shared__ bool last;
+  const int half = a.D >> 1;
+  const int lanes = 1 << a.lanes_log2;
+  const int sub = threadIdx.x & (lanes - 1);
+  const int group = threadIdx.x >> a.lanes_log2, groups = kThreads >> a.lanes_log2;
+  const bool on = sub * V < half;
+  const float inv = 1.0f / static_cast<float>(a.D);
+  wait_prior_grid();
+  const int tiles = (a.rows + a.tile - 1) / a.tile;
+  float* sums = reinterpret_cast<float*>(table);
+  for (int side = 0; side < 2; ++side) {
+    const View& in = side ? a.k : a.q;
+    const View& gr = side ? a.gk : a.gq;
+    const View& out = side ? a.ok : a.oq;
+    const float* wsrc = side ? a.wk : a.wq;
+    const int heads = side ? a.hk : a.hq;
+    if (heads == 0) continue;
+    float w[2 * V], acc[2 * V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      w[i] = on ? wsrc[sub * V + i] : 0.0f;
+      w[V + i] = on ? wsrc[half + sub * V + i] : 0.0f;
+      acc[i] = acc[V + i] = 0.0f;
+    }
+    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+      const int t0 = tile * a.tile;
+      const int tokens = min(a.tile, a.rows - t0);
+      __syncthreads();
+      fill_table(a, t0, tokens, table);
+      __syncthreads();
+      for (int r0 = 0; r0 < tokens * heads; r0 += groups) {
+        const int r = r0 + group;
+        const bool live = on && r < tokens * heads;
+        const int t = r / heads, h = r - t * heads;
+        float x[2 * V], g[2 * V];
+        float ss = 0.0f, dot = 0.0f;
+        if (live) {
+          const char* p = in.data + (t0 + t) * in.row + h * in.head + sub * 16;
+          const char* pg = gr.data + (t0 + t) * gr.row + h * gr.head + sub * 16;
+          Pack<T>::load(p, x);
+          Pack<T>::load(p + half * sizeof(T), x + V);
+          Pack<T>::load(pg, g);
+          Pack<T>::load(pg + half * sizeof(T), g + V);
+          const float2* cs = table + t * half + sub * V;
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            const float2 c = cs[i];
+            const float g0 = fmaf(g[i], c.x, g[V + i] * c.y), g1 = fmaf(g[V + i], c.x, -(g[i] * c.y));
+            g[i] = g0;
+            g[V + i] = g1;
+          }
+#pragma unroll
+          for (int i = 0; i < 2 * V; ++i) {
+            ss = fmaf(x[i], x[i], ss);
+            dot = fmaf(g[i] * w[i], x[i], dot);
+          }
+        }
+        ss = group_sum(ss, lanes);
+        dot = group_sum(dot, lanes);
+        if (live) {
+          const float rs = rsqrtf(fmaf(ss, inv, a.eps));
+          const float m = dot * inv * rs * rs;  // mean(g w n) / |x| scale: n = x rs
+#pragma unroll
+          for (int i = 0; i < 2 * V; ++i) {
+            const float n = x[i] * rs;
+            acc[i] = fmaf(g[i], n, acc[i]);
+            x[i] = rs * fmaf(g[i], w[i], -(m * x[i]));
+          }
+          char* p = out.data + (t0 + t) * out.row + h * out.head + sub * 16;
+          Pack<T>::store(p, x);
+          Pack<T>::store(p + half * sizeof(T), x + V);
+        }
+      }
+    }
+    // Lanes of equal `sub` hold the same columns: joined over the warp, then
+    // warp by warp.
+#pragma unroll
+    for (int i = 0; i < 2 * V; ++i)
+      for (int o = lanes; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(0xFFFFFFFFu, acc[i], o);
+    __syncthreads();
+    const int warp = threadIdx.x >> 5;
+    if ((threadIdx.x & 31) < lanes && on) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        sums[warp * a.D + sub * V + i] = acc[i];
+        sums[warp * a.D + half + sub * V + i] = acc[V + i];
+      }
+    }
+    __syncthreads();
+    for (int d = threadIdx.x; d < a.D; d += kThreads) {
+      float v = 0.0f;
+      for (int i = 0; i < kThreads / 32; ++i) v += sums[i * a.D + d];
+      a.partial[(static_cast<long long>(blockIdx.x) * 2 + side) * a.D + d] = v;
+    }
+  }
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) last = atomicAdd(a.done, 1u) == gridDim.x - 1;
+  __syncthreads();
+  if (last) {
+    __threadfence();
+    // kThreads / 64 slices of the blocks for each of 64 columns, joined in order.
+    const int cols = a.hk ? 2 * a.D : a.D;
+    const int slice = threadIdx.x >> 6, slices = kThreads / 64;
+    for (int c0 = 0; c0 < cols; c0 += 64) {
+      const int c = c0 + (threadIdx.x & 63);
+      float v = 0.0f;
+      if (c < cols) {
+#pragma unroll 8
+        for (int b = slice; b < static_cast<int>(gridDim.x); b += slices)
+          v += __ldcg(a.partial + static_cast<long long>(b) * 2 * a.D + c);
+      }
+      __syncthreads();
+      sums[threadIdx.x] = v;
+      __syncthreads();
+      if (threadIdx.x < 64 && c < cols) {
+        for (int i = 1; i < slices; ++i) v += sums[i * 64 + threadIdx.x];
+        if (c < a.D)
+          a.dwq[c] = v;
+        else
+          a.dwk[c - a.D] = v;
+      }
+    }
+    if (threadIdx.x == 0) *a.done = 0;
+  }
+  allow_next_grid();
+}
+
+// ------------------------------------------------------------ host side
+
+View view_of(const pv_heads* h, int elem) {
+  View v{};
+  if (h) v = View{static_cast<char*>(h->data), h->row_stride * elem, h->head_stride * elem};
+  return v;
+}
+
+int check_params(const pv_rope_params* p, int* dev) {
+  if (!p) return PV_ERR_INVALID;
+  if (!dtype_size(p->dtype) || p->rows < 0 || p->rows >= (int64_t(1) << 31)) return PV_ERR_INVALID;
+  if (p->q_heads < 1 || p->k_heads < 0 || p->q_heads > 4096 || p->k_heads > 4096) return PV_ERR_INVALID;
+  if (p->head_dim < 16 || p->head_dim > 256 || p->head_dim % 16) return PV_ERR_INVALID;
+  if (p->axes < 1 || p->axes > 3 || p->position_stride < p->axes) return PV_ERR_INVALID;
+  if (!(p->eps >= 0.0f) || !std::isfinite(p->eps)) return PV_ERR_INVALID;
+  if (!p->q_weight || !p->inv_freq || (p->k_heads && !p->k_weight) || (p->rows && !p->positions))
+    return PV_ERR_INVALID;
+  if (!aligned(p->q_weight, 4) || !aligned(p->k_weight, 4) || !aligned(p->inv_freq, 4) || !aligned(p->positions, 4))
+    return PV_ERR_INVALID;
+  *dev = device_of(p->q_weight);
+  if (*dev < 0 || device_of(p->inv_freq) != *dev || (p->k_heads && device_of(p->k_weight) != *dev) ||
+      (p->rows && device_of(p->positions) != *dev))
+    return PV_ERR_INVALID;
+  return PV_OK;
+}
+
+RopeArgs args_of(const pv_rope_params* p) {
+  RopeArgs a{};
+  a.wq = p->q_weight;
+  a.wk = p->k_weight;
+  a.pos = p->positions;
+  a.pos_stride = p->position_stride;
+  a.freq = p->inv_freq;
+  a.rows = static_cast<int>(p->rows);
+  a.hq = p->q_heads;
+  a.hk = p->k_heads;
+  a.D = p->head_dim;
+  a.axes = p->axes;
+  a.eps = p->eps;
+  const int per = 16 / dtype_size(p->dtype);
+  while ((per << a.lanes_log2) < a.D / 2) ++a.lanes_log2;
+  return a;
+}
+
+// Tokens of a tile: about 8 rows for each group of lanes, as many as the table
+// holds, and few enough that the tiles spread over `blocks` blocks.
+int tile_tokens(const RopeArgs& a, int blocks) {
+  const int groups = kThreads >> a.lanes_log2;
+  long long t = (8LL * groups + a.hq + a.hk - 1) / (a.hq + a.hk);
+  t = std::min<long long>(t, kTableFloats / a.D);
+  t = std::min<long long>(t, (a.rows + blocks - 1LL) / blocks);
+  return static_cast<int>(std::max<long long>(t, 1));
+}
+
+template <typename K>
+int launch(K kernel, int blocks, const RopeArgs& a, pv_stream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) {
+    cudaGetLastError();
+    return PV_ERR_CUDA;
+  }
+  return PV_OK;
+}
+
+}  // namespace
+
+extern "C" int pv_qk_norm_rope(const pv_rope_params* params, const pv_heads* q, const pv_heads* k,
+                               const pv_heads* out_q, const pv_heads* out_k, pv_stream_t stream) {
+  int dev = 0, st = check_params(params, &dev);
+  if (st != PV_OK) return st;
+  const int elem = dtype_size(params->dtype);
+  if ((st = check_heads(q, params->rows, params->q_heads, elem, dev)) != PV_OK ||
+      (st = check_heads(out_q, params->rows, params->q_heads, elem, dev)) != PV_OK)
+    return st;
+  if (params->k_heads && ((st = check_heads(k, params->rows, params->k_heads, elem, dev)) != PV_OK ||
+                          (st = check_heads(out_k, params->rows, params->k_heads, elem, dev)) != PV_OK))
+    return st;
+  if (params->rows == 0) return PV_OK;
+  DeviceScope scope(dev);
+  const int sms = sm_count(dev);
+  if (!scope.ok() || sms < 1) return PV_ERR_CUDA;
+  RopeArgs a = args_of(params);
+  a.q = view_of(q, elem);
+  a.k = view_of(k, elem);
+  a.oq = view_of(out_q, elem);
+  a.ok = view_of(out_k, elem);
+  a.tile = tile_tokens(a, 8 * sms);
+  const int blocks = (a.rows + a.tile - 1) / a.tile;
+  switch (params->dtype) {
+    case PV_F32: return launch(pv_rope_kernel<float>, blocks, a, stream);
+    case PV_BF16: return launch(pv_rope_kernel<__nv_bfloat16>, blocks, a, stream);
+    default: return launch(pv_rope_kernel<__half>, blocks, a, stream);
+  }
+}
+
+extern "C" int pv_qk_norm_rope_backward(const pv_rope_params* params, const pv_heads* dout_q, const pv_heads* dout_k,
+                                        const pv_heads* q, const pv_heads* k, const pv_heads* dq, const pv_heads* dk,
+                                        float* dq_weight, float* dk_weight, pv_stream_t stream) {
+  int dev = 0, st = check_params(params, &dev);
+  if (st != PV_OK) return st;
+  const int elem = dtype_size(params->dtype);
+  for (const pv_heads* h : {dout_q, q, dq})
+    if ((st = check_heads(h, params->rows, params->q_heads, elem, dev)) != PV_OK) return st;
+  if (params->k_heads)
+    for (const pv_heads* h : {dout_k, k, dk})
+      if ((st = check_heads(h, params->rows, params->k_heads, elem, dev)) != PV_OK) return st;
+  if (!dq_weight || !aligned(dq_weight, 4) || device_of(dq_weight) != dev) return PV_ERR_INVALID;
+  if (params->k_heads && (!dk_weight || !aligned(dk_weight, 4) || device_of(dk_weight) != dev)) return PV_ERR_INVALID;
+  DeviceScope scope(dev);
+  const int sms = sm_count(dev);
+  if (!scope.ok() || sms < 1) return PV_ERR_CUDA;
+  RopeArgs a = args_of(params);
+  a.q = view_of(q, elem);
+  a.k = view_of(k, elem);
+  a.gq = view_of(dout_q, elem);
+  a.gk = view_of(dout_k, elem);
+  a.oq = view_of(dq, elem);
+  a.ok = view_of(dk, elem);
+  a.dwq = dq_weight;
+  a.dwk = dk_weight;
+  const int most = std::min(kMaxBlocks, 4 * sms);
+  a.tile = tile_tokens(a, most);
+  const int tiles = (a.rows + a.tile - 1) / a.tile;
+  const int blocks = std::max(1, std::min(most, tiles));
+  Scratch scratch;
+  if ((st = scratch.open(dev, stream, kPlain, sizeof(float) * 2 * a.D * static_cast<size_t>(blocks))) != PV_OK)
+    return st;
+  a.partial = static_cast<float*>(scratch.body());
+  a.done = static_cast<unsigned int*>(scratch.head());
+  switch (params->dtype) {
+    case PV_F32: return launch(pv_rope_backward_kernel<float>, blocks, a, stream);
+    case PV_BF16: return launch(pv_rope_backward_kernel<__nv_bfloat16>, blocks, a, stream);
+    default: return launch(pv_rope_backward_kernel<__half>, blocks, a, stream);
+  }
+}

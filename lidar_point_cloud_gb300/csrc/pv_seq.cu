@@ -1,0 +1,114 @@
+// Host side shared by the voxel-token operators: argument checks and their
+// per-(device, stream) scratch (see pv_seq.cuh).
+
+#include "pv_seq.cuh"
+
+#include <map>
+#include <new>
+#include <tuple>
+
+namespace pvs {
+
+struct SeqSpace {
+  std::mutex mu;
+  int device = 0;
+  unsigned char* mem = nullptr;
+  size_t cap = 0;
+};
+
+namespace {
+std::mutex g_seq_mu;
+std::map<std::tuple<int, pv_stream_t, int>, SeqSpace*> g_seq;
+std::mutex g_sms_mu;
+int g_sms[64];
+}  // namespace
+
+int device_of(const void* ptr) {
+  cudaPointerAttributes at;
+  if (cudaPointerGetAttributes(&at, ptr) != cudaSuccess) {
+    cudaGetLastError();
+    return -1;
+  }
+  return at.type == cudaMemoryTypeDevice || at.type == cudaMemoryTypeManaged ? at.device : -1;
+}
+
+int sm_count(int dev) {
+  if (dev < 0 || dev >= 64) return 0;
+  std::lock_guard<std::mutex> lk(g_sms_mu);
+  if (!g_sms[dev] && cudaDeviceGetAttribute(&g_sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    g_sms[dev] = 0;
+  }
+  return g_sms[dev];
+}
+
+int check_offsets(const int64_t* off, int n) {
+  if (!off || n < 1 || n > PV_MAX_FRAMES || off[0] != 0) return PV_ERR_INVALID;
+  for (int i = 0; i < n; ++i)
+    if (off[i + 1] < off[i]) return PV_ERR_INVALID;
+  return off[n] < (int64_t(1) << 31) ? PV_OK : PV_ERR_INVALID;
+}
+
+int check_heads(const pv_heads* h, int64_t rows, int heads, int elem, int dev) {
+  if (!h) return PV_ERR_INVALID;
+  if (rows == 0 || heads == 0) return PV_OK;
+  if (!h->data || !aligned(h->data, 16) || h->row_stride < 0 || h->head_stride < 0) return PV_ERR_INVALID;
+  if (h->row_stride * elem % 16 || h->head_stride * elem % 16) return PV_ERR_INVALID;
+  return device_of(h->data) == dev ? PV_OK : PV_ERR_INVALID;
+}
+
+int Scratch::open(int dev, pv_stream_t stream, ScratchKind kind, size_t bytes) {
+  {
+    std::lock_guard<std::mutex> lk(g_seq_mu);
+    SeqSpace*& sp = g_seq[std::make_tuple(dev, stream, static_cast<int>(kind))];
+    if (!sp) sp = new (std::nothrow) SeqSpace();
+    if (!sp) return PV_ERR_ALLOC;
+    sp->device = dev;
+    sp->mu.lock();
+    sp_ = sp;
+  }
+  const size_t need = round_up(kHead + bytes, size_t(1) << 16);
+  if (sp_->cap >= need) return PV_OK;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (sp_->mem && cudaStreamSynchronize(s) != cudaSuccess) return PV_ERR_CUDA;
+  if (sp_->mem) cudaFree(sp_->mem);
+  sp_->mem = nullptr;
+  sp_->cap = 0;
+  void* mem = nullptr;
+  if (cudaMalloc(&mem, need) != cudaSuccess) {
+    cudaGetLastError();
+    return PV_ERR_ALLOC;
+  }
+  if (cudaMemsetAsync(mem, 0, need, s) != cudaSuccess) {
+    cudaGetLastError();
+    cudaFree(mem);
+    return PV_ERR_CUDA;
+  }
+  sp_->mem = static_cast<unsigned char*>(mem);
+  sp_->cap = need;
+  return PV_OK;
+}
+
+Scratch::~Scratch() {
+  if (sp_) sp_->mu.unlock();
+}
+
+void* Scratch::head() const { return sp_->mem; }
+
+int release_scratch() {
+  std::lock_guard<std::mutex> lk(g_seq_mu);
+  int st = PV_OK;
+  for (auto& kv : g_seq) {
+    SeqSpace* sp = kv.second;
+    DeviceScope scope(sp->device);
+    if (!scope.ok() || cudaDeviceSynchronize() != cudaSuccess) st = PV_ERR_CUDA;
+    sp->mu.lock();  // wait for a call that is still enqueueing
+    sp->mu.unlock();
+    cudaFree(sp->mem);
+    delete sp;
+  }
+  g_seq.clear();
+  return st;
+}
+
+}  // namespace pvs
