@@ -11,7 +11,10 @@
 
 #include "pv_attn.cuh"
 
+#include <cudaTypedefs.h>
+
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <initializer_list>
 
@@ -57,63 +60,6 @@ __device__ __forceinline__ float dot_of(const float* a, const float* b, int D) {
   float s = 0.0f;
   for (int d = 0; d < D; ++d) s = fmaf(a[d], b[d], s);
   return s;
-}
-
-__device__ __forceinline__ float row_sum(float v) {  // the 8 threads of a row
-  for (int o = 4; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  return v;
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kThreads) pv_attn_kernel(const __grid_constant__ AttnArgs a) {
-  __shared__ float qs[kOwn][kPad], ks[kOther][kPad], vs[kOther][kPad], ps[kOwn][kOther + 1];
-  wait_prior_grid();
-  const int f = frame_of(a.tile0, a.frames, blockIdx.x), h = blockIdx.y, g = h / a.G;
-  const int nq = a.q0[f + 1] - a.q0[f], nk = a.k0[f + 1] - a.k0[f];
-  const int i0 = (blockIdx.x - a.tile0[f]) * kOwn;
-  const int r = threadIdx.x >> 3, c = threadIdx.x & 7, i = i0 + r, qrow = a.q0[f] + i;
-  load_rows<T>(a.q, h, a.q0[f] + i0, nq - i0, kOwn, a.D, qs);
-  float top = -INFINITY, sum = 0.0f, acc[16];
-  for (int d = 0; d < 16; ++d) acc[d] = 0.0f;
-  const float slope = a.slopes ? a.slopes[h] : 0.0f;
-  for (int j0 = 0; j0 < nk; j0 += kOther) {
-    __syncthreads();
-    load_rows<T>(a.k, g, a.k0[f] + j0, nk - j0, kOther, a.D, ks);
-    load_rows<T>(a.v, g, a.k0[f] + j0, nk - j0, kOther, a.D, vs);
-    __syncthreads();
-    float s[4], most = top, grad;
-    for (int x = 0; x < 4; ++x) {
-      const int j = j0 + c + 8 * x;
-      s[x] = -INFINITY;
-      if (visible(a, f, i, j, nq, nk))
-        s[x] = score(a, dot_of(qs[r], ks[c + 8 * x], a.D), slope, a.qpos + qrow * a.qpos_stride,
-                     a.kpos + (a.k0[f] + j) * a.kpos_stride, &grad);
-      most = fmaxf(most, s[x]);
-    }
-    for (int o = 4; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
-    const float base = most == -INFINITY ? 0.0f : most;
-    const float old = expf(top - base);
-    float part = 0.0f;
-    for (int x = 0; x < 4; ++x) {
-      const float p = expf(s[x] - base);
-      part += p;
-      ps[r][c + 8 * x] = p;
-    }
-    sum = fmaf(sum, old, row_sum(part));
-    top = most;
-    __syncwarp();
-    for (int d = 0; d < 16; ++d) acc[d] *= old;
-    for (int j = 0; j < kOther; ++j)
-      for (int d = 0; d < 16; ++d)
-        if (c + 8 * d < a.D) acc[d] = fmaf(ps[r][j], vs[j][c + 8 * d], acc[d]);
-  }
-  if (i < nq) {
-    T* o = reinterpret_cast<T*>(a.o.data + qrow * a.o.row + h * a.o.head);
-    for (int d = 0; d < 16; ++d)
-      if (c + 8 * d < a.D) o[c + 8 * d] = Pack<T>::one(sum > 0.0f ? acc[d] / sum : 0.0f);
-    if (a.lse && c == 0) a.lse[static_cast<long long>(h) * a.queries + qrow] = sum > 0.0f ? top + logf(sum) : -INFINITY;
-  }
-  allow_next_grid();
 }
 
 template <typename T>
@@ -278,6 +224,7 @@ AttnArgs args_of(const pv_attention_params* p) {
   a.Hk = p->k_heads;
   a.G = p->q_heads / p->k_heads;
   a.D = p->head_dim;
+  a.Dn = (a.D + 15) / 16 * 16;
   a.frames = p->frames;
   a.queries = static_cast<int>(p->q_offsets[p->frames]);
   a.keys = static_cast<int>(p->k_offsets[p->frames]);
@@ -287,6 +234,44 @@ AttnArgs args_of(const pv_attention_params* p) {
     a.prefix[b] = p->prefix ? static_cast<int>(std::min<int64_t>(p->prefix[b], a.k0[b + 1] - a.k0[b])) : 0;
   }
   return a;
+}
+
+// Heads that share a tile of rows: the largest power of two of those that share
+// a key head.
+int pack_of(int G) {
+  int p = 0;
+  while (p < 7 && G % (2 << p) == 0) ++p;
+  return p;
+}
+
+// How many key tiles a block takes.  A block's time goes by its key tiles, and
+// the blocks run in rounds of one a multiprocessor: of the counts that leave
+// some `kLeast` tiles a block, the one with the shortest rounds, where a join
+// and its second launch are worth `kJoin` tiles.
+int chunk_of(const AttnArgs& a, int heads, int sms) {
+  constexpr int kLeast = 2, kJoin = 4;
+  int most = 1;
+  for (int f = 0; f < a.frames; ++f) most = std::max(most, (a.k0[f + 1] - a.k0[f] + 127) / 128);
+  auto cost = [&](int chunk) {
+    int64_t blocks = 0;
+    for (int f = 0; f < a.frames; ++f) {
+      const int64_t rows = static_cast<int64_t>(a.q0[f + 1] - a.q0[f]) << a.pack_log2;
+      const int tiles = (a.k0[f + 1] - a.k0[f] + 127) / 128;
+      blocks += (rows + 255) / 256 * std::max(1, (tiles + chunk - 1) / chunk);
+    }
+    return (blocks * heads + sms - 1) / sms * (chunk + 1) + (chunk < most ? kJoin : 0);
+  };
+  int best = most;
+  int64_t least = cost(most);
+  for (int parts = 2; parts <= 64 && (most + parts - 1) / parts >= kLeast; ++parts) {
+    const int chunk = (most + parts - 1) / parts;
+    const int64_t c = cost(chunk);
+    if (c < least) {
+      least = c;
+      best = chunk;
+    }
+  }
+  return best;
 }
 
 // Tiles of `own` rows along frames with row offsets `off`; how many there are.
@@ -334,6 +319,33 @@ int backward(AttnArgs& a, pv_stream_t stream) {
 
 }  // namespace
 
+int pvs::make_map(CUtensorMap* map, const View& v, int dtype, int D, int heads, int pack, int64_t total, int rows) {
+  static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> encode{nullptr};
+  auto fn = encode.load();
+  if (!fn) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult got;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &got) != cudaSuccess ||
+        got != cudaDriverEntryPointSuccess || !p) {
+      cudaGetLastError();
+      return PV_ERR_CUDA;
+    }
+    fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    encode.store(fn);
+  }
+  // A head stride of zero is one head that every head reads.
+  const cuuint64_t head = v.head ? v.head : 16;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(v.head ? pack : 1),
+                              static_cast<cuuint64_t>(v.head ? heads / pack : 1), static_cast<cuuint64_t>(total)};
+  const cuuint64_t strides[3] = {head, head * pack, static_cast<cuuint64_t>(v.row ? v.row : 16)};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(pack), 1, static_cast<cuuint32_t>(rows)};
+  const cuuint32_t step[4] = {1, 1, 1, 1};
+  const CUresult r = fn(map, dtype == PV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, v.data,
+                        dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? PV_OK : PV_ERR_INVALID;
+}
+
 extern "C" int pv_attention(const pv_attention_params* params, const pv_heads* q, const pv_heads* k, const pv_heads* v,
                             const pv_heads* out, float* lse, pv_stream_t stream) {
   if (!params || !params->q_offsets || !out || !q) return PV_ERR_INVALID;
@@ -357,9 +369,34 @@ extern "C" int pv_attention(const pv_attention_params* params, const pv_heads* q
   a.v = view_of(v);
   a.o = view_of(out);
   a.lse = lse;
-  const int n = tiles_of(a, a.q0, kOwn);
-  if (params->dtype == PV_BF16) return launch(pv_attn_kernel<__nv_bfloat16>, dim3(n, a.H), 0, a, stream);
-  return launch(pv_attn_kernel<__half>, dim3(n, a.H), 0, a, stream);
+  a.pack_log2 = a.q.head ? pack_of(a.G) : 0;
+  const int heads = a.H >> a.pack_log2;
+  const int sms = sm_count(dev);
+  if (sms < 1) return PV_ERR_CUDA;
+  a.chunk = chunk_of(a, heads, sms);
+  int parts = 1;
+  for (int f = 0; f < a.frames; ++f) {
+    const int rows = static_cast<int>(((static_cast<int64_t>(a.q0[f + 1] - a.q0[f]) << a.pack_log2) + 255) / 256);
+    const int splits = std::max(1, ((a.k0[f + 1] - a.k0[f] + 127) / 128 + a.chunk - 1) / a.chunk);
+    a.tile0[f + 1] = a.tile0[f] + rows * splits;
+    parts = std::max(parts, splits);
+  }
+  Scratch scratch;
+  if (parts > 1) {
+    const size_t rows = static_cast<size_t>(parts) * nq * a.H;
+    if ((st = scratch.open(dev, stream, kPlain, rows * (sizeof(float) * a.D + sizeof(float2)))) != PV_OK) return st;
+    a.part_o = static_cast<float*>(scratch.body());
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + rows * a.D);
+  }
+  AttnMaps m;
+  if ((st = make_map(&m.q, a.q, params->dtype, a.D, a.H, 1 << a.pack_log2, nq, 128 >> a.pack_log2)) != PV_OK) return st;
+  if (nk == 0) {
+    m.k = m.v = m.q;  // no key is loaded
+  } else if ((st = make_map(&m.k, a.k, params->dtype, a.D, a.Hk, 1, nk, 128)) != PV_OK ||
+             (st = make_map(&m.v, a.v, params->dtype, a.D, a.Hk, 1, nk, 128)) != PV_OK) {
+    return st;
+  }
+  return attn_forward(a, params->dtype, m, dim3(a.tile0[a.frames], heads), reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" int pv_attention_backward(const pv_attention_params* params, const pv_heads* dout, const pv_heads* q,

@@ -4,6 +4,8 @@
 
 #include "pv_seq.cuh"
 
+#include <cuda.h>
+
 namespace pvs {
 
 struct View {
@@ -21,11 +23,46 @@ struct AttnArgs {
   long long qpos_stride, kpos_stride;
   float scale, cap;
   int axes, causal, H, Hk, G, D, frames, queries, keys;
+  int Dn;          // D rounded up to 16
+  int pack_log2;   // heads of a key head that share a tile of rows (log2)
+  int chunk;       // key tiles of a block: fewer than there are if the keys are split
+  float* part_o;   // split keys: [split, queries, H, D] unnormalised outputs, or null
+  float2* part_ml; // split keys: [split, queries, H] maximum (in units of log2) and sum
   int q0[PV_MAX_FRAMES + 1];    // row offsets of the frames
   int k0[PV_MAX_FRAMES + 1];
   int tile0[PV_MAX_FRAMES + 1]; // first tile of each frame
   int prefix[PV_MAX_FRAMES];
 };
+
+struct AttnMaps {
+  CUtensorMap q, k, v, dout;
+};
+
+// Tensor map of rows of heads for tiles of `rows` rows of `pack` heads of 64
+// elements: dimensions (D, pack, heads / pack, rows), elements past D read as 0.
+int make_map(CUtensorMap* map, const View& v, int dtype, int D, int heads, int pack, int64_t total, int rows);
+
+// Kernel launches of pv_attn_fwd.cu and pv_attn_bwd.cu.
+int attn_forward(AttnArgs& a, int dtype, const AttnMaps& m, dim3 grid, cudaStream_t s);
+
+template <typename K, typename... A>
+int launch_pdl(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
+    cudaGetLastError();
+    return PV_ERR_CUDA;
+  }
+  return PV_OK;
+}
 
 // The frame that tile t belongs to: the last one whose first tile is not past t.
 __device__ __forceinline__ int frame_of(const int* tile0, int frames, int t) {

@@ -1,0 +1,450 @@
+// Attention inside frames, forward, on the tensor cores.
+//
+// A block takes two tiles of 128 query rows and walks the frame's keys in
+// tiles of 128.  Warps 0-3 and 4-7 own a query tile each, one row a thread: they
+// read the scores from tensor memory, keep the row's running maximum and sum,
+// and write the probabilities back over the scores as the next product's
+// operand.  Warp 8 issues the products, warp 9 the TMA loads of keys and values
+// into a ring of shared-memory slots, warp 10 puts key positions there.  While
+// one tile's scores go through the exponential, the other tile's products run.
+//
+// Rows are (query, head) pairs of the heads that share a key head (the largest
+// power of two of them), so that one query of many heads fills a tile as far as
+// it can, and its keys are read once for all of them.
+//
+// With few rows the keys are split over blocks: each leaves its unnormalised
+// output, maximum and sum, and a second kernel joins them in order.
+//
+// The running maximum moves only when a row's scores rise by more than 2^8 over
+// it: sums and outputs then stay below 2^8 times what they would be, well
+// inside 32 bits (and probabilities inside float16), and the output in tensor
+// memory is rescaled a few times per row instead of at every tile.
+// Probabilities are rounded to the storage type for the second product, as the
+// tensor cores take it; their sum is taken before rounding, in 32 bits.
+
+#include "pv_attn.cuh"
+#include "pv_tc.cuh"
+
+#include <type_traits>
+
+namespace pvs {
+
+namespace {
+
+constexpr int kThreads = 384;
+// Registers of a thread: 168 at launch (384 x 168 = 64,512 of a multiprocessor's
+// 65,536); the softmax warpgroups take what the other one gives back: 256 x 208 +
+// 128 x 80 = 63,488.
+constexpr int kRegsSoftmax = 208, kRegsOther = 80;
+constexpr int kRows = 128;      // rows of a query tile, keys of a key tile
+constexpr int kPosSlots = 2;
+constexpr float kLazy = 8.0f;   // log2 of how far scores may rise over the kept maximum
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+template <int kBlocks>  // 64-element blocks of a head: 1 or 2
+struct Smem {
+  static constexpr int kTile = kRows * 128 * kBlocks;  // bytes of 128 rows of a head
+  static constexpr int kSlots = kBlocks == 1 ? 8 : 4;
+  alignas(1024) unsigned char q[2][kTile];
+  alignas(1024) unsigned char kv[kSlots][kTile];
+  float pos[kPosSlots][3][kRows];
+  uint64_t q_full, kv_full[kSlots], kv_empty[kSlots], s_full[2], p_full[2], o_full[2], pos_full[kPosSlots], pos_empty[kPosSlots];
+  uint32_t tmem;
+  int given_up;
+};
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  return Pack<T>::two(a, b);
+}
+
+template <typename T, int kBlocks>
+__global__ void __launch_bounds__(kThreads, 1)
+    pv_attn_fwd_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap mq,
+                       const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+  using S = Smem<kBlocks>;
+  constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  extern __shared__ __align__(1024) unsigned char raw[];
+  S& sm = *reinterpret_cast<S*>(raw + ((1024 - (smem_addr(raw) & 1023)) & 1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // ---- which rows, which keys
+  const int f = frame_of(a.tile0, a.frames, blockIdx.x);
+  const int nq = a.q0[f + 1] - a.q0[f], nk = a.k0[f + 1] - a.k0[f];
+  const int pack = 1 << a.pack_log2;
+  const int mblocks = (((nq << a.pack_log2) + 2 * kRows - 1) / (2 * kRows));
+  const int local = blockIdx.x - a.tile0[f];
+  // Later rows see more keys under a causal mask: they go first.
+  const int mb = mblocks - 1 - local % mblocks, split = local / mblocks;
+  const int hb = blockIdx.y;  // block of `pack` heads
+  const int kh = (hb << a.pack_log2) / a.G;
+  // Keys that query i sees: all below this.
+  auto limit = [&](int i) { return a.causal ? max(min(max(i + nk - nq + 1, a.prefix[f]), nk), 0) : nk; };
+  const int js = split * a.chunk;
+  int first[2], last_j[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    first[t] = (mb * 2 + t) * (kRows >> a.pack_log2);  // its first query
+    const int end = min(first[t] + (kRows >> a.pack_log2), nq);
+    const int tiles = first[t] < nq ? (limit(end - 1) + kRows - 1) / kRows : 0;
+    last_j[t] = max(min(tiles, js + a.chunk), js);
+  }
+  const int je = max(last_j[0], last_j[1]);
+
+  // ---- set up
+  if (threadIdx.x == 0) {
+    sm.given_up = 0;
+    bar_init(&sm.q_full, 1);
+    for (int i = 0; i < S::kSlots; ++i) bar_init(&sm.kv_full[i], 1), bar_init(&sm.kv_empty[i], 1);
+    for (int t = 0; t < 2; ++t) bar_init(&sm.s_full[t], 1), bar_init(&sm.p_full[t], kRows), bar_init(&sm.o_full[t], 1);
+    for (int i = 0; i < kPosSlots; ++i) bar_init(&sm.pos_full[i], 32), bar_init(&sm.pos_empty[i], 2 * kRows);
+    fence_bar_init();
+    tma_prefetch(&mq);
+    tma_prefetch(&mk);
+    tma_prefetch(&mv);
+  }
+  if (warp == 8) tmem_alloc<512>(&sm.tmem);
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tm = sm.tmem;
+  volatile int* given_up = &sm.given_up;
+  const int heads_k = a.k.head ? kh : 0, heads_v = a.v.head ? kh : 0;
+  wait_prior_grid();
+
+  if (warp >= 8) regs_down<kRegsOther>();
+  if (warp == 9) {
+    // ---- loads
+    if (lane == 0 && je > js) {
+      const bool two = last_j[1] > js;
+      bar_expect(&sm.q_full, (two ? 2 : 1) * S::kTile);
+      for (int t = 0; t < (two ? 2 : 1); ++t)
+        for (int b = 0; b < kBlocks; ++b)
+          tma_load4(sm.q[t] + b * kRows * 128, &mq, b * 64, 0, a.q.head ? hb : 0, a.q0[f] + first[t], &sm.q_full);
+      for (int n = 0; n < 2 * (je - js); ++n) {
+        const int slot = n % S::kSlots;
+        if (!bar_wait(&sm.kv_empty[slot], ((n / S::kSlots) & 1) ^ 1, given_up)) break;
+        bar_expect(&sm.kv_full[slot], S::kTile);
+        const CUtensorMap* m = n & 1 ? &mv : &mk;
+        for (int b = 0; b < kBlocks; ++b)
+          tma_load4(sm.kv[slot] + b * kRows * 128, m, b * 64, 0, n & 1 ? heads_v : heads_k,
+                    a.k0[f] + (js + (n >> 1)) * kRows, &sm.kv_full[slot]);
+      }
+    }
+  } else if (warp == 8) {
+    // ---- products
+    const uint32_t word_s = mma_word(kBf16, 128, 128, false, false);
+    const uint32_t word_o = mma_word(kBf16, 128, 0, false, true) | (static_cast<uint32_t>(a.Dn >> 3) << 17);
+    const int ksteps = (a.D + 15) / 16;
+    bool ok = je > js && warp_wait(&sm.q_full, 0, given_up);
+    auto scores = [&](int t, int n) {  // S_t = Q_t K^T
+      if (lane == 0) {
+        const uint32_t q = smem_addr(sm.q[t]), k = smem_addr(sm.kv[n % S::kSlots]);
+        for (int x = 0; x < ksteps; ++x) {
+          const uint32_t off = (x >> 2) * kRows * 128 + (x & 3) * 32;
+          mma_ss(tm + t * 128, operand(q + off, 16), operand(k + off, 16), word_s, x > 0);
+        }
+        mma_commit(&sm.s_full[t]);
+      }
+      __syncwarp();
+    };
+    auto full = [&](int n) { return warp_wait(&sm.kv_full[n % S::kSlots], (n / S::kSlots) & 1, given_up); };
+    if (ok) ok = full(0);
+    if (ok) {
+      tc_after();
+      for (int t = 0; t < 2; ++t)
+        if (last_j[t] > js) scores(t, 0);
+      if (lane == 0) mma_commit(&sm.kv_empty[0]);
+    }
+    for (int j = js; ok && j < je; ++j) {
+      const int nv = 2 * (j - js) + 1, nk1 = nv + 1;
+      if (!(ok = full(nv))) break;
+      if ((j + 1) * kRows > nk) {
+        // Rows past the frame's end are another frame's: whatever they hold must
+        // not meet the zero probabilities of these places.
+        const int have = nk - j * kRows;
+        uint4* v = reinterpret_cast<uint4*>(sm.kv[nv % S::kSlots]);
+        for (int b = 0; b < kBlocks; ++b)
+          for (int i = have * 8 + lane; i < kRows * 8; i += 32) v[b * kRows * 8 + i] = make_uint4(0, 0, 0, 0);
+        fence_to_async();
+        __syncwarp();
+      }
+      if (j + 1 < je && !(ok = full(nk1))) break;
+      for (int t = 0; t < 2; ++t) {
+        if (j >= last_j[t]) continue;
+        if (!(ok = warp_wait(&sm.p_full[t], (j - js) & 1, given_up))) break;
+        tc_after();
+        if (lane == 0) {
+          const uint32_t v = smem_addr(sm.kv[nv % S::kSlots]);
+          for (int x = 0; x < kRows / 16; ++x)
+            mma_ts(tm + 256 + t * 64 * kBlocks, tm + t * 128 + x * 8, operand(v + x * 2048, kRows * 128), word_o,
+                   j > js || x > 0);
+        }
+        __syncwarp();
+        if (j + 1 < last_j[t])
+          scores(t, nk1);
+        else if (lane == 0)
+          mma_commit(&sm.o_full[t]);
+      }
+      if (ok && lane == 0) {
+        mma_commit(&sm.kv_empty[nv % S::kSlots]);
+        if (j + 1 < je) mma_commit(&sm.kv_empty[nk1 % S::kSlots]);
+      }
+      __syncwarp();
+    }
+  } else if (warp == 10) {
+    // ---- key positions
+    if (a.slopes) {
+      for (int j = js; j < je; ++j) {
+        const int n = j - js, slot = n % kPosSlots;
+        if (!warp_wait(&sm.pos_empty[slot], ((n / kPosSlots) & 1) ^ 1, given_up)) break;
+        for (int x = lane; x < kRows; x += 32) {
+          const int key = j * kRows + x;
+          for (int c = 0; c < a.axes; ++c)
+            sm.pos[slot][c][x] =
+                key < nk ? static_cast<float>(a.kpos[static_cast<long long>(a.k0[f] + key) * a.kpos_stride + c]) : 0.0f;
+        }
+        bar_arrive(&sm.pos_full[slot]);
+      }
+    }
+  } else if (warp < 8) {
+    // ---- softmax: one row a thread
+    regs_up<kRegsSoftmax>();
+    const int t = warp >> 2, r = threadIdx.x & (kRows - 1);
+    const int i = first[t] + (r >> a.pack_log2);
+    const int h = (hb << a.pack_log2) + (r & (pack - 1));
+    const bool live = i < nq;
+    const int lim = live ? limit(i) : nk;
+    const int clear = first[t] < nq ? limit(first[t]) : nk;  // tiles that end at or below this are seen whole
+    const uint32_t mine = tm + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t sc = mine + t * 128, oc = mine + 256 + t * 64 * kBlocks;
+    const long long qrow = a.q0[f] + i;
+    float slope = 0.0f, qp[3] = {0.0f, 0.0f, 0.0f};
+    if (a.slopes && live) {
+      slope = -a.slopes[h] * kLog2e;
+      for (int c = 0; c < a.axes; ++c) qp[c] = -static_cast<float>(a.qpos[qrow * a.qpos_stride + c]);
+    }
+    // Scores in units of log2: raw scores times `unit`, or final ones if a cap or
+    // a distance has been worked in.
+    const float unit = a.scale * kLog2e;
+    const float mul = a.slopes || a.cap > 0.0f ? 1.0f : unit;
+    const float cap_in = a.cap > 0.0f ? 2.0f * unit / a.cap : 0.0f, cap_out = a.cap * kLog2e;
+    float top = -INFINITY, sum = 0.0f;
+    bool ok = true;
+    for (int j = js; j < last_j[t]; ++j) {
+      const int n = j - js;
+      if (!(ok = warp_wait(&sm.s_full[t], n & 1, given_up))) break;
+      tc_after();
+      float u[kRows];
+      uint32_t* ur = reinterpret_cast<uint32_t*>(u);
+#pragma unroll
+      for (int x = 0; x < kRows; x += 32) tmem_ld32(sc + x, ur + x);
+      tc_wait_ld<kRows>(ur);
+      if (a.cap > 0.0f) {
+        // cap tanh(s / cap) = cap (1 - 2 / (1 + exp(2 s / cap)))
+#pragma unroll
+        for (int x = 0; x < kRows; ++x)
+          u[x] = fmaf(-2.0f * cap_out, rcp_fast(1.0f + exp2_fast(u[x] * cap_in)), cap_out);
+      }
+      if (a.slopes) {
+        const float by = a.cap > 0.0f ? 1.0f : unit;
+        if (!(ok = warp_wait(&sm.pos_full[n % kPosSlots], (n / kPosSlots) & 1, given_up))) break;
+#pragma unroll
+        for (int x = 0; x < kRows; x += 8) {
+          float d[8];
+          for (int c = 0; c < a.axes; ++c) {
+            const float4* p = reinterpret_cast<const float4*>(&sm.pos[n % kPosSlots][c][x]);
+            const float4 v0 = p[0], v1 = p[1];
+            float e[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+#pragma unroll
+            for (int y = 0; y < 8; y += 2) add2(e[y], e[y + 1], e[y], e[y + 1], qp[c], qp[c]);
+#pragma unroll
+            for (int y = 0; y < 8; ++y) d[y] = c ? d[y] + fabsf(e[y]) : fabsf(e[y]);
+          }
+#pragma unroll
+          for (int y = 0; y < 8; y += 2) {
+            fma2(u[x + y], u[x + y + 1], u[x + y], u[x + y + 1], by, by, 0.0f, 0.0f);
+            fma2(u[x + y], u[x + y + 1], d[y], d[y + 1], slope, slope, u[x + y], u[x + y + 1]);
+          }
+        }
+        bar_arrive(&sm.pos_empty[n % kPosSlots]);
+      }
+      if ((j + 1) * kRows > clear) {
+        const int seen = lim - j * kRows;
+#pragma unroll
+        for (int x = 0; x < kRows; ++x) u[x] = x < seen ? u[x] : -INFINITY;
+      }
+      float m0 = u[0], m1 = u[1];
+#pragma unroll
+      for (int x = 2; x < kRows; x += 4) {
+        m0 = max3(m0, u[x], u[x + 1]);
+        if (x + 3 < kRows) m1 = max3(m1, u[x + 2], u[x + 3]);
+      }
+      const float most = fmaxf(m0, m1) * mul;
+      const bool rise = most > top + kLazy;  // -inf + 8 is -inf: any first score is a rise
+      if (j == js) {
+        if (rise) top = most;
+      } else if (__any_sync(0xFFFFFFFFu, rise)) {
+        const float by = rise ? exp2_fast(top - most) : 1.0f;
+        if (rise) top = most;
+        sum *= by;
+        for (int x = 0; x < a.Dn; x += 16) {
+          uint32_t o[16];
+          tmem_ld16(oc + x, o);
+          tc_wait_ld<16>(o);
+#pragma unroll
+          for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * by);
+          tmem_st16(oc + x, o);
+        }
+      }
+      const float base = top == -INFINITY ? 0.0f : -top;
+      float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+      for (int y = 0; y < kRows; y += 64) {
+        uint32_t p[32];
+#pragma unroll
+        for (int x = 0; x < 64; x += 2) {
+          float e0, e1;
+          fma2(e0, e1, u[y + x], u[y + x + 1], mul, mul, base, base);
+          e0 = exp2_fast(e0);
+          e1 = exp2_fast(e1);
+          add2(s0, s1, s0, s1, e0, e1);
+          p[x >> 1] = pack2<T>(e0, e1);
+        }
+        tmem_st32(sc + (y >> 1), p);
+      }
+      sum += s0 + s1;
+      tc_wait_st();
+      tc_before();
+      bar_arrive(&sm.p_full[t]);
+    }
+    // A tile that ends earlier lets go of the other tile's key positions.
+    if (a.slopes)
+      for (int j = last_j[t]; ok && j < je; ++j) {
+        const int n = j - js;
+        if ((ok = warp_wait(&sm.pos_full[n % kPosSlots], (n / kPosSlots) & 1, given_up))) bar_arrive(&sm.pos_empty[n % kPosSlots]);
+      }
+    // ---- output
+    const bool any = last_j[t] > js;
+    if (any && ok) ok = warp_wait(&sm.o_full[t], 0, given_up);
+    tc_after();
+    const bool parts = a.part_o != nullptr;
+    float by = parts ? 1.0f : sum > 0.0f ? 1.0f / sum : 0.0f;
+    if (!ok || *given_up) by = __int_as_float(0x7FFFFFFF);  // a wait ran out: nothing here is an answer
+    char* out = a.o.data + qrow * a.o.row + h * a.o.head;
+    float* part = parts ? a.part_o + ((static_cast<long long>(split) * a.queries + qrow) * a.H + h) * a.D : nullptr;
+    for (int x = 0; x < a.Dn; x += 16) {
+      uint32_t o[16];
+      float v[16];
+      if (any) {
+        tmem_ld16(oc + x, o);
+        tc_wait_ld<16>(o);
+      }
+#pragma unroll
+      for (int y = 0; y < 16; ++y) v[y] = any ? __uint_as_float(o[y]) * by : 0.0f * by;
+      if (!live) continue;
+#pragma unroll
+      for (int y = 0; y < 16; y += 8) {
+        if (x + y >= a.D) break;
+        if (parts) {
+          Pack<float>::store(part + x + y, v + y);
+          Pack<float>::store(part + x + y + 4, v + y + 4);
+        } else {
+          Pack<T>::store(out + (x + y) * 2, v + y);
+        }
+      }
+    }
+    if (live) {
+      const long long at = static_cast<long long>(h) * a.queries + qrow;
+      if (parts)
+        a.part_ml[(static_cast<long long>(split) * a.queries + qrow) * a.H + h] = make_float2(top, sum);
+      else if (a.lse)
+        a.lse[at] = sum > 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+    }
+    tc_before();
+  }
+  __syncthreads();
+  if (warp == 8) {
+    if (*given_up) {
+      // Loads and products still in flight end in this block's shared and tensor
+      // memory: two milliseconds are a thousand times what they take.
+      const unsigned long long until = now_ns() + 2000000ull;
+      while (now_ns() < until) {
+      }
+      __syncwarp();
+    }
+    tc_after();
+    tmem_free<512>(tm);
+  }
+  allow_next_grid();
+}
+
+// Joins the parts of a row: weights 2^(top - highest top), in order.
+template <typename T>
+__global__ void __launch_bounds__(128) pv_attn_join_kernel(const __grid_constant__ AttnArgs a) {
+  wait_prior_grid();
+  const long long w = (static_cast<long long>(blockIdx.x) * 128 + threadIdx.x) >> 5;
+  const int lane = threadIdx.x & 31;
+  if (w < static_cast<long long>(a.queries) * a.H) {
+    const int row = static_cast<int>(w / a.H), h = static_cast<int>(w % a.H);
+    const int f = frame_of(a.q0, a.frames, row);
+    const int nk = a.k0[f + 1] - a.k0[f];
+    const int splits = max(1, ((nk + kRows - 1) / kRows + a.chunk - 1) / a.chunk);
+    float top = -INFINITY;
+    for (int s = 0; s < splits; ++s) top = fmaxf(top, a.part_ml[(static_cast<long long>(s) * a.queries + row) * a.H + h].x);
+    float sum = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s = 0; s < splits; ++s) {
+      const long long at = (static_cast<long long>(s) * a.queries + row) * a.H + h;
+      const float2 ml = a.part_ml[at];
+      const float by = ml.x == -INFINITY ? 0.0f : exp2_fast(ml.x - top);
+      sum = fmaf(ml.y, by, sum);
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        if (lane * 4 + x < a.D) v[x] = fmaf(a.part_o[at * a.D + lane * 4 + x], by, v[x]);
+    }
+    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    T* out = reinterpret_cast<T*>(a.o.data + row * a.o.row + h * a.o.head);
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      if (lane * 4 + x < a.D) out[lane * 4 + x] = Pack<T>::one(v[x] * inv);
+    if (a.lse && lane == 0)
+      a.lse[static_cast<long long>(h) * a.queries + row] = sum > 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+  }
+  allow_next_grid();
+}
+
+template <typename T, int kBlocks>
+int launch_fwd(const AttnArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, dim3 grid, cudaStream_t s) {
+  auto kernel = pv_attn_fwd_kernel<T, kBlocks>;
+  const int smem = static_cast<int>(sizeof(Smem<kBlocks>)) + 1024;
+  static bool ready[64];  // set once per device; a second set does no harm
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (!ready[dev & 63]) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+      cudaGetLastError();
+      return PV_ERR_CUDA;
+    }
+    ready[dev & 63] = true;
+  }
+  return launch_pdl(kernel, grid, kThreads, smem, s, a, q, k, v);
+}
+
+}  // namespace
+
+int attn_forward(AttnArgs& a, int dtype, const AttnMaps& m, dim3 grid, cudaStream_t s) {
+  const bool wide = a.D > 64;
+  int st;
+  if (dtype == PV_BF16)
+    st = wide ? launch_fwd<__nv_bfloat16, 2>(a, m.q, m.k, m.v, grid, s) : launch_fwd<__nv_bfloat16, 1>(a, m.q, m.k, m.v, grid, s);
+  else
+    st = wide ? launch_fwd<__half, 2>(a, m.q, m.k, m.v, grid, s) : launch_fwd<__half, 1>(a, m.q, m.k, m.v, grid, s);
+  if (st != PV_OK || !a.part_o) return st;
+  const long long warps = static_cast<long long>(a.queries) * a.H;
+  const dim3 g(static_cast<unsigned int>((warps + 3) / 4));
+  return dtype == PV_BF16 ? launch_pdl(pv_attn_join_kernel<__nv_bfloat16>, g, 128, 0, s, a)
+                          : launch_pdl(pv_attn_join_kernel<__half>, g, 128, 0, s, a);
+}
+
+}  // namespace pvs
