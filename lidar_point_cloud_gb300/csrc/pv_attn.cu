@@ -6,8 +6,8 @@
 //   dv = p^T do;  du = p (do.v - delta), delta = do.o;
 //   ds = du (1 - (t / cap)^2) scale;  dq = ds k;  dk = ds^T q.
 //
-// Tiles of 16 rows against tiles of 32, in 32-bit arithmetic on the CUDA
-// cores; the running maximum and sum of a row stay in registers.
+// This file: argument checks, tensor maps, how the work is cut.  The kernels are
+// in pv_attn_fwd.cu and pv_attn_bwd.cu.
 
 #include "pv_attn.cuh"
 
@@ -21,167 +21,6 @@
 namespace {
 
 using namespace pvs;
-
-constexpr int kThreads = 128;
-constexpr int kOwn = 16;    // rows of a block
-constexpr int kOther = 32;  // rows of a step
-constexpr int kPad = 129;
-
-// The score of a pair and, for the backward pass, d(score)/d(scale q.k).
-__device__ __forceinline__ float score(const AttnArgs& a, float dot, float slope, const int* qp, const int* kp, float* grad) {
-  float s = dot * a.scale;
-  *grad = 1.0f;
-  if (a.cap > 0.0f) {
-    const float t = tanhf(s / a.cap);
-    *grad = 1.0f - t * t;
-    s = a.cap * t;
-  }
-  if (a.slopes) {
-    float d = 0.0f;
-    for (int x = 0; x < a.axes; ++x) d += fabsf(static_cast<float>(qp[x]) - static_cast<float>(kp[x]));
-    s = fmaf(-slope, d, s);
-  }
-  return s;
-}
-
-__device__ __forceinline__ bool visible(const AttnArgs& a, int f, int i, int j, int nq, int nk) {
-  return i < nq && j < nk && (!a.causal || j <= i + nk - nq || j < a.prefix[f]);
-}
-
-template <typename T>
-__device__ __forceinline__ void load_rows(const View& v, int head, int row0, int rows, int most, int D, float (*to)[kPad]) {
-  for (int i = threadIdx.x; i < most * D; i += kThreads) {
-    const int r = i / D, d = i - r * D;
-    to[r][d] = r < rows ? Pack<T>::to(*(reinterpret_cast<const T*>(v.data + (row0 + r) * v.row + head * v.head) + d)) : 0.0f;
-  }
-}
-
-__device__ __forceinline__ float dot_of(const float* a, const float* b, int D) {
-  float s = 0.0f;
-  for (int d = 0; d < D; ++d) s = fmaf(a[d], b[d], s);
-  return s;
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kThreads) pv_attn_delta_kernel(const __grid_constant__ AttnArgs a) {
-  wait_prior_grid();
-  const long long w = (static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
-  if (w < static_cast<long long>(a.queries) * a.H) {
-    const int row = static_cast<int>(w / a.H), h = static_cast<int>(w % a.H);
-    const T* o = reinterpret_cast<const T*>(a.o.data + row * a.o.row + h * a.o.head);
-    const T* g = reinterpret_cast<const T*>(a.dout.data + row * a.dout.row + h * a.dout.head);
-    float s = 0.0f;
-    for (int d = lane; d < a.D; d += 32) s = fmaf(Pack<T>::to(o[d]), Pack<T>::to(g[d]), s);
-    for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, x);
-    if (lane == 0) a.delta[static_cast<long long>(h) * a.queries + row] = s;
-  }
-  allow_next_grid();
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kThreads) pv_attn_dq_kernel(const __grid_constant__ AttnArgs a) {
-  extern __shared__ float dyn[];
-  auto rows = [&](int at) { return reinterpret_cast<float(*)[kPad]>(dyn + at * kPad); };
-  float(*qs)[kPad] = rows(0), (*gs)[kPad] = rows(kOwn), (*ks)[kPad] = rows(2 * kOwn), (*vs)[kPad] = rows(2 * kOwn + kOther);
-  __shared__ float ps[kOwn][kOther + 1];
-  wait_prior_grid();
-  const int f = frame_of(a.tile0, a.frames, blockIdx.x), h = blockIdx.y, g = h / a.G;
-  const int nq = a.q0[f + 1] - a.q0[f], nk = a.k0[f + 1] - a.k0[f];
-  const int i0 = (blockIdx.x - a.tile0[f]) * kOwn;
-  const int r = threadIdx.x >> 3, c = threadIdx.x & 7, i = i0 + r, qrow = a.q0[f] + i;
-  load_rows<T>(a.q, h, a.q0[f] + i0, nq - i0, kOwn, a.D, qs);
-  load_rows<T>(a.dout, h, a.q0[f] + i0, nq - i0, kOwn, a.D, gs);
-  float acc[16];
-  for (int d = 0; d < 16; ++d) acc[d] = 0.0f;
-  const float slope = a.slopes ? a.slopes[h] : 0.0f;
-  const float lse = i < nq ? a.lse[static_cast<long long>(h) * a.queries + qrow] : 0.0f;
-  const float delta = i < nq ? a.delta[static_cast<long long>(h) * a.queries + qrow] : 0.0f;
-  for (int j0 = 0; j0 < nk; j0 += kOther) {
-    __syncthreads();
-    load_rows<T>(a.k, g, a.k0[f] + j0, nk - j0, kOther, a.D, ks);
-    load_rows<T>(a.v, g, a.k0[f] + j0, nk - j0, kOther, a.D, vs);
-    __syncthreads();
-    for (int x = 0; x < 4; ++x) {
-      const int j = j0 + c + 8 * x;
-      float ds = 0.0f, grad;
-      if (visible(a, f, i, j, nq, nk)) {
-        const float s = score(a, dot_of(qs[r], ks[c + 8 * x], a.D), slope, a.qpos + qrow * a.qpos_stride,
-                              a.kpos + (a.k0[f] + j) * a.kpos_stride, &grad);
-        ds = expf(s - lse) * (dot_of(gs[r], vs[c + 8 * x], a.D) - delta) * grad;
-      }
-      ps[r][c + 8 * x] = ds;
-    }
-    __syncwarp();
-    for (int j = 0; j < kOther; ++j)
-      for (int d = 0; d < 16; ++d)
-        if (c + 8 * d < a.D) acc[d] = fmaf(ps[r][j], ks[j][c + 8 * d], acc[d]);
-  }
-  if (i < nq) {
-    T* o = reinterpret_cast<T*>(a.dq.data + qrow * a.dq.row + h * a.dq.head);
-    for (int d = 0; d < 16; ++d)
-      if (c + 8 * d < a.D) o[c + 8 * d] = Pack<T>::one(acc[d] * a.scale);
-  }
-  allow_next_grid();
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kThreads) pv_attn_dkv_kernel(const __grid_constant__ AttnArgs a) {
-  extern __shared__ float dyn[];
-  auto rows = [&](int at) { return reinterpret_cast<float(*)[kPad]>(dyn + at * kPad); };
-  float(*ks)[kPad] = rows(0), (*vs)[kPad] = rows(kOwn), (*qs)[kPad] = rows(2 * kOwn), (*gs)[kPad] = rows(2 * kOwn + kOther);
-  __shared__ float ps[kOwn][kOther + 1], dss[kOwn][kOther + 1];
-  wait_prior_grid();
-  const int f = frame_of(a.tile0, a.frames, blockIdx.x), g = blockIdx.y;
-  const int nq = a.q0[f + 1] - a.q0[f], nk = a.k0[f + 1] - a.k0[f];
-  const int j0 = (blockIdx.x - a.tile0[f]) * kOwn;
-  const int r = threadIdx.x >> 3, c = threadIdx.x & 7, j = j0 + r, krow = a.k0[f] + j;
-  load_rows<T>(a.k, g, a.k0[f] + j0, nk - j0, kOwn, a.D, ks);
-  load_rows<T>(a.v, g, a.k0[f] + j0, nk - j0, kOwn, a.D, vs);
-  float dk[16], dv[16];
-  for (int d = 0; d < 16; ++d) dk[d] = dv[d] = 0.0f;
-  for (int h = g * a.G; h < (g + 1) * a.G; ++h) {
-    const float slope = a.slopes ? a.slopes[h] : 0.0f;
-    for (int i0 = 0; i0 < nq; i0 += kOther) {
-      __syncthreads();
-      load_rows<T>(a.q, h, a.q0[f] + i0, nq - i0, kOther, a.D, qs);
-      load_rows<T>(a.dout, h, a.q0[f] + i0, nq - i0, kOther, a.D, gs);
-      __syncthreads();
-      for (int x = 0; x < 4; ++x) {
-        const int i = i0 + c + 8 * x, qrow = a.q0[f] + i;
-        float p = 0.0f, ds = 0.0f, grad;
-        if (visible(a, f, i, j, nq, nk)) {
-          const long long at = static_cast<long long>(h) * a.queries + qrow;
-          const float s = score(a, dot_of(ks[r], qs[c + 8 * x], a.D), slope, a.qpos + qrow * a.qpos_stride,
-                                a.kpos + krow * a.kpos_stride, &grad);
-          p = expf(s - a.lse[at]);
-          ds = p * (dot_of(vs[r], gs[c + 8 * x], a.D) - a.delta[at]) * grad;
-        }
-        ps[r][c + 8 * x] = p;
-        dss[r][c + 8 * x] = ds;
-      }
-      __syncwarp();
-      for (int i = 0; i < kOther; ++i)
-        for (int d = 0; d < 16; ++d)
-          if (c + 8 * d < a.D) {
-            dv[d] = fmaf(ps[r][i], gs[i][c + 8 * d], dv[d]);
-            dk[d] = fmaf(dss[r][i], qs[i][c + 8 * d], dk[d]);
-          }
-    }
-  }
-  if (j < nk) {
-    T* ok = reinterpret_cast<T*>(a.dk.data + krow * a.dk.row + g * a.dk.head);
-    T* ov = reinterpret_cast<T*>(a.dv.data + krow * a.dv.row + g * a.dv.head);
-    for (int d = 0; d < 16; ++d)
-      if (c + 8 * d < a.D) {
-        ok[c + 8 * d] = Pack<T>::one(dk[d] * a.scale);
-        ov[c + 8 * d] = Pack<T>::one(dv[d]);
-      }
-  }
-  allow_next_grid();
-}
-
-// ------------------------------------------------------------ host side
 
 View view_of(const pv_heads* h) { return View{static_cast<char*>(h->data), h->row_stride * 2, h->head_stride * 2}; }
 
@@ -278,43 +117,6 @@ int chunk_of(const AttnArgs& a, int heads, int sms) {
 int tiles_of(AttnArgs& a, const int* off, int own) {
   for (int b = 0; b < a.frames; ++b) a.tile0[b + 1] = a.tile0[b] + (off[b + 1] - off[b] + own - 1) / own;
   return a.tile0[a.frames];
-}
-
-template <typename K>
-int launch(K kernel, dim3 grid, size_t smem, const AttnArgs& a, pv_stream_t stream) {
-  if (grid.x == 0 || grid.y == 0) return PV_OK;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess) {
-    cudaGetLastError();
-    return PV_ERR_CUDA;
-  }
-  if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) {
-    cudaGetLastError();
-    return PV_ERR_CUDA;
-  }
-  return PV_OK;
-}
-
-template <typename T>
-int backward(AttnArgs& a, pv_stream_t stream) {
-  const size_t smem = sizeof(float) * kPad * 2 * (kOwn + kOther);
-  const long long rows = static_cast<long long>(a.queries) * a.H;
-  int st = launch(pv_attn_delta_kernel<T>, dim3(static_cast<unsigned int>((rows * 32 + kThreads - 1) / kThreads)), 0, a, stream);
-  if (st != PV_OK) return st;
-  int n = tiles_of(a, a.q0, kOwn);
-  if ((st = launch(pv_attn_dq_kernel<T>, dim3(n, a.H), smem, a, stream)) != PV_OK) return st;
-  n = tiles_of(a, a.k0, kOwn);
-  return launch(pv_attn_dkv_kernel<T>, dim3(n, a.Hk), smem, a, stream);
 }
 
 }  // namespace
@@ -430,5 +232,18 @@ extern "C" int pv_attention_backward(const pv_attention_params* params, const pv
   Scratch scratch;
   if ((st = scratch.open(dev, stream, kPlain, sizeof(float) * static_cast<size_t>(nq) * a.H)) != PV_OK) return st;
   a.delta = static_cast<float*>(scratch.body());
-  return params->dtype == PV_BF16 ? backward<__nv_bfloat16>(a, stream) : backward<__half>(a, stream);
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  AttnMaps m{};
+  if (nq && ((st = make_map(&m.q, a.q, params->dtype, a.D, a.H, 1, nq, 64)) != PV_OK ||
+             (st = make_map(&m.dout, a.dout, params->dtype, a.D, a.H, 1, nq, 64)) != PV_OK))
+    return st;
+  if (nk && ((st = make_map(&m.k, a.k, params->dtype, a.D, a.Hk, 1, nk, 64)) != PV_OK ||
+             (st = make_map(&m.v, a.v, params->dtype, a.D, a.Hk, 1, nk, 64)) != PV_OK))
+    return st;
+  if (!nk) m.k = m.v = m.q;  // nothing is loaded through these
+  if (!nq) m.q = m.dout = m.k;
+  int n = tiles_of(a, a.q0, 128);
+  if ((st = attn_backward_dq(a, params->dtype, m, dim3(n, a.H), cs)) != PV_OK) return st;
+  n = tiles_of(a, a.k0, 128);
+  return attn_backward_dkv(a, params->dtype, m, dim3(n, a.Hk), cs);
 }

@@ -16,7 +16,7 @@ struct View {
 struct AttnArgs {
   View q, k, v, o, dout, dq, dk, dv;
   float* lse;            // [H, queries]
-  float* delta;          // [H, queries]: sum of dout * out (backward)
+  float* delta;          // [H, queries]: sum of P dP (backward)
   const float* slopes;
   const int32_t* qpos;
   const int32_t* kpos;
@@ -44,6 +44,8 @@ int make_map(CUtensorMap* map, const View& v, int dtype, int D, int heads, int p
 
 // Kernel launches of pv_attn_fwd.cu and pv_attn_bwd.cu.
 int attn_forward(AttnArgs& a, int dtype, const AttnMaps& m, dim3 grid, cudaStream_t s);
+int attn_backward_dq(const AttnArgs& a, int dtype, const AttnMaps& m, dim3 grid, cudaStream_t s);   // and delta
+int attn_backward_dkv(const AttnArgs& a, int dtype, const AttnMaps& m, dim3 grid, cudaStream_t s);  // after it
 
 template <typename K, typename... A>
 int launch_pdl(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t s, const A&... args) {

@@ -343,10 +343,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
 #pragma unroll
       for (int y = 0; y < 16; ++y) v[y] = any ? __uint_as_float(o[y]) * by : 0.0f * by;
-      if (!live) continue;
 #pragma unroll
       for (int y = 0; y < 16; y += 8) {
-        if (x + y >= a.D) break;
+        if (!live || x + y >= a.D) continue;
         if (parts) {
           Pack<float>::store(part + x + y, v + y);
           Pack<float>::store(part + x + y + 4, v + y + 4);
@@ -354,6 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           Pack<T>::store(out + (x + y) * 2, v + y);
         }
       }
+      __syncwarp();
     }
     if (live) {
       const long long at = static_cast<long long>(h) * a.queries + qrow;
