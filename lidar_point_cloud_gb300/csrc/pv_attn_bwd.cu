@@ -49,12 +49,101 @@ struct Smem {
   static constexpr int kSlots = kBlocks == 1 ? 6 : 4;
   alignas(1024) unsigned char own[2][kOwnBytes];
   alignas(1024) unsigned char other[kSlots][2][kOtherBytes];
-  float side[kSides][5][kOther];  // lse (as an exponent's offset), delta, positions
+  float side[kSides][5][kOther];  // lse (as an offset of the exponent), delta (negated), positions
   float rest[2][kOwn];            // dq: each warpgroup's sum of P dP
   uint64_t own_full, full[kSlots], empty[kSlots], sp_full[2], pd_full[2], acc_full, side_full[kSides], side_empty[kSides];
   uint32_t tmem;
   int given_up;
 };
+
+struct Row {
+  float pos[3];        // negated
+  float slope, mul;    // exponent = mul * (score + slope * distance) + off
+  float cap_in;        // score = tanh of half this times the raw one, if capped
+  float off, delta;    // dq: the row's own (delta negated); dk, dv: a column's, in shared memory
+  float total;         // dq: sum of 16 P (dP - delta)
+  int lo, hi;          // columns seen: lo <= column < hi
+};
+
+// One row's 64 scores and dP, at column `at` and 64 after it, to 16 P and 16 dS
+// in the storage type in their place (dq with a cap: P times the cap's slope
+// for P).  32 columns at a time, one operation after the other over all of
+// them: an element's chain is long, 32 of them hide it.
+template <typename T, bool kDkv, bool kCap, bool kMask>
+__device__ __forceinline__ void tile(uint32_t at, const float (*side)[kOther], int axes, Row& row) {
+  float u[2][32], g[2][32];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    tmem_ld32(at + h * 32, reinterpret_cast<uint32_t*>(u[h]));
+    tmem_ld32(at + 64 + h * 32, reinterpret_cast<uint32_t*>(g[h]));
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    tc_wait_ld<32>(reinterpret_cast<uint32_t*>(u[h]));
+    tc_wait_ld<32>(reinterpret_cast<uint32_t*>(g[h]));
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float steep[kCap ? 32 : 1];
+    if (kCap) {
+#pragma unroll
+      for (int x = 0; x < 32; ++x) {
+        u[h][x] = tanh_half(u[h][x] * row.cap_in);
+        steep[x] = fmaf(-u[h][x], u[h][x], 1.0f);
+      }
+    }
+    if (axes == 1) lower<1, 32>(u[h], &side[2][h * 32], kOther, row.pos, row.slope);
+    if (axes == 2) lower<2, 32>(u[h], &side[2][h * 32], kOther, row.pos, row.slope);
+    if (axes == 3) lower<3, 32>(u[h], &side[2][h * 32], kOther, row.pos, row.slope);
+#pragma unroll
+    for (int x = 0; x < 32; x += 4) {
+      float4 l = make_float4(row.off, row.off, row.off, row.off), d = make_float4(row.delta, row.delta, row.delta, row.delta);
+      if (kDkv) {
+        l = *reinterpret_cast<const float4*>(&side[0][h * 32 + x]);
+        d = *reinterpret_cast<const float4*>(&side[1][h * 32 + x]);
+      }
+      fma2(u[h][x], u[h][x + 1], u[h][x], u[h][x + 1], row.mul, row.mul, l.x, l.y);
+      fma2(u[h][x + 2], u[h][x + 3], u[h][x + 2], u[h][x + 3], row.mul, row.mul, l.z, l.w);
+      add2(g[h][x], g[h][x + 1], g[h][x], g[h][x + 1], d.x, d.y);
+      add2(g[h][x + 2], g[h][x + 3], g[h][x + 2], g[h][x + 3], d.z, d.w);
+    }
+#pragma unroll
+    for (int x = 0; x < 32; ++x) u[h][x] = exp2_fast(u[h][x]);
+#pragma unroll
+    for (int x = 0; x < 32; ++x) {
+      g[h][x] *= u[h][x];
+      if (kMask) {
+        const bool seen = h * 32 + x >= row.lo && h * 32 + x < row.hi;
+        u[h][x] = seen ? u[h][x] : 0.0f;
+        g[h][x] = seen ? g[h][x] : 0.0f;
+      }
+    }
+    if (!kDkv) {
+      float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+#pragma unroll
+      for (int x = 0; x < 32; x += 4) {
+        add2(s0, s1, s0, s1, g[h][x], g[h][x + 1]);
+        add2(s2, s3, s2, s3, g[h][x + 2], g[h][x + 3]);
+      }
+      row.total += (s0 + s1) + (s2 + s3);
+    }
+    if (kCap) {
+#pragma unroll
+      for (int x = 0; x < 32; ++x) {
+        g[h][x] *= steep[x];
+        if (!kDkv) u[h][x] *= steep[x];
+      }
+    }
+    uint32_t p[16], s[16];
+#pragma unroll
+    for (int x = 0; x < 32; x += 2) {
+      p[x >> 1] = Pack<T>::two(u[h][x], u[h][x + 1]);
+      s[x >> 1] = Pack<T>::two(g[h][x], g[h][x + 1]);
+    }
+    tmem_st16(at + h * 16, p);
+    tmem_st16(at + 64 + h * 16, s);
+  }
+}
 
 template <typename T, int kBlocks, bool kDkv>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -170,13 +259,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
       tc_after();
-      if (lane == 0) {
+      if (elect_one()) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          const uint32_t own = smem_addr(sm.own[s]), other = smem_addr(sm.other[slot][s]);
-          for (int x = 0; x < ksteps; ++x)
-            mma_ss(tm + b * 128 + s * 64, operand(own + (x >> 2) * kOwn * 128 + (x & 3) * 32, 16),
-                   operand(other + (x >> 2) * kOther * 128 + (x & 3) * 32, 16), word_s, x > 0);
+          const uint32_t own = operand(smem_addr(sm.own[s]), 16), other = operand(smem_addr(sm.other[slot][s]), 16);
+#pragma unroll
+          for (int x = 0; x < 4 * kBlocks; ++x)
+            if (x < ksteps)
+              mma_ss(tm + b * 128 + s * 64, own + (((x >> 2) * kOwn * 128 + (x & 3) * 32) >> 4),
+                     other + (((x >> 2) * kOther * 128 + (x & 3) * 32) >> 4), word_s, x > 0);
         }
         mma_commit(&sm.sp_full[b]);
       }
@@ -188,12 +279,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int slot = n % S::kSlots, b = n & 1;
       if (!(ok = warp_wait(&sm.pd_full[b], (n >> 1) & 1, given_up))) break;
       tc_after();
-      if (lane == 0) {
-        const uint32_t b1 = smem_addr(sm.other[slot][0]), b2 = kDkv ? smem_addr(sm.other[slot][1]) : b1;
+      if (elect_one()) {
+        const uint32_t b1 = operand(smem_addr(sm.other[slot][0]), kOther * 128);
+        const uint32_t b2 = kDkv ? operand(smem_addr(sm.other[slot][1]), kOther * 128) : b1;
+#pragma unroll
         for (int x = 0; x < kOther / 16; ++x)
-          mma_ts(acc1, tm + b * 128 + 64 + x * 8, operand(b1 + x * 2048, kOther * 128), word_a, n > 0 || x > 0);
+          mma_ts(acc1, tm + b * 128 + 64 + x * 8, b1 + x * (2048 >> 4), word_a, n > 0 || x > 0);
+#pragma unroll
         for (int x = 0; x < kOther / 16; ++x)
-          mma_ts(acc2, tm + b * 128 + x * 8, operand(b2 + x * 2048, kOther * 128), word_a, n > 0 || x > 0);
+          mma_ts(acc2, tm + b * 128 + x * 8, b2 + x * (2048 >> 4), word_a, n > 0 || x > 0);
         mma_commit(&sm.empty[slot]);
         if (n == steps - 1) mma_commit(&sm.acc_full);
       }
@@ -212,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const long long row = (kDkv ? a.q0[f] : a.k0[f]) + row0 + x;
           if (kDkv) {
             sm.side[slot][0][x] = in ? fmaf(-kLog2e, a.lse[static_cast<long long>(h) * a.queries + row], kUp) : 0.0f;
-            sm.side[slot][1][x] = in ? a.delta[static_cast<long long>(h) * a.queries + row] : 0.0f;
+            sm.side[slot][1][x] = in ? -a.delta[static_cast<long long>(h) * a.queries + row] : 0.0f;
           }
           for (int c = 0; c < a.axes; ++c)
             sm.side[slot][2 + c][x] =
@@ -229,18 +323,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool live = own < own_rows;
     const long long own_row = (kDkv ? a.k0[f] : a.q0[f]) + own;
     const uint32_t mine = tm + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    float op[3] = {0.0f, 0.0f, 0.0f};
+    Row row{};
     if (a.slopes && live)
-      for (int c = 0; c < a.axes; ++c)
-        op[c] = -static_cast<float>(kDkv ? a.kpos[own_row * a.kpos_stride + c] : a.qpos[own_row * a.qpos_stride + c]);
-    const float unit = a.scale * kLog2e;
-    const float mul = a.slopes || a.cap > 0.0f ? 1.0f : unit;
-    const float cap_in = a.cap > 0.0f ? 2.0f * unit / a.cap : 0.0f, cap_out = a.cap * kLog2e;
-    const float by = a.cap > 0.0f ? 1.0f : unit;
-    float slope = a.slopes && !kDkv ? -a.slopes[own_head] * kLog2e : 0.0f;
-    float off = 0.0f, delta = 0.0f, total = 0.0f;
+#pragma unroll
+      for (int c = 0; c < 3; ++c)
+        if (c < a.axes) row.pos[c] = -static_cast<float>(kDkv ? a.kpos[own_row * a.kpos_stride + c] : a.qpos[own_row * a.qpos_stride + c]);
+    row.mul = (a.cap > 0.0f ? a.cap : a.scale) * kLog2e;
+    row.cap_in = a.cap > 0.0f ? 2.0f * a.scale * kLog2e / a.cap : 0.0f;
+    row.slope = a.slopes && !kDkv ? -a.slopes[own_head] * kLog2e / row.mul : 0.0f;
+    float delta = 0.0f;
     if (!kDkv && live) {
-      off = fmaf(-kLog2e, a.lse[static_cast<long long>(own_head) * a.queries + own_row], kUp);
+      row.off = fmaf(-kLog2e, a.lse[static_cast<long long>(own_head) * a.queries + own_row], kUp);
       const char* o = a.o.data + own_row * a.o.row + own_head * a.o.head;
       const char* g = a.dout.data + own_row * a.dout.row + own_head * a.dout.head;
       for (int d = 0; d < a.D; d += 8) {
@@ -250,6 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int e = 0; e < 8; ++e) delta = fmaf(x[e], y[e], delta);
       }
+      row.delta = -delta;
     }
     // A place is seen if its column is at least `from` and below `to`.
     int from = 0, to = other_rows;
@@ -264,87 +358,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(ok = warp_wait(&sm.sp_full[wg], (n >> 1) & 1, given_up))) break;
       const int slot = n % kSides;
       if (sides && !(ok = warp_wait(&sm.side_full[slot], (n / kSides) & 1, given_up))) break;
-      if (kDkv && a.slopes) slope = -a.slopes[other_head(n)] * kLog2e;
+      if (kDkv && a.slopes) row.slope = -a.slopes[other_head(n)] * kLog2e / row.mul;
       tc_after();
       const int row0 = other_row(n);
-      float u[kOther], g[kOther];
-      uint32_t *ur = reinterpret_cast<uint32_t*>(u), *gr = reinterpret_cast<uint32_t*>(g);
-#pragma unroll
-      for (int x = 0; x < kOther; x += 32) {
-        tmem_ld32(mine + wg * 128 + x, ur + x);
-        tmem_ld32(mine + wg * 128 + 64 + x, gr + x);
-      }
-      tc_wait_ld<kOther>(ur);
-      tc_wait_ld<kOther>(gr);
       const float(*side)[kOther] = sm.side[slot];
       // Seen whole: nothing of the tile is hidden from any of the block's rows.
       const bool whole = row0 + kOther <= other_rows &&
                          (!a.causal || (kDkv ? limit(row0) >= min(own0 + kOwn, nk) : limit(own0) >= row0 + kOther));
-      const int lo = from - row0, hi = to - row0;
-      uint32_t p[kOther / 2], s[kOther / 2];
-#pragma unroll
-      for (int x = 0; x < kOther; x += 4) {
-        float steep[4] = {1.0f, 1.0f, 1.0f, 1.0f};
-        if (a.cap > 0.0f) {
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const float t = fmaf(-2.0f, rcp_fast(1.0f + exp2_fast(u[x + y] * cap_in)), 1.0f);
-            steep[y] = fmaf(-t, t, 1.0f);
-            u[x + y] = cap_out * t;
-          }
-        }
-        if (a.slopes) {
-          float d[4];
-          for (int c = 0; c < a.axes; ++c) {
-            const float4 v = *reinterpret_cast<const float4*>(&side[2 + c][x]);
-            float e[4];
-            add2(e[0], e[1], v.x, v.y, op[c], op[c]);
-            add2(e[2], e[3], v.z, v.w, op[c], op[c]);
-#pragma unroll
-            for (int y = 0; y < 4; ++y) d[y] = c ? d[y] + fabsf(e[y]) : fabsf(e[y]);
-          }
-#pragma unroll
-          for (int y = 0; y < 4; y += 2) {
-            fma2(u[x + y], u[x + y + 1], u[x + y], u[x + y + 1], by, by, 0.0f, 0.0f);
-            fma2(u[x + y], u[x + y + 1], d[y], d[y + 1], slope, slope, u[x + y], u[x + y + 1]);
-          }
-        }
-        float l[4] = {off, off, off, off}, dl[4] = {-delta, -delta, -delta, -delta};
-        if (kDkv) {
-          const float4 v = *reinterpret_cast<const float4*>(&side[0][x]);
-          const float4 w = *reinterpret_cast<const float4*>(&side[1][x]);
-          l[0] = v.x, l[1] = v.y, l[2] = v.z, l[3] = v.w;
-          dl[0] = -w.x, dl[1] = -w.y, dl[2] = -w.z, dl[3] = -w.w;
-        }
-        float e[4], ds[4];
-#pragma unroll
-        for (int y = 0; y < 4; y += 2) {
-          fma2(e[y], e[y + 1], u[x + y], u[x + y + 1], mul, mul, l[y], l[y + 1]);
-          e[y] = exp2_fast(e[y]);
-          e[y + 1] = exp2_fast(e[y + 1]);
-          add2(ds[y], ds[y + 1], g[x + y], g[x + y + 1], dl[y], dl[y + 1]);
-        }
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          ds[y] *= e[y];
-          if (!whole) {
-            const bool seen = x + y >= lo && x + y < hi;
-            e[y] = seen ? e[y] : 0.0f;
-            ds[y] = seen ? ds[y] : 0.0f;
-          }
-          if (!kDkv) total += ds[y];
-          if (a.cap > 0.0f) {
-            ds[y] *= steep[y];
-            if (!kDkv) e[y] *= steep[y];
-          }
-        }
-        p[x >> 1] = Pack<T>::two(e[0], e[1]);
-        p[(x >> 1) + 1] = Pack<T>::two(e[2], e[3]);
-        s[x >> 1] = Pack<T>::two(ds[0], ds[1]);
-        s[(x >> 1) + 1] = Pack<T>::two(ds[2], ds[3]);
+      row.lo = from - row0;
+      row.hi = to - row0;
+      const uint32_t at = mine + wg * 128;
+      if (a.cap > 0.0f) {
+        if (whole)
+          tile<T, kDkv, true, false>(at, side, a.axes, row);
+        else
+          tile<T, kDkv, true, true>(at, side, a.axes, row);
+      } else {
+        if (whole)
+          tile<T, kDkv, false, false>(at, side, a.axes, row);
+        else
+          tile<T, kDkv, false, true>(at, side, a.axes, row);
       }
-      tmem_st32(mine + wg * 128, p);
-      tmem_st32(mine + wg * 128 + 64, s);
       if (sides) bar_arrive(&sm.side_empty[slot]);
       tc_wait_st();
       tc_before();
@@ -356,10 +390,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_after();
     // dq: the sum of P (dP - delta) is what delta is off by.
     if (!kDkv) {
-      sm.rest[wg][r] = total;
+      sm.rest[wg][r] = row.total;
       asm volatile("bar.sync 1, 256;" ::: "memory");
-      total = (sm.rest[0][r] + sm.rest[1][r]) * kDown;
-      if (live && wg == 0) a.delta[static_cast<long long>(own_head) * a.queries + own_row] = delta + total;
+      row.total = (sm.rest[0][r] + sm.rest[1][r]) * kDown;
+      if (live && wg == 0) a.delta[static_cast<long long>(own_head) * a.queries + own_row] = delta + row.total;
     }
     const float bad = !ok || *given_up ? __int_as_float(0x7FFFFFFF) : 1.0f;  // a wait ran out: nothing here is an answer
     const View& out = kDkv ? (wg ? a.dv : a.dk) : a.dq;
@@ -378,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int y = 0; y < 16; ++y) {
         float w = any ? __uint_as_float(c[y]) : 0.0f;
-        if (!kDkv && any) w = fmaf(-total, __uint_as_float(d[y]), w);
+        if (!kDkv && any) w = fmaf(-row.total, __uint_as_float(d[y]), w);
         v[y] = w * k1;
       }
 #pragma unroll

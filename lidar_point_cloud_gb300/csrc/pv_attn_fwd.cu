@@ -139,11 +139,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int ksteps = (a.D + 15) / 16;
     bool ok = je > js && warp_wait(&sm.q_full, 0, given_up);
     auto scores = [&](int t, int n) {  // S_t = Q_t K^T
-      if (lane == 0) {
-        const uint32_t q = smem_addr(sm.q[t]), k = smem_addr(sm.kv[n % S::kSlots]);
-        for (int x = 0; x < ksteps; ++x) {
-          const uint32_t off = (x >> 2) * kRows * 128 + (x & 3) * 32;
-          mma_ss(tm + t * 128, operand(q + off, 16), operand(k + off, 16), word_s, x > 0);
+      if (elect_one()) {
+        const uint32_t q = operand(smem_addr(sm.q[t]), 16), k = operand(smem_addr(sm.kv[n % S::kSlots]), 16);
+#pragma unroll
+        for (int x = 0; x < 4 * kBlocks; ++x) {
+          const uint32_t off = ((x >> 2) * kRows * 128 + (x & 3) * 32) >> 4;
+          if (x < ksteps) mma_ss(tm + t * 128, q + off, k + off, word_s, x > 0);
         }
         mma_commit(&sm.s_full[t]);
       }
@@ -155,7 +156,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_after();
       for (int t = 0; t < 2; ++t)
         if (last_j[t] > js) scores(t, 0);
-      if (lane == 0) mma_commit(&sm.kv_empty[0]);
+      if (elect_one()) mma_commit(&sm.kv_empty[0]);
+      __syncwarp();
     }
     for (int j = js; ok && j < je; ++j) {
       const int nv = 2 * (j - js) + 1, nk1 = nv + 1;
@@ -175,19 +177,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (j >= last_j[t]) continue;
         if (!(ok = warp_wait(&sm.p_full[t], (j - js) & 1, given_up))) break;
         tc_after();
-        if (lane == 0) {
-          const uint32_t v = smem_addr(sm.kv[nv % S::kSlots]);
+        if (elect_one()) {
+          const uint32_t v = operand(smem_addr(sm.kv[nv % S::kSlots]), kRows * 128);
+#pragma unroll
           for (int x = 0; x < kRows / 16; ++x)
-            mma_ts(tm + 256 + t * 64 * kBlocks, tm + t * 128 + x * 8, operand(v + x * 2048, kRows * 128), word_o,
-                   j > js || x > 0);
+            mma_ts(tm + 256 + t * 64 * kBlocks, tm + t * 128 + x * 8, v + x * (2048 >> 4), word_o, j > js || x > 0);
         }
         __syncwarp();
         if (j + 1 < last_j[t])
           scores(t, nk1);
-        else if (lane == 0)
+        else if (elect_one())
           mma_commit(&sm.o_full[t]);
+        __syncwarp();
       }
-      if (ok && lane == 0) {
+      if (ok && elect_one()) {
         mma_commit(&sm.kv_empty[nv % S::kSlots]);
         if (j + 1 < je) mma_commit(&sm.kv_empty[nk1 % S::kSlots]);
       }
@@ -223,13 +226,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     float slope = 0.0f, qp[3] = {0.0f, 0.0f, 0.0f};
     if (a.slopes && live) {
       slope = -a.slopes[h] * kLog2e;
-      for (int c = 0; c < a.axes; ++c) qp[c] = -static_cast<float>(a.qpos[qrow * a.qpos_stride + c]);
+#pragma unroll
+      for (int c = 0; c < 3; ++c)
+        if (c < a.axes) qp[c] = -static_cast<float>(a.qpos[qrow * a.qpos_stride + c]);
     }
-    // Scores in units of log2: raw scores times `unit`, or final ones if a cap or
-    // a distance has been worked in.
-    const float unit = a.scale * kLog2e;
-    const float mul = a.slopes || a.cap > 0.0f ? 1.0f : unit;
-    const float cap_in = a.cap > 0.0f ? 2.0f * unit / a.cap : 0.0f, cap_out = a.cap * kLog2e;
+    // What a score (the raw product, or tanh of it if capped) is multiplied by to
+    // be in units of log2.
+    const float mul = (a.cap > 0.0f ? a.cap : a.scale) * kLog2e;
+    const float cap_in = a.cap > 0.0f ? 2.0f * a.scale * kLog2e / a.cap : 0.0f;
+    slope /= mul;
     float top = -INFINITY, sum = 0.0f;
     bool ok = true;
     for (int j = js; j < last_j[t]; ++j) {
@@ -242,32 +247,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int x = 0; x < kRows; x += 32) tmem_ld32(sc + x, ur + x);
       tc_wait_ld<kRows>(ur);
       if (a.cap > 0.0f) {
-        // cap tanh(s / cap) = cap (1 - 2 / (1 + exp(2 s / cap)))
 #pragma unroll
-        for (int x = 0; x < kRows; ++x)
-          u[x] = fmaf(-2.0f * cap_out, rcp_fast(1.0f + exp2_fast(u[x] * cap_in)), cap_out);
+        for (int x = 0; x < kRows; ++x) u[x] = tanh_half(u[x] * cap_in);
       }
       if (a.slopes) {
-        const float by = a.cap > 0.0f ? 1.0f : unit;
         if (!(ok = warp_wait(&sm.pos_full[n % kPosSlots], (n / kPosSlots) & 1, given_up))) break;
-#pragma unroll
-        for (int x = 0; x < kRows; x += 8) {
-          float d[8];
-          for (int c = 0; c < a.axes; ++c) {
-            const float4* p = reinterpret_cast<const float4*>(&sm.pos[n % kPosSlots][c][x]);
-            const float4 v0 = p[0], v1 = p[1];
-            float e[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-#pragma unroll
-            for (int y = 0; y < 8; y += 2) add2(e[y], e[y + 1], e[y], e[y + 1], qp[c], qp[c]);
-#pragma unroll
-            for (int y = 0; y < 8; ++y) d[y] = c ? d[y] + fabsf(e[y]) : fabsf(e[y]);
-          }
-#pragma unroll
-          for (int y = 0; y < 8; y += 2) {
-            fma2(u[x + y], u[x + y + 1], u[x + y], u[x + y + 1], by, by, 0.0f, 0.0f);
-            fma2(u[x + y], u[x + y + 1], d[y], d[y + 1], slope, slope, u[x + y], u[x + y + 1]);
-          }
-        }
+        const float(*pos)[kRows] = sm.pos[n % kPosSlots];
+        if (a.axes == 1)
+          lower<1, kRows>(u, pos[0], kRows, qp, slope);
+        else if (a.axes == 2)
+          lower<2, kRows>(u, pos[0], kRows, qp, slope);
+        else
+          lower<3, kRows>(u, pos[0], kRows, qp, slope);
         bar_arrive(&sm.pos_empty[n % kPosSlots]);
       }
       if ((j + 1) * kRows > clear) {
@@ -275,13 +266,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int x = 0; x < kRows; ++x) u[x] = x < seen ? u[x] : -INFINITY;
       }
-      float m0 = u[0], m1 = u[1];
+      float m[4] = {u[0], u[1], u[2], u[3]};
 #pragma unroll
-      for (int x = 2; x < kRows; x += 4) {
-        m0 = max3(m0, u[x], u[x + 1]);
-        if (x + 3 < kRows) m1 = max3(m1, u[x + 2], u[x + 3]);
-      }
-      const float most = fmaxf(m0, m1) * mul;
+      for (int x = 4; x < kRows; x += 8)
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          if (x + 2 * y + 1 < kRows) m[y] = max3(m[y], u[x + 2 * y], u[x + 2 * y + 1]);
+      const float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * mul;
       const bool rise = most > top + kLazy;  // -inf + 8 is -inf: any first score is a rise
       if (j == js) {
         if (rise) top = most;

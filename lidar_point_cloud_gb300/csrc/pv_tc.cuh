@@ -145,10 +145,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
 // Shared-memory operand in 128-byte swizzled rows (64 16-bit elements), 8 rows
 // to 1,024 bytes.  Rows along M or N ("K-major"): `lead` is not used.  Rows
 // along K ("MN-major"): `lead` is the distance of the next 64 elements of M or N.
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead) {
-  return (static_cast<uint64_t>(addr >> 4) & 0x3FFF) | (static_cast<uint64_t>((lead >> 4) & 0x3FFF) << 16) |
-         (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+// The low word; steps through the operand add (bytes / 16) to it.
+__device__ __forceinline__ uint32_t operand(uint32_t addr, uint32_t lead) {
+  return ((addr >> 4) & 0x3FFF) | ((lead >> 4) << 16);
 }
+constexpr uint32_t kOperandHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
 
 // Instruction word: 32-bit sums, both operands bf16 or both f16.
 __host__ __device__ constexpr uint32_t mma_word(bool bf16, int M, int N, bool a_mn, bool b_mn) {
@@ -156,19 +157,35 @@ __host__ __device__ constexpr uint32_t mma_word(bool bf16, int M, int N, bool a_
          ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// One thread; D (tensor memory) = A B (+ D if `add`), 16 elements of K.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t word, bool add) {
+// One thread of a converged warp: the products' operands live in registers that
+// a warp shares, and with elect.sync the compiler knows that one lane runs.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(word), "r"(static_cast<uint32_t>(add))
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+
+// One thread; D (tensor memory) = A B (+ D if `add`), 16 elements of K.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t word, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(word), "r"(static_cast<uint32_t>(add)), "r"(kOperandHigh)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t word, bool add) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t word, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(word), "r"(static_cast<uint32_t>(add))
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+      "mov.b64 db, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(word), "r"(static_cast<uint32_t>(add)), "r"(kOperandHigh)
       : "memory");
 }
 // The barrier gets one arrival when everything that this thread has issued is done.
@@ -219,6 +236,28 @@ __device__ __forceinline__ void add2(float& x0, float& x1, float a0, float a1, f
       "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
       : "=f"(x0), "=f"(x1)
       : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+
+// tanh(x / (2 log2(e))) = 1 - 2 / (1 + 2^x): a few 2^-24 off, absolutely.
+__device__ __forceinline__ float tanh_half(float x) { return fmaf(-2.0f, rcp_fast(1.0f + exp2_fast(x)), 1.0f); }
+
+// u += slope * distance between a row's position (negated, in `own`) and those of
+// n columns, axis after axis `stride` floats apart.
+template <int kAxes, int n>
+__device__ __forceinline__ void lower(float* u, const float* pos, int stride, const float* own, float slope) {
+#pragma unroll
+  for (int x = 0; x < n; x += 4) {
+    float d[4];
+#pragma unroll
+    for (int c = 0; c < kAxes; ++c) {
+      const float4 v = *reinterpret_cast<const float4*>(pos + c * stride + x);
+      const float e[4] = {v.x + own[c], v.y + own[c], v.z + own[c], v.w + own[c]};
+#pragma unroll
+      for (int y = 0; y < 4; ++y) d[y] = c ? d[y] + fabsf(e[y]) : fabsf(e[y]);
+    }
+#pragma unroll
+    for (int y = 0; y < 4; ++y) u[x + y] = fmaf(slope, d[y], u[x + y]);
+  }
 }
 
 }  // namespace pvs
