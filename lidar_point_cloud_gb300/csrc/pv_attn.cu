@@ -229,21 +229,32 @@ extern "C" int pv_attention_backward(const pv_attention_params* params, const pv
   a.dq = view_of(dq);
   a.dk = view_of(dk);
   a.dv = view_of(dv);
+  const int sms = sm_count(dev);
+  if (sms < 1) return PV_ERR_CUDA;
+  const int key_tiles = tiles_of(a, a.k0, 128);
+  // A key head's block walks the queries of all heads that share it: with few
+  // blocks for the multiprocessors (under a causal mask of unequal length too) the
+  // heads are cut into parts, joined by one more kernel.
+  a.head_parts = 1;
+  while (a.G % (2 * a.head_parts) == 0 && static_cast<int64_t>(key_tiles) * a.Hk * a.head_parts < 4 * sms) a.head_parts *= 2;
   Scratch scratch;
-  if ((st = scratch.open(dev, stream, kPlain, sizeof(float) * static_cast<size_t>(nq) * a.H)) != PV_OK) return st;
+  const size_t rows = round_up(static_cast<size_t>(nq) * a.H, 4);
+  const size_t parts = a.head_parts > 1 ? static_cast<size_t>(2) * a.head_parts * nk * a.Hk * a.D : 0;
+  if ((st = scratch.open(dev, stream, kPlain, sizeof(float) * (rows + parts))) != PV_OK) return st;
   a.delta = static_cast<float*>(scratch.body());
+  a.part_o = a.delta + rows;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   AttnMaps m{};
-  if (nq && ((st = make_map(&m.q, a.q, params->dtype, a.D, a.H, 1, nq, 64)) != PV_OK ||
-             (st = make_map(&m.dout, a.dout, params->dtype, a.D, a.H, 1, nq, 64)) != PV_OK))
+  if (nq && ((st = make_map(&m.q, a.q, params->dtype, a.D, a.H, 1, nq, 128)) != PV_OK ||
+             (st = make_map(&m.dout, a.dout, params->dtype, a.D, a.H, 1, nq, 128)) != PV_OK))
     return st;
-  if (nk && ((st = make_map(&m.k, a.k, params->dtype, a.D, a.Hk, 1, nk, 64)) != PV_OK ||
-             (st = make_map(&m.v, a.v, params->dtype, a.D, a.Hk, 1, nk, 64)) != PV_OK))
+  if (nk && ((st = make_map(&m.k, a.k, params->dtype, a.D, a.Hk, 1, nk, 128)) != PV_OK ||
+             (st = make_map(&m.v, a.v, params->dtype, a.D, a.Hk, 1, nk, 128)) != PV_OK))
     return st;
   if (!nk) m.k = m.v = m.q;  // nothing is loaded through these
   if (!nq) m.q = m.dout = m.k;
   int n = tiles_of(a, a.q0, 128);
   if ((st = attn_backward_dq(a, params->dtype, m, dim3(n, a.H), cs)) != PV_OK) return st;
   n = tiles_of(a, a.k0, 128);
-  return attn_backward_dkv(a, params->dtype, m, dim3(n, a.Hk), cs);
+  return attn_backward_dkv(a, params->dtype, m, dim3(n, a.Hk * a.head_parts), cs);
 }

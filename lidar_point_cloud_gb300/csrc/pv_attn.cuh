@@ -25,8 +25,10 @@ struct AttnArgs {
   int axes, causal, H, Hk, G, D, frames, queries, keys;
   int Dn;          // D rounded up to 16
   int pack_log2;   // heads of a key head that share a tile of rows (log2)
+  int head_parts;  // blocks among which the query heads of a key head are cut (dk, dv)
   int chunk;       // key tiles of a block: fewer than there are if the keys are split
-  float* part_o;   // split keys: [split, queries, H, D] unnormalised outputs, or null
+  float* part_o;   // split keys: [split, queries, H, D] unnormalised outputs, or null;
+                   // backward with head_parts > 1: [part, dk or dv, keys, Hk, D]
   float2* part_ml; // split keys: [split, queries, H] maximum (in units of log2) and sum
   int q0[PV_MAX_FRAMES + 1];    // row offsets of the frames
   int k0[PV_MAX_FRAMES + 1];

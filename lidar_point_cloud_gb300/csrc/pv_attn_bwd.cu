@@ -2,16 +2,22 @@
 //
 // Two kernels of one form, so that every sum is taken in a fixed order and
 // none needs atomics.  A block owns 128 rows (queries for dq, keys for dk and
-// dv), held in shared memory, and walks the other side in tiles of 64 rows:
+// dv), held in shared memory, and walks the other side in tiles of 128 rows:
 //   S = own1 other1^T, dP = own2 other2^T     (scores and do.v, or transposed)
 //   P = exp(score - lse), dS = P (dP - delta) d(score)/d(s)
-//   acc1 += dS other1,  acc2 += P other
+//   acc2 += P other,  acc1 += dS other1
 // with own = (q, do), other = (k, v) for dq, and the other way round for dk
-// (acc1) and dv (acc2 += P^T do).  S and dP are double-buffered in tensor memory;
-// P and dS replace them there, as the next products' operands.  Warps 0-3 and
-// 4-7 take the two buffers in turn, one row a thread; warp 8 issues the
-// products, warp 9 the loads, warp 10 puts what belongs to the other side's
-// rows (lse, delta, positions) into shared memory.
+// (acc1) and dv (acc2 += P^T do).  P replaces S in tensor memory and dS dP, as
+// the next products' operands.  Warps 0-3 and 4-7 take 64 columns each, one row
+// a thread; warp 8 issues the products, warp 9 the loads, warp 10 puts what
+// belongs to the other side's rows (lse, delta, positions) into shared memory.
+//
+// The accumulators of 128-element heads leave room for one S and one dP only,
+// so the work is staggered: while the threads make dS of a tile, the tensor cores
+// run acc2 and the next tile's S, and while they make the next P, acc1 and the
+// next dP.  A product of 128 columns from shared memory takes 64 cycles, as much as
+// one of 64 columns (55 measured): tiles of 64 columns with two buffers, tried
+// first, left the tensor cores 1.4 times the work.
 //
 // delta = do.o of the rounded o would leave each row's dS with a sum that is
 // not zero: an error of P times the rounding of o, which for a row that few
@@ -27,6 +33,7 @@
 #include "pv_attn.cuh"
 #include "pv_tc.cuh"
 
+#include <algorithm>
 #include <type_traits>
 
 namespace pvs {
@@ -36,22 +43,23 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kRegsMath = 208, kRegsOther = 80;  // 256 x 208 + 128 x 80 = 63,488 of 384 x 168 = 64,512
 constexpr int kOwn = 128;    // rows of a block
-constexpr int kOther = 64;   // rows of a step
-constexpr int kSides = 4;    // slots of what belongs to the other side's rows
+constexpr int kOther = 128;  // rows of a step
+constexpr int kHalf = 64;    // columns of a thread
+constexpr int kSides = 3;    // slots of what belongs to the other side's rows
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kUp = 4.0f;  // log2 of the factor on P and dS
 constexpr float kDown = 0.0625f;
 
 template <int kBlocks>
 struct Smem {
-  static constexpr int kOwnBytes = kOwn * 128 * kBlocks;
-  static constexpr int kOtherBytes = kOther * 128 * kBlocks;
-  static constexpr int kSlots = kBlocks == 1 ? 6 : 4;
-  alignas(1024) unsigned char own[2][kOwnBytes];
-  alignas(1024) unsigned char other[kSlots][2][kOtherBytes];
+  static constexpr int kTile = kOwn * 128 * kBlocks;  // bytes of 128 rows of a head
+  static constexpr int kSlots = kBlocks == 1 ? 4 : 2;
+  alignas(1024) unsigned char own[2][kTile];
+  alignas(1024) unsigned char other[2][kSlots][kTile];
   float side[kSides][5][kOther];  // lse (as an offset of the exponent), delta (negated), positions
-  float rest[2][kOwn];            // dq: each warpgroup's sum of P dP
-  uint64_t own_full, full[kSlots], empty[kSlots], sp_full[2], pd_full[2], acc_full, side_full[kSides], side_empty[kSides];
+  float rest[2][kOwn];            // dq: each warpgroup's sum of P (dP - delta)
+  uint64_t own_full, full[2][kSlots], empty[2][kSlots], s_full, dp_full, p_full, ds_full, acc_full, side_full[kSides],
+      side_empty[kSides];
   uint32_t tmem;
   int given_up;
 };
@@ -65,84 +73,113 @@ struct Row {
   int lo, hi;          // columns seen: lo <= column < hi
 };
 
-// One row's 64 scores and dP, at column `at` and 64 after it, to 16 P and 16 dS
-// in the storage type in their place (dq with a cap: P times the cap's slope
-// for P).  32 columns at a time, one operation after the other over all of
-// them: an element's chain is long, 32 of them hide it.
+// One row's 64 scores at column `at` of tensor memory to 16 P there, in the
+// storage type.  e keeps what dS is made of: 16 P times the cap's slope; with a
+// cap, dq also needs 16 P itself (as half pairs in `whole_p`: only the small
+// sum that mends delta is made of it) and takes e for acc2.  Columns are taken 32 at a
+// time, one operation after the other over all of them: an element's chain is
+// long, 32 of them hide it.
 template <typename T, bool kDkv, bool kCap, bool kMask>
-__device__ __forceinline__ void tile(uint32_t at, const float (*side)[kOther], int axes, Row& row) {
-  float u[2][32], g[2][32];
+__device__ __forceinline__ void probabilities(uint32_t at, const float (*side)[kOther], int c0, int axes, const Row& row,
+                                              float* e, uint32_t* whole_p) {
+  tmem_ld32(at, reinterpret_cast<uint32_t*>(e));
+  tmem_ld32(at + 32, reinterpret_cast<uint32_t*>(e + 32));
+  tc_wait_ld<kHalf>(reinterpret_cast<uint32_t*>(e));
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    tmem_ld32(at + h * 32, reinterpret_cast<uint32_t*>(u[h]));
-    tmem_ld32(at + 64 + h * 32, reinterpret_cast<uint32_t*>(g[h]));
-  }
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    tc_wait_ld<32>(reinterpret_cast<uint32_t*>(u[h]));
-    tc_wait_ld<32>(reinterpret_cast<uint32_t*>(g[h]));
-  }
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
+    float* u = e + h * 32;
+    const int c = c0 + h * 32;
     float steep[kCap ? 32 : 1];
     if (kCap) {
 #pragma unroll
       for (int x = 0; x < 32; ++x) {
-        u[h][x] = tanh_half(u[h][x] * row.cap_in);
-        steep[x] = fmaf(-u[h][x], u[h][x], 1.0f);
+        u[x] = tanh_half(u[x] * row.cap_in);
+        steep[x] = fmaf(-u[x], u[x], 1.0f);
       }
     }
-    if (axes == 1) lower<1, 32>(u[h], &side[2][h * 32], kOther, row.pos, row.slope);
-    if (axes == 2) lower<2, 32>(u[h], &side[2][h * 32], kOther, row.pos, row.slope);
-    if (axes == 3) lower<3, 32>(u[h], &side[2][h * 32], kOther, row.pos, row.slope);
+    if (axes == 1) lower<1, 32>(u, &side[2][c], kOther, row.pos, row.slope);
+    if (axes == 2) lower<2, 32>(u, &side[2][c], kOther, row.pos, row.slope);
+    if (axes == 3) lower<3, 32>(u, &side[2][c], kOther, row.pos, row.slope);
 #pragma unroll
     for (int x = 0; x < 32; x += 4) {
-      float4 l = make_float4(row.off, row.off, row.off, row.off), d = make_float4(row.delta, row.delta, row.delta, row.delta);
-      if (kDkv) {
-        l = *reinterpret_cast<const float4*>(&side[0][h * 32 + x]);
-        d = *reinterpret_cast<const float4*>(&side[1][h * 32 + x]);
-      }
-      fma2(u[h][x], u[h][x + 1], u[h][x], u[h][x + 1], row.mul, row.mul, l.x, l.y);
-      fma2(u[h][x + 2], u[h][x + 3], u[h][x + 2], u[h][x + 3], row.mul, row.mul, l.z, l.w);
-      add2(g[h][x], g[h][x + 1], g[h][x], g[h][x + 1], d.x, d.y);
-      add2(g[h][x + 2], g[h][x + 3], g[h][x + 2], g[h][x + 3], d.z, d.w);
+      float4 l = make_float4(row.off, row.off, row.off, row.off);
+      if (kDkv) l = *reinterpret_cast<const float4*>(&side[0][c + x]);
+      fma2(u[x], u[x + 1], u[x], u[x + 1], row.mul, row.mul, l.x, l.y);
+      fma2(u[x + 2], u[x + 3], u[x + 2], u[x + 3], row.mul, row.mul, l.z, l.w);
     }
-#pragma unroll
-    for (int x = 0; x < 32; ++x) u[h][x] = exp2_fast(u[h][x]);
 #pragma unroll
     for (int x = 0; x < 32; ++x) {
-      g[h][x] *= u[h][x];
-      if (kMask) {
-        const bool seen = h * 32 + x >= row.lo && h * 32 + x < row.hi;
-        u[h][x] = seen ? u[h][x] : 0.0f;
-        g[h][x] = seen ? g[h][x] : 0.0f;
-      }
+      u[x] = exp2_fast(u[x]);
+      if (kMask) u[x] = c + x >= row.lo && c + x < row.hi ? u[x] : 0.0f;
     }
-    if (!kDkv) {
-      float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+    uint32_t p[16];
+    if (!kCap || kDkv) {
 #pragma unroll
-      for (int x = 0; x < 32; x += 4) {
-        add2(s0, s1, s0, s1, g[h][x], g[h][x + 1]);
-        add2(s2, s3, s2, s3, g[h][x + 2], g[h][x + 3]);
-      }
-      row.total += (s0 + s1) + (s2 + s3);
+      for (int x = 0; x < 32; x += 2) p[x >> 1] = Pack<T>::two(u[x], u[x + 1]);
     }
     if (kCap) {
+      if (!kDkv) {
 #pragma unroll
-      for (int x = 0; x < 32; ++x) {
-        g[h][x] *= steep[x];
-        if (!kDkv) u[h][x] *= steep[x];
+        for (int x = 0; x < 32; x += 2) whole_p[h * 16 + (x >> 1)] = Pack<__half>::two(u[x], u[x + 1]);
+      }
+#pragma unroll
+      for (int x = 0; x < 32; ++x) u[x] *= steep[x];
+      if (!kDkv) {
+#pragma unroll
+        for (int x = 0; x < 32; x += 2) p[x >> 1] = Pack<T>::two(u[x], u[x + 1]);
       }
     }
-    uint32_t p[16], s[16];
-#pragma unroll
-    for (int x = 0; x < 32; x += 2) {
-      p[x >> 1] = Pack<T>::two(u[h][x], u[h][x + 1]);
-      s[x >> 1] = Pack<T>::two(g[h][x], g[h][x + 1]);
-    }
     tmem_st16(at + h * 16, p);
-    tmem_st16(at + 64 + h * 16, s);
   }
+}
+
+// dP at column `at` to 16 dS there.
+template <typename T, bool kDkv, bool kCap, bool kMask>
+__device__ __forceinline__ void gradients(uint32_t at, const float (*side)[kOther], int c0, Row& row, const float* e,
+                                          const uint32_t* whole_p) {
+  float g[kHalf];
+  tmem_ld32(at, reinterpret_cast<uint32_t*>(g));
+  tmem_ld32(at + 32, reinterpret_cast<uint32_t*>(g + 32));
+  tc_wait_ld<kHalf>(reinterpret_cast<uint32_t*>(g));
+  float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t s[16];
+#pragma unroll
+    for (int x = h * 32; x < h * 32 + 32; x += 4) {
+      float4 d = make_float4(row.delta, row.delta, row.delta, row.delta);
+      if (kDkv) d = *reinterpret_cast<const float4*>(&side[1][c0 + x]);
+      add2(g[x], g[x + 1], g[x], g[x + 1], d.x, d.y);
+      add2(g[x + 2], g[x + 3], g[x + 2], g[x + 3], d.z, d.w);
+      float v[4];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        v[y] = g[x + y] * e[x + y];
+        // (A hidden place has e = 0, but what stands at it need not be finite.)
+        if (kMask) v[y] = c0 + x + y >= row.lo && c0 + x + y < row.hi ? v[y] : 0.0f;
+      }
+      s[(x & 31) >> 1] = Pack<T>::two(v[0], v[1]);
+      s[((x & 31) >> 1) + 1] = Pack<T>::two(v[2], v[3]);
+      if (!kDkv) {
+        if (kCap) {
+          float w[4];
+#pragma unroll
+          for (int y = 0; y < 4; y += 2) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&whole_p[(x + y) >> 1]));
+            w[y] = g[x + y] * f.x;
+            w[y + 1] = g[x + y + 1] * f.y;
+          }
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            v[y] = !kMask || (c0 + x + y >= row.lo && c0 + x + y < row.hi) ? w[y] : 0.0f;
+        }
+        add2(s0, s1, s0, s1, v[0], v[1]);
+        add2(s2, s3, s2, s3, v[2], v[3]);
+      }
+    }
+    tmem_st16(at + h * 16, s);
+  }
+  if (!kDkv) row.total += (s0 + s1) + (s2 + s3);
 }
 
 template <typename T, int kBlocks, bool kDkv>
@@ -163,20 +200,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Under a causal mask late queries and early keys have the most work: they go first.
   const int own0 = (kDkv ? local : tiles - 1 - local) * kOwn;
   auto limit = [&](int i) { return a.causal ? max(min(max(i + shift + 1, a.prefix[f]), nk), 0) : nk; };
-  int other_tile0, per_head, steps;
+  // dk, dv: the query heads of a key head may be cut into parts, a block each.
+  const int own_head = kDkv ? blockIdx.y / a.head_parts : blockIdx.y;
+  const int heads = kDkv ? a.G / a.head_parts : 1;
+  const int head0 = kDkv ? blockIdx.y * heads : own_head / a.G;
+  int other_tile0 = 0, per_head;
   if (kDkv) {
     const int begin = a.causal && own0 >= a.prefix[f] ? max(own0 - shift, 0) : 0;
     other_tile0 = begin / kOther;
     per_head = max((nq + kOther - 1) / kOther - other_tile0, 0);
-    steps = per_head * a.G;
   } else {
-    other_tile0 = 0;
-    per_head = steps = (limit(min(own0 + kOwn, nq) - 1) + kOther - 1) / kOther;
+    per_head = (limit(min(own0 + kOwn, nq) - 1) + kOther - 1) / kOther;
   }
+  const int steps = per_head * heads;
   const int own_rows = kDkv ? nk : nq, other_rows = kDkv ? nq : nk;
-  const int own_head = blockIdx.y;
   // Head of the other side at step n, and its first row.
-  auto other_head = [&](int n) { return kDkv ? own_head * a.G + n / per_head : own_head / a.G; };
+  auto other_head = [&](int n) { return kDkv ? head0 + n / per_head : head0; };
   auto other_row = [&](int n) { return (other_tile0 + (kDkv ? n % per_head : n)) * kOther; };
 
   // ---- set up
@@ -184,9 +223,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     sm.given_up = 0;
     bar_init(&sm.own_full, 1);
     bar_init(&sm.acc_full, 1);
-    for (int i = 0; i < S::kSlots; ++i) bar_init(&sm.full[i], 1), bar_init(&sm.empty[i], 1);
-    for (int b = 0; b < 2; ++b) bar_init(&sm.sp_full[b], 1), bar_init(&sm.pd_full[b], kOwn);
-    for (int i = 0; i < kSides; ++i) bar_init(&sm.side_full[i], 32), bar_init(&sm.side_empty[i], kOwn);
+    for (int s = 0; s < 2; ++s)
+      for (int i = 0; i < S::kSlots; ++i) bar_init(&sm.full[s][i], 1), bar_init(&sm.empty[s][i], 1);
+    bar_init(&sm.s_full, 1);
+    bar_init(&sm.dp_full, 1);
+    bar_init(&sm.p_full, 2 * kOwn);
+    bar_init(&sm.ds_full, 2 * kOwn);
+    for (int i = 0; i < kSides; ++i) bar_init(&sm.side_full[i], 32), bar_init(&sm.side_empty[i], 2 * kOwn);
     fence_bar_init();
     tma_prefetch(&mq);
     tma_prefetch(&mk);
@@ -197,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_before();
   __syncthreads();
   tc_after();
-  const uint32_t tm = sm.tmem;
+  const uint32_t tm = sm.tmem;  // columns: S 0, dP 128, acc1 256, acc2 256 + 64 kBlocks
   volatile int* given_up = &sm.given_up;
   const bool sides = kDkv || a.slopes != nullptr;
   wait_prior_grid();
@@ -206,35 +249,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 9) {
     // ---- loads
     if (lane == 0 && steps > 0) {
-      const CUtensorMap* o1 = kDkv ? &mk : &mq;
-      const CUtensorMap* o2 = kDkv ? &mv : &mdo;
-      const CUtensorMap* t1 = kDkv ? &mq : &mk;
-      const CUtensorMap* t2 = kDkv ? &mdo : &mv;
-      const View& v1 = kDkv ? a.k : a.q;
-      const View& v2 = kDkv ? a.v : a.dout;
-      const View& w1 = kDkv ? a.q : a.k;
-      const View& w2 = kDkv ? a.dout : a.v;
+      const CUtensorMap* own_map[2] = {kDkv ? &mk : &mq, kDkv ? &mv : &mdo};
+      const CUtensorMap* other_map[2] = {kDkv ? &mq : &mk, kDkv ? &mdo : &mv};
+      const bool own_heads[2] = {(kDkv ? a.k.head : a.q.head) != 0, (kDkv ? a.v.head : a.dout.head) != 0};
+      const bool other_heads[2] = {(kDkv ? a.q.head : a.k.head) != 0, (kDkv ? a.dout.head : a.v.head) != 0};
       const int own_base = (kDkv ? a.k0[f] : a.q0[f]) + own0, other_base = kDkv ? a.q0[f] : a.k0[f];
-      // The second half of the own rows may lie past the last row of all: it is
-      // then left out (nothing of those rows is written).
-      const int halves = own0 + kOther < own_rows ? 2 : 1;
-      bar_expect(&sm.own_full, 2 * halves * kOther * 128 * kBlocks);
-      for (int b = 0; b < kBlocks; ++b)
-        for (int x = 0; x < halves; ++x) {
-          tma_load4(sm.own[0] + b * kOwn * 128 + x * kOther * 128, o1, b * 64, 0, v1.head ? own_head : 0,
-                    own_base + x * kOther, &sm.own_full);
-          tma_load4(sm.own[1] + b * kOwn * 128 + x * kOther * 128, o2, b * 64, 0, v2.head ? own_head : 0,
-                    own_base + x * kOther, &sm.own_full);
-        }
+      bar_expect(&sm.own_full, 2 * S::kTile);
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        for (int b = 0; b < kBlocks; ++b)
+          tma_load4(sm.own[s] + b * kOwn * 128, own_map[s], b * 64, 0, own_heads[s] ? own_head : 0, own_base, &sm.own_full);
       for (int n = 0; n < steps; ++n) {
-        const int slot = n % S::kSlots;
-        if (!bar_wait(&sm.empty[slot], ((n / S::kSlots) & 1) ^ 1, given_up)) break;
-        bar_expect(&sm.full[slot], 2 * S::kOtherBytes);
-        const int h = other_head(n), row = other_base + other_row(n);
-        for (int b = 0; b < kBlocks; ++b) {
-          tma_load4(sm.other[slot][0] + b * kOther * 128, t1, b * 64, 0, w1.head ? h : 0, row, &sm.full[slot]);
-          tma_load4(sm.other[slot][1] + b * kOther * 128, t2, b * 64, 0, w2.head ? h : 0, row, &sm.full[slot]);
+        const int slot = n % S::kSlots, h = other_head(n), row = other_base + other_row(n);
+        bool ok = true;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          if (!ok || !(ok = bar_wait(&sm.empty[s][slot], ((n / S::kSlots) & 1) ^ 1, given_up))) continue;
+          bar_expect(&sm.full[s][slot], S::kTile);
+          for (int b = 0; b < kBlocks; ++b)
+            tma_load4(sm.other[s][slot] + b * kOther * 128, other_map[s], b * 64, 0, other_heads[s] ? h : 0, row,
+                      &sm.full[s][slot]);
         }
+        if (!ok) break;
       }
     }
   } else if (warp == 8) {
@@ -242,57 +278,58 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t word_s = mma_word(kBf16, 128, kOther, false, false);
     const uint32_t word_a = mma_word(kBf16, 128, 0, false, true) | (static_cast<uint32_t>(a.Dn >> 3) << 17);
     const int ksteps = (a.D + 15) / 16;
-    const uint32_t acc1 = tm + 256, acc2 = tm + 256 + 64 * kBlocks;
     bool ok = steps > 0 && warp_wait(&sm.own_full, 0, given_up);
-    auto scores = [&](int n) {
-      const int slot = n % S::kSlots, b = n & 1;
-      if (!warp_wait(&sm.full[slot], (n / S::kSlots) & 1, given_up)) return false;
+    // S (s = 0) or dP (s = 1) of step n, from its operand's arrival.
+    auto scores = [&](int s, int n) {
+      const int slot = n % S::kSlots;
+      if (!warp_wait(&sm.full[s][slot], (n / S::kSlots) & 1, given_up)) return false;
       const int have = other_rows - other_row(n);
       if (have < kOther) {
         // Rows past the frame's end are another frame's, whatever they hold.
-        for (int s = 0; s < 2; ++s) {
-          uint4* v = reinterpret_cast<uint4*>(sm.other[slot][s]);
-          for (int c = 0; c < kBlocks; ++c)
-            for (int i = have * 8 + lane; i < kOther * 8; i += 32) v[c * kOther * 8 + i] = make_uint4(0, 0, 0, 0);
-        }
+        uint4* v = reinterpret_cast<uint4*>(sm.other[s][slot]);
+        for (int c = 0; c < kBlocks; ++c)
+          for (int i = have * 8 + lane; i < kOther * 8; i += 32) v[c * kOther * 8 + i] = make_uint4(0, 0, 0, 0);
         fence_to_async();
         __syncwarp();
       }
       tc_after();
       if (elect_one()) {
+        const uint32_t own = operand(smem_addr(sm.own[s]), 16), other = operand(smem_addr(sm.other[s][slot]), 16);
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const uint32_t own = operand(smem_addr(sm.own[s]), 16), other = operand(smem_addr(sm.other[slot][s]), 16);
-#pragma unroll
-          for (int x = 0; x < 4 * kBlocks; ++x)
-            if (x < ksteps)
-              mma_ss(tm + b * 128 + s * 64, own + (((x >> 2) * kOwn * 128 + (x & 3) * 32) >> 4),
-                     other + (((x >> 2) * kOther * 128 + (x & 3) * 32) >> 4), word_s, x > 0);
+        for (int x = 0; x < 4 * kBlocks; ++x) {
+          const uint32_t off = ((x >> 2) * kOwn * 128 + (x & 3) * 32) >> 4;
+          if (x < ksteps) mma_ss(tm + s * 128, own + off, other + off, word_s, x > 0);
         }
-        mma_commit(&sm.sp_full[b]);
+        mma_commit(s ? &sm.dp_full : &sm.s_full);
+        if (!kDkv && s) mma_commit(&sm.empty[1][slot]);  // dq: nothing else needs v
       }
       __syncwarp();
       return true;
     };
-    for (int n = 0; ok && n < min(steps, 2); ++n) ok = scores(n);
-    for (int n = 0; ok && n < steps; ++n) {
-      const int slot = n % S::kSlots, b = n & 1;
-      if (!(ok = warp_wait(&sm.pd_full[b], (n >> 1) & 1, given_up))) break;
+    // acc2 += P other (s = 0) or acc1 += dS other1 (s = 1).
+    auto sums = [&](int s, int n) {
+      const int slot = n % S::kSlots, from = kDkv && s == 0 ? 1 : 0;
       tc_after();
       if (elect_one()) {
-        const uint32_t b1 = operand(smem_addr(sm.other[slot][0]), kOther * 128);
-        const uint32_t b2 = kDkv ? operand(smem_addr(sm.other[slot][1]), kOther * 128) : b1;
+        const uint32_t b = operand(smem_addr(sm.other[from][slot]), kOther * 128);
+        const uint32_t acc = tm + 256 + (s ? 0 : 64 * kBlocks), left = tm + s * 128;
 #pragma unroll
-        for (int x = 0; x < kOther / 16; ++x)
-          mma_ts(acc1, tm + b * 128 + 64 + x * 8, b1 + x * (2048 >> 4), word_a, n > 0 || x > 0);
-#pragma unroll
-        for (int x = 0; x < kOther / 16; ++x)
-          mma_ts(acc2, tm + b * 128 + x * 8, b2 + x * (2048 >> 4), word_a, n > 0 || x > 0);
-        mma_commit(&sm.empty[slot]);
-        if (n == steps - 1) mma_commit(&sm.acc_full);
+        for (int x = 0; x < kOther / 16; ++x)  // the two halves' columns lie 64 apart
+          mma_ts(acc, left + (x >> 2) * 64 + (x & 3) * 8, b + x * (2048 >> 4), word_a, n > 0 || x > 0);
+        if (kDkv && s == 0) mma_commit(&sm.empty[1][slot]);
+        if (s == 1) mma_commit(&sm.empty[0][slot]);
+        if (s == 1 && n == steps - 1) mma_commit(&sm.acc_full);
       }
       __syncwarp();
-      if (n + 2 < steps) ok = scores(n + 2);
+    };
+    ok = ok && scores(0, 0) && scores(1, 0);
+    for (int n = 0; ok && n < steps; ++n) {
+      if (!(ok = warp_wait(&sm.p_full, n & 1, given_up))) break;
+      sums(0, n);
+      if (n + 1 < steps && !(ok = scores(0, n + 1))) break;
+      if (!(ok = warp_wait(&sm.ds_full, n & 1, given_up))) break;
+      sums(1, n);
+      if (n + 1 < steps) ok = scores(1, n + 1);
     }
   } else if (warp == 10) {
     // ---- what belongs to the other side's rows
@@ -301,6 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int slot = n % kSides;
         if (!warp_wait(&sm.side_empty[slot], ((n / kSides) & 1) ^ 1, given_up)) break;
         const int h = other_head(n), row0 = other_row(n);
+#pragma unroll
         for (int x = lane; x < kOther; x += 32) {
           const bool in = row0 + x < other_rows;
           const long long row = (kDkv ? a.q0[f] : a.k0[f]) + row0 + x;
@@ -316,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp < 8) {
-    // ---- probabilities and gradients: one own row a thread
+    // ---- probabilities and gradients: one own row, 64 columns of each step a thread
     regs_up<kRegsMath>();
     const int wg = warp >> 2, r = threadIdx.x & (kOwn - 1);
     const int own = own0 + r;
@@ -327,7 +365,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (a.slopes && live)
 #pragma unroll
       for (int c = 0; c < 3; ++c)
-        if (c < a.axes) row.pos[c] = -static_cast<float>(kDkv ? a.kpos[own_row * a.kpos_stride + c] : a.qpos[own_row * a.qpos_stride + c]);
+        if (c < a.axes)
+          row.pos[c] = -static_cast<float>(kDkv ? a.kpos[own_row * a.kpos_stride + c] : a.qpos[own_row * a.qpos_stride + c]);
     row.mul = (a.cap > 0.0f ? a.cap : a.scale) * kLog2e;
     row.cap_in = a.cap > 0.0f ? 2.0f * a.scale * kLog2e / a.cap : 0.0f;
     row.slope = a.slopes && !kDkv ? -a.slopes[own_head] * kLog2e / row.mul : 0.0f;
@@ -353,36 +392,52 @@ __global__ void __launch_bounds__(kThreads, 1)
       else
         to = live ? limit(own) : 0;
     }
+    const int c0 = wg * kHalf;
+    const uint32_t s_at = mine + c0, dp_at = mine + 128 + c0;
     bool ok = true;
-    for (int n = wg; n < steps; n += 2) {
-      if (!(ok = warp_wait(&sm.sp_full[wg], (n >> 1) & 1, given_up))) break;
+    // One step with the cap and the mask as compile-time choices.
+    auto step = [&](auto cap, auto mask, int n, const float(*side)[kOther]) {
+      constexpr bool kCap = decltype(cap)::value, kMask = decltype(mask)::value;
+      float e[kHalf];
+      uint32_t whole_p[kCap && !kDkv ? kHalf / 2 : 1];
+      probabilities<T, kDkv, kCap, kMask>(s_at, side, c0, a.axes, row, e, whole_p);
+      tc_wait_st();
+      tc_before();
+      bar_arrive(&sm.p_full);
+      if (!(ok = warp_wait(&sm.dp_full, n & 1, given_up))) return;
+      tc_after();
+      gradients<T, kDkv, kCap, kMask>(dp_at, side, c0, row, e, whole_p);
+      tc_wait_st();
+      tc_before();
+      bar_arrive(&sm.ds_full);
+    };
+    for (int n = 0; n < steps; ++n) {
       const int slot = n % kSides;
       if (sides && !(ok = warp_wait(&sm.side_full[slot], (n / kSides) & 1, given_up))) break;
       if (kDkv && a.slopes) row.slope = -a.slopes[other_head(n)] * kLog2e / row.mul;
-      tc_after();
       const int row0 = other_row(n);
-      const float(*side)[kOther] = sm.side[slot];
       // Seen whole: nothing of the tile is hidden from any of the block's rows.
       const bool whole = row0 + kOther <= other_rows &&
                          (!a.causal || (kDkv ? limit(row0) >= min(own0 + kOwn, nk) : limit(own0) >= row0 + kOther));
       row.lo = from - row0;
       row.hi = to - row0;
-      const uint32_t at = mine + wg * 128;
+      if (!(ok = warp_wait(&sm.s_full, n & 1, given_up))) break;
+      tc_after();
+      using Yes = std::true_type;
+      using No = std::false_type;
       if (a.cap > 0.0f) {
         if (whole)
-          tile<T, kDkv, true, false>(at, side, a.axes, row);
+          step(Yes{}, No{}, n, sm.side[slot]);
         else
-          tile<T, kDkv, true, true>(at, side, a.axes, row);
+          step(Yes{}, Yes{}, n, sm.side[slot]);
       } else {
         if (whole)
-          tile<T, kDkv, false, false>(at, side, a.axes, row);
+          step(No{}, No{}, n, sm.side[slot]);
         else
-          tile<T, kDkv, false, true>(at, side, a.axes, row);
+          step(No{}, Yes{}, n, sm.side[slot]);
       }
+      if (!ok) break;
       if (sides) bar_arrive(&sm.side_empty[slot]);
-      tc_wait_st();
-      tc_before();
-      bar_arrive(&sm.pd_full[wg]);
     }
     // ---- outputs
     const bool any = steps > 0;
@@ -398,6 +453,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float bad = !ok || *given_up ? __int_as_float(0x7FFFFFFF) : 1.0f;  // a wait ran out: nothing here is an answer
     const View& out = kDkv ? (wg ? a.dv : a.dk) : a.dq;
     char* to_row = out.data + own_row * out.row + own_head * out.head;
+    const bool parts = kDkv && a.head_parts > 1;
+    float* part = parts ? a.part_o + (((static_cast<long long>(blockIdx.y % a.head_parts) * 2 + wg) * a.keys + own_row) * a.Hk + own_head) * a.D
+                        : nullptr;
     const float k1 = (kDkv && wg ? 1.0f : a.scale) * kDown * bad;
     const uint32_t acc = mine + 256 + (kDkv && wg ? 64 * kBlocks : 0);
     for (int x = kDkv ? 0 : wg * 16; x < a.Dn; x += kDkv ? 16 : 32) {
@@ -416,8 +474,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         v[y] = w * k1;
       }
 #pragma unroll
-      for (int y = 0; y < 16; y += 8)
-        if (live && x + y < a.D) Pack<T>::store(to_row + (x + y) * 2, v + y);
+      for (int y = 0; y < 16; y += 8) {
+        if (!live || x + y >= a.D) continue;
+        if (parts) {
+          Pack<float>::store(part + x + y, v + y);
+          Pack<float>::store(part + x + y + 4, v + y + 4);
+        } else {
+          Pack<T>::store(to_row + (x + y) * 2, v + y);
+        }
+      }
       __syncwarp();
     }
     tc_before();
@@ -434,6 +499,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc_after();
     tmem_free<512>(tm);
+  }
+  allow_next_grid();
+}
+
+// dk and dv of a key head whose query heads were cut into parts: the parts' sum, in order.
+template <typename T>
+__global__ void __launch_bounds__(256) pv_attn_bwd_join_kernel(const __grid_constant__ AttnArgs a) {
+  wait_prior_grid();
+  const long long per = static_cast<long long>(a.keys) * a.Hk * a.D / 8;
+  for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < 2 * per; i += static_cast<long long>(gridDim.x) * 256) {
+    const int wg = i >= per;
+    const long long at = (i - wg * per) * 8;
+    float v[8] = {};
+    for (int p = 0; p < a.head_parts; ++p) {
+      const float* part = a.part_o + (static_cast<long long>(p) * 2 + wg) * per * 8 + at;
+      float x[8];
+      Pack<float>::load(part, x);
+      Pack<float>::load(part + 4, x + 4);
+#pragma unroll
+      for (int y = 0; y < 8; ++y) v[y] += x[y];
+    }
+    const long long d = at % a.D, head = at / a.D % a.Hk, r = at / a.D / a.Hk;
+    const View& out = wg ? a.dv : a.dk;
+    Pack<T>::store(out.data + r * out.row + head * out.head + d * 2, v);
   }
   allow_next_grid();
 }
@@ -468,7 +557,12 @@ int attn_backward_dq(const AttnArgs& a, int dtype, const AttnMaps& m, dim3 grid,
 }
 
 int attn_backward_dkv(const AttnArgs& a, int dtype, const AttnMaps& m, dim3 grid, cudaStream_t s) {
-  return dtype == PV_BF16 ? side<__nv_bfloat16, true>(a, m, grid, s) : side<__half, true>(a, m, grid, s);
+  const int st = dtype == PV_BF16 ? side<__nv_bfloat16, true>(a, m, grid, s) : side<__half, true>(a, m, grid, s);
+  if (st != PV_OK || a.head_parts < 2 || grid.x == 0) return st;
+  const long long words = static_cast<long long>(a.keys) * a.Hk * a.D / 4;
+  const dim3 g(static_cast<unsigned int>(std::min<long long>((words + 255) / 256, 4096)));
+  return dtype == PV_BF16 ? launch_pdl(pv_attn_bwd_join_kernel<__nv_bfloat16>, g, 256, 0, s, a)
+                          : launch_pdl(pv_attn_bwd_join_kernel<__half>, g, 256, 0, s, a);
 }
 
 }  // namespace pvs
