@@ -77,16 +77,15 @@ class RopeParams(ctypes.Structure):
 
 
 class AttentionParams(ctypes.Structure):
-    _fields_ = [("frames", ctypes.c_int), ("q_offsets", ctypes.POINTER(ctypes.c_int64)),
-                ("k_offsets", ctypes.POINTER(ctypes.c_int64)), ("q_heads", ctypes.c_int), ("k_heads", ctypes.c_int),
+    _fields_ = [("frames", ctypes.c_int), ("q_offsets", ctypes.c_void_p), ("k_offsets", ctypes.c_void_p), ("q_heads", ctypes.c_int), ("k_heads", ctypes.c_int),
                 ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int), ("scale", ctypes.c_float), ("cap", ctypes.c_float),
                 ("slopes", ctypes.c_void_p), ("q_positions", ctypes.c_void_p), ("q_position_stride", ctypes.c_int64),
                 ("k_positions", ctypes.c_void_p), ("k_position_stride", ctypes.c_int64), ("axes", ctypes.c_int),
-                ("causal", ctypes.c_int), ("prefix", ctypes.POINTER(ctypes.c_int64))]
+                ("causal", ctypes.c_int), ("prefix", ctypes.c_void_p)]
 
 
 class ScanParams(ctypes.Structure):
-    _fields_ = [("frames", ctypes.c_int), ("offsets", ctypes.POINTER(ctypes.c_int64)), ("channels", ctypes.c_int64),
+    _fields_ = [("frames", ctypes.c_int), ("offsets", ctypes.c_void_p), ("channels", ctypes.c_int64),
                 ("dtype", ctypes.c_int), ("reverse", ctypes.c_int), ("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64),
                 ("gate", ctypes.c_void_p), ("gate_stride", ctypes.c_int64)]
 
@@ -102,6 +101,8 @@ def lib_path() -> str:
 def load(path: Optional[str] = None):
     """Load libpv.so.  Raises if it has not been built (no fallback)."""
     global _lib
+    if _lib is not None and path is None:
+        return _lib
     with _lock:
         if _lib is not None and path is None:
             return _lib

@@ -11,25 +11,20 @@ its own, to be used from a ``torch.autograd.Function``.
 
 from __future__ import annotations
 
-import ctypes
+import array
 from typing import Optional, Sequence
 
 from ._binding import (MAX_FRAMES, AttentionParams, Heads, PVError, RopeParams, ScanParams, _torch, load)
 
-
-def _dtypes():
-    torch = _torch()
-    return {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-
-
-_DTYPES = None
+_codes = None
 
 
 def _dtype(t, name: str, wide: bool = True) -> int:
-    global _DTYPES
-    if _DTYPES is None:
-        _DTYPES = _dtypes()
-    code = _DTYPES.get(t.dtype)
+    global _codes
+    if _codes is None:
+        torch = _torch()
+        _codes = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+    code = _codes.get(t.dtype)
     if code is None or (code == 0 and not wide):
         raise TypeError(f"{name} must be {'float32, ' if wide else ''}bfloat16 or float16, got {t.dtype}")
     return code
@@ -37,60 +32,78 @@ def _dtype(t, name: str, wide: bool = True) -> int:
 
 def _heads(t, name: str, like=None, heads: Optional[int] = None) -> Heads:
     """[rows, heads, head_dim] as the library reads it: any strides that are
-    multiples of 16 bytes, the last dimension dense."""
-    if t.dim() != 3:
+    multiples of 16 bytes, the last dimension dense.  `like`: the tensor whose
+    dtype, device and head_dim (and, with no `heads`, shape) it must have."""
+    shape = t.shape
+    if len(shape) != 3:
         raise ValueError(f"{name} must have shape [rows, heads, head_dim]")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if like is not None:
-        if t.dtype != like.dtype or t.device != like.device:
+    if like is None:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+    else:
+        if t.dtype is not like.dtype or t.get_device() != like.get_device():
             raise TypeError(f"{name} must have the dtype and device of the other tensors")
-        if t.shape[2] != like.shape[2] or (heads is None and t.shape != like.shape):
-            raise ValueError(f"{name} has the wrong shape {tuple(t.shape)}")
-    s = t.stride()
-    if t.numel():
-        align = 16 // t.element_size()
-        if (s[2] != 1 and t.shape[2] > 1) or s[0] % align or s[1] % align or s[0] < 0 or t.data_ptr() % 16:
+        if shape[2] != like.shape[2] or (heads is None and shape != like.shape):
+            raise ValueError(f"{name} has the wrong shape {tuple(shape)}")
+    row, head, one = t.stride()
+    at = t.data_ptr()
+    size = t.element_size()
+    if (at | row * size | head * size) & 15 or one != 1 or row < 0:
+        if t.numel() and not (one != 1 and shape[2] == 1 and not (at | row * size | head * size) & 15):
             raise ValueError(f"{name}: head_dim must be dense, its rows and heads on 16-byte boundaries")
-    return Heads(t.data_ptr(), s[0], s[1])
+    return Heads(at, row, head)
 
 
-def _floats(t, shape, device, name: str) -> int:
+def _dense(like):
     torch = _torch()
-    if t.dtype != torch.float32 or t.device != device:
-        raise TypeError(f"{name} must be a float32 tensor on {device}")
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}")
+    if like.is_contiguous():
+        return torch.empty_like(like)  # the quickest of torch's ways
+    return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+
+
+def _new(like):
+    """A dense tensor like this one, and how the library reads it."""
+    t = _dense(like)
+    row, head, _ = t.stride()
+    return t, Heads(t.data_ptr(), row, head)
+
+
+def _floats(t, shape, dev: int, name: str) -> int:
+    if t.dtype is not _torch().float32 or t.get_device() != dev:
+        raise TypeError(f"{name} must be a float32 tensor on the device of the others")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with shape {shape}")
     return t.data_ptr()
 
 
-def _positions(t, rows: int, device, name: str):
+def _positions(t, rows: int, dev: int, name: str):
     """int32 [rows, axes], 1 to 3 axes, rows strided as they come (a slice of
     the voxelizer's coordinates)."""
-    torch = _torch()
-    if t.dtype != torch.int32 or t.device != device:
-        raise TypeError(f"{name} must be an int32 tensor on {device}")
-    if t.dim() != 2 or t.shape[0] != rows or not 1 <= t.shape[1] <= 3:
+    if t.dtype is not _torch().int32 or t.get_device() != dev:
+        raise TypeError(f"{name} must be an int32 tensor on the device of the others")
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != rows or not 1 <= shape[1] <= 3:
         raise ValueError(f"{name} must have shape [{rows}, 1..3]")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    stride, one = t.stride()
+    if shape[1] > 1 and one != 1:
         raise ValueError(f"{name}: the axes of a row must be dense")
-    return t.data_ptr(), (t.stride(0) if rows > 1 else max(t.stride(0), t.shape[1])), int(t.shape[1])
+    return t.data_ptr(), (stride if rows > 1 else max(stride, shape[1])), shape[1]
 
 
 def _offsets(seq: Sequence[int], rows: int, name: str):
     n = len(seq) - 1
     if not 1 <= n <= MAX_FRAMES:
         raise ValueError(f"{name} must hold 1 to {MAX_FRAMES} frames' offsets and the end")
-    off = (ctypes.c_int64 * (n + 1))(*seq)
+    off = array.array("q", seq)
     if off[0] != 0 or off[n] != rows:
         raise ValueError(f"{name} must run from 0 to the {rows} rows")
     return off, n
 
 
-def _stream(stream, device):
+def _stream(stream, t) -> int:
     if stream is None:
-        stream = _torch().cuda.current_stream(device)
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+        return _torch()._C._cuda_getCurrentRawStream(t.get_device())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _check(status: int, where: str) -> None:
@@ -111,17 +124,13 @@ def rope_frequencies(head_dim: int, axes: int = 1, theta: float = 10000.0, devic
 
 def _rope_params(q, k, q_weight, k_weight, positions, inv_freq, eps):
     rows, hq, D = q.shape
-    p = RopeParams()
-    p.rows, p.q_heads, p.k_heads, p.head_dim = rows, hq, k.shape[1], D
-    p.dtype = _dtype(q, "q")
     if k.shape[0] != rows:
         raise ValueError("k must have the rows of q")
-    p.q_weight = _floats(q_weight, (D,), q.device, "q_weight")
-    p.k_weight = _floats(k_weight, (D,), q.device, "k_weight")
-    p.positions, p.position_stride, p.axes = _positions(positions, rows, q.device, "positions")
-    p.inv_freq = _floats(inv_freq, (D // 2,), q.device, "inv_freq")
-    p.eps = eps
-    return p
+    dev = q.get_device()
+    pos, stride, axes = _positions(positions, rows, dev, "positions")
+    return RopeParams(rows, hq, k.shape[1], D, _dtype(q, "q"), _floats(q_weight, (D,), dev, "q_weight"),
+                      _floats(k_weight, (D,), dev, "k_weight"), pos, stride, axes,
+                      _floats(inv_freq, (D // 2,), dev, "inv_freq"), eps)
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps: float = 1e-6, out=None, stream=None):
@@ -135,13 +144,14 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps: float = 1e-
     coordinates as they stand, e.g. ``coords[:, 1:]``).  ``out`` = (q, k)
     buffers, which may be the inputs.  Returns (q, k).
     """
-    torch = _torch()
-    hq, hk = _heads(q, "q"), _heads(k, "k", q, k.shape[1] if k.dim() == 3 else None)
+    hq, hk = _heads(q, "q"), _heads(k, "k", q, 1)
     p = _rope_params(q, k, q_weight, k_weight, positions, inv_freq, eps)
-    oq, ok = out if out is not None else (torch.empty(q.shape, dtype=q.dtype, device=q.device),
-                                          torch.empty(k.shape, dtype=q.dtype, device=q.device))
-    _check(load().pv_qk_norm_rope(p, hq, hk, _heads(oq, "out q", q), _heads(ok, "out k", k),
-                                  _stream(stream, q.device)), "pv_qk_norm_rope")
+    if out is None:
+        (oq, hoq), (ok, hok) = _new(q), _new(k)
+    else:
+        oq, ok = out
+        hoq, hok = _heads(oq, "out q", q), _heads(ok, "out k", k)
+    _check(load().pv_qk_norm_rope(p, hq, hk, hoq, hok, _stream(stream, q)), "pv_qk_norm_rope")
     return oq, ok
 
 
@@ -150,47 +160,51 @@ def qk_norm_rope_backward(dout_q, dout_k, q, k, q_weight, k_weight, positions, i
     """Gradients of :func:`qk_norm_rope` from those of its outputs and its
     inputs: (dq, dk, dq_weight, dk_weight), the last two float32."""
     torch = _torch()
-    hq, hk = _heads(q, "q"), _heads(k, "k", q, k.shape[1] if k.dim() == 3 else None)
+    hq, hk = _heads(q, "q"), _heads(k, "k", q, 1)
     p = _rope_params(q, k, q_weight, k_weight, positions, inv_freq, eps)
-    dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    dk = torch.empty(k.shape, dtype=q.dtype, device=q.device)
-    dw = torch.empty((2, q.shape[2]), dtype=torch.float32, device=q.device)
-    _check(load().pv_qk_norm_rope_backward(
-        p, _heads(dout_q, "dout_q", q), _heads(dout_k, "dout_k", k), hq, hk, _heads(dq, "dq"), _heads(dk, "dk"),
-        dw.data_ptr(), dw.data_ptr() + 4 * q.shape[2], _stream(stream, q.device)), "pv_qk_norm_rope_backward")
+    (dq, hdq), (dk, hdk) = _new(q), _new(k)
+    D = q.shape[2]
+    dw = torch.empty((2, D), dtype=torch.float32, device=q.device)
+    at = dw.data_ptr()
+    _check(load().pv_qk_norm_rope_backward(p, _heads(dout_q, "dout_q", q), _heads(dout_k, "dout_k", k), hq, hk, hdq, hdk,
+                                           at, at + 4 * D, _stream(stream, q)), "pv_qk_norm_rope_backward")
     return dq, dk, dw[0], dw[1]
 
 
 def _attention_params(q, k, v, q_offsets, k_offsets, scale, cap, slopes, q_positions, k_positions, causal, prefix):
-    p = AttentionParams()
-    p.dtype = _dtype(q, "q", wide=False)
+    """The call's parameters, and the host arrays that they point to."""
     if v.shape != k.shape:
         raise ValueError("k and v must have one shape")
-    p.q_offsets, p.frames = _offsets(q_offsets, q.shape[0], "q_offsets")
-    p.k_offsets, n = _offsets(k_offsets, k.shape[0], "k_offsets")
-    if n != p.frames:
+    rows, H, D = q.shape
+    keys, Hk, _ = k.shape
+    qo, frames = _offsets(q_offsets, rows, "q_offsets")
+    ko, n = _offsets(k_offsets, keys, "k_offsets")
+    if n != frames:
         raise ValueError("q_offsets and k_offsets must hold the same frames")
-    p.q_heads, p.k_heads, p.head_dim = q.shape[1], k.shape[1], q.shape[2]
-    if k.shape[1] < 1 or q.shape[1] % k.shape[1]:
+    if Hk < 1 or H % Hk:
         raise ValueError("the heads of q must be a multiple of those of k")
-    p.scale = q.shape[2] ** -0.5 if scale is None else scale
-    p.cap = cap
+    p = AttentionParams(frames, qo.buffer_info()[0], ko.buffer_info()[0], H, Hk, D, _dtype(q, "q", wide=False),
+                        D ** -0.5 if scale is None else scale, cap)
     if slopes is not None:
         if q_positions is None or k_positions is None:
             raise ValueError("slopes need q_positions and k_positions")
-        p.slopes = _floats(slopes, (q.shape[1],), q.device, "slopes")
-        p.q_positions, p.q_position_stride, p.axes = _positions(q_positions, q.shape[0], q.device, "q_positions")
-        p.k_positions, p.k_position_stride, axes = _positions(k_positions, k.shape[0], q.device, "k_positions")
+        dev = q.get_device()
+        p.slopes = _floats(slopes, (H,), dev, "slopes")
+        p.q_positions, p.q_position_stride, p.axes = _positions(q_positions, rows, dev, "q_positions")
+        p.k_positions, p.k_position_stride, axes = _positions(k_positions, keys, dev, "k_positions")
         if axes != p.axes:
             raise ValueError("q_positions and k_positions must have the same axes")
-    p.causal = bool(causal)
+    pre = None
+    if causal:
+        p.causal = 1
     if prefix is not None:
         if not causal:
             raise ValueError("prefix is for causal attention")
-        if len(prefix) != p.frames:
+        if len(prefix) != frames:
             raise ValueError("prefix must hold one length per frame")
-        p.prefix = (ctypes.c_int64 * p.frames)(*prefix)
-    return p
+        pre = array.array("q", prefix)
+        p.prefix = pre.buffer_info()[0]
+    return p, (qo, ko, pre)
 
 
 def attention(q, k, v, q_offsets, k_offsets, scale: Optional[float] = None, cap: float = 0.0, slopes=None,
@@ -208,14 +222,17 @@ def attention(q, k, v, q_offsets, k_offsets, scale: Optional[float] = None, cap:
     gives 0.  Returns out [queries, H, D], with ``return_lse`` also the float32
     [H, queries] logarithms of the softmax sums for :func:`attention_backward`.
     """
-    torch = _torch()
     hq, hk, hv = _heads(q, "q"), _heads(k, "k", q, 1), _heads(v, "v", k)
-    p = _attention_params(q, k, v, q_offsets, k_offsets, scale, cap, slopes, q_positions, k_positions, causal, prefix)
-    o = out if out is not None else torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device) if return_lse else None
-    _check(load().pv_attention(p, hq, hk, hv, _heads(o, "out", q), lse.data_ptr() if return_lse else None,
-                               _stream(stream, q.device)), "pv_attention")
-    return (o, lse) if return_lse else o
+    p, _alive = _attention_params(q, k, v, q_offsets, k_offsets, scale, cap, slopes, q_positions, k_positions, causal,
+                                  prefix)
+    o, ho = _new(q) if out is None else (out, _heads(out, "out", q))
+    if not return_lse:
+        _check(load().pv_attention(p, hq, hk, hv, ho, None, _stream(stream, q)), "pv_attention")
+        return o
+    torch = _torch()
+    lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
+    _check(load().pv_attention(p, hq, hk, hv, ho, lse.data_ptr(), _stream(stream, q)), "pv_attention")
+    return o, lse
 
 
 def attention_backward(dout, q, k, v, out, lse, q_offsets, k_offsets, scale: Optional[float] = None, cap: float = 0.0,
@@ -223,42 +240,47 @@ def attention_backward(dout, q, k, v, out, lse, q_offsets, k_offsets, scale: Opt
                        stream=None):
     """Gradients (dq, dk, dv) of :func:`attention` from that of its output,
     its inputs, ``out`` and ``lse``; the other arguments as there."""
-    torch = _torch()
     hq, hk, hv = _heads(q, "q"), _heads(k, "k", q, 1), _heads(v, "v", k)
-    p = _attention_params(q, k, v, q_offsets, k_offsets, scale, cap, slopes, q_positions, k_positions, causal, prefix)
-    dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    dk = torch.empty(k.shape, dtype=q.dtype, device=q.device)
-    dv = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+    p, _alive = _attention_params(q, k, v, q_offsets, k_offsets, scale, cap, slopes, q_positions, k_positions, causal,
+                                  prefix)
+    (dq, hdq), (dk, hdk), (dv, hdv) = _new(q), _new(k), _new(k)
     _check(load().pv_attention_backward(
         p, _heads(dout, "dout", q), hq, hk, hv, _heads(out, "out", q),
-        _floats(lse, (q.shape[1], q.shape[0]), q.device, "lse"), _heads(dq, "dq"), _heads(dk, "dk"), _heads(dv, "dv"),
-        _stream(stream, q.device)), "pv_attention_backward")
+        _floats(lse, (q.shape[1], q.shape[0]), q.get_device(), "lse"), hdq, hdk, hdv, _stream(stream, q)),
+        "pv_attention_backward")
     return dq, dk, dv
 
 
 def _rows(t, name: str, like=None):
     """[rows, channels], rows strided as they come, channels dense."""
-    if t.dim() != 2 or not t.is_cuda:
+    shape = t.shape
+    if len(shape) != 2 or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor of shape [rows, channels]")
     if like is not None:
-        if t.dtype != like.dtype or t.device != like.device:
+        if t.dtype is not like.dtype or t.get_device() != like.get_device():
             raise TypeError(f"{name} must have the dtype and device of x")
-        if t.shape != like.shape:
+        if shape != like.shape:
             raise ValueError(f"{name} must have the shape of x")
-    if t.shape[1] < 1 or (t.shape[1] > 1 and t.stride(1) != 1):
+    row, one = t.stride()
+    if shape[1] < 1 or (shape[1] > 1 and one != 1):
         raise ValueError(f"{name}: the channels of a row must be dense")
-    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else t.shape[1])
+    return t.data_ptr(), (row if shape[0] > 1 else shape[1])
 
 
 def _scan_params(x, gate, offsets, reverse):
-    p = ScanParams()
-    p.x, p.x_stride = _rows(x, "x")
-    p.gate, p.gate_stride = _rows(gate, "gate", x)
-    p.dtype = _dtype(x, "x")
-    p.offsets, p.frames = _offsets(offsets, x.shape[0], "offsets")
-    p.channels = x.shape[1]
-    p.reverse = bool(reverse)
-    return p
+    """The call's parameters, and the host array that they point to."""
+    xp, xs = _rows(x, "x")
+    gp, gs = _rows(gate, "gate", x)
+    code = _dtype(x, "x")
+    off, frames = _offsets(offsets, x.shape[0], "offsets")
+    return ScanParams(frames, off.buffer_info()[0], x.shape[1], code, 1 if reverse else 0, xp, xs, gp, gs), off
+
+
+def _states(lib, p) -> int:
+    n = lib.pv_gated_scan_states(p)
+    if n < 0:
+        raise PVError(int(n), "pv_gated_scan_states")
+    return n
 
 
 def gated_scan(x, gate, offsets, h0=None, reverse: bool = False, return_states: bool = False, out=None, stream=None):
@@ -274,37 +296,35 @@ def gated_scan(x, gate, offsets, h0=None, reverse: bool = False, return_states: 
     starts from.
     """
     torch = _torch()
-    p = _scan_params(x, gate, offsets, reverse)
+    p, _alive = _scan_params(x, gate, offsets, reverse)
     C = x.shape[1]
-    h = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    last = torch.empty((p.frames, C), dtype=torch.float32, device=x.device)
+    state = (p.frames, C)
     lib = load()
-    states = None
-    if return_states:
-        n = lib.pv_gated_scan_states(p)
-        if n < 0:
-            raise PVError(int(n), "pv_gated_scan_states")
-        states = torch.empty((n, C), dtype=torch.float32, device=x.device)
-    _check(lib.pv_gated_scan(p, None if h0 is None else _floats(h0, (p.frames, C), x.device, "h0"),
-                             *_rows(h, "out", x), last.data_ptr(), states.data_ptr() if return_states else None,
-                             _stream(stream, x.device)), "pv_gated_scan")
-    return (h, last, states) if return_states else (h, last)
+    if out is None:
+        out = _dense(x)
+        h, hs = out.data_ptr(), C
+    else:
+        h, hs = _rows(out, "out", x)
+    last = torch.empty(state, dtype=torch.float32, device=x.device)
+    states = torch.empty((_states(lib, p), C), dtype=torch.float32, device=x.device) if return_states else None
+    _check(lib.pv_gated_scan(p, None if h0 is None else _floats(h0, state, x.get_device(), "h0"), h, hs, last.data_ptr(),
+                             states.data_ptr() if return_states else None, _stream(stream, x)), "pv_gated_scan")
+    return (out, last, states) if return_states else (out, last)
 
 
 def gated_scan_backward(dh, dlast, x, gate, states, offsets, reverse: bool = False, stream=None):
     """Gradients (dx, dgate, dh0) of :func:`gated_scan` from those of h and of
     the last states (``dlast`` None: zeros), its inputs and its ``states``."""
+    p, _alive = _scan_params(x, gate, offsets, reverse)
+    C, dev = x.shape[1], x.get_device()
+    state = (p.frames, C)
+    lib = load()
+    dhp, dhs = _rows(dh, "dh", x)
+    dx, dgate = _dense(x), _dense(x)
     torch = _torch()
-    p = _scan_params(x, gate, offsets, reverse)
-    C = x.shape[1]
-    n = load().pv_gated_scan_states(p)
-    if n < 0:
-        raise PVError(int(n), "pv_gated_scan_states")
-    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    dgate = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    dh0 = torch.empty((p.frames, C), dtype=torch.float32, device=x.device)
-    _check(load().pv_gated_scan_backward(
-        p, *_rows(dh, "dh", x), None if dlast is None else _floats(dlast, (p.frames, C), x.device, "dlast"),
-        _floats(states, (n, C), x.device, "states"), *_rows(dx, "dx"), *_rows(dgate, "dgate"), dh0.data_ptr(),
-        _stream(stream, x.device)), "pv_gated_scan_backward")
+    dh0 = torch.empty(state, dtype=torch.float32, device=x.device)
+    _check(lib.pv_gated_scan_backward(
+        p, dhp, dhs, None if dlast is None else _floats(dlast, state, dev, "dlast"),
+        _floats(states, (_states(lib, p), C), dev, "states"), dx.data_ptr(), C, dgate.data_ptr(), C, dh0.data_ptr(),
+        _stream(stream, x)), "pv_gated_scan_backward")
     return dx, dgate, dh0
