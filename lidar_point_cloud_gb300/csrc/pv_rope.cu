@@ -47,9 +47,29 @@ struct RopeArgs {
   float* dwk;
 };
 
+// A pair weighted and turned.
+__device__ __forceinline__ void turn(float& x0, float& x1, float w0, float w1, float c, float s) {
+  const float n0 = x0 * w0, n1 = x1 * w1;
+  x0 = fmaf(n0, c, -(n1 * s));
+  x1 = fmaf(n1, c, n0 * s);
+}
+
 __device__ __forceinline__ float group_sum(float v, int lanes) {
   for (int o = lanes >> 1; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
+}
+
+// Cosine and sine of an angle in radians.  It is brought to turns first, in two
+// 32-bit parts of 1 / (2 pi) (the fused product makes the first part's rounding
+// known), so that whole turns drop out exactly; then CUDA's sincospif.
+__device__ __forceinline__ float2 cos_sin(float angle) {
+  constexpr double kTurn = 0.15915494309189533577;  // 1 / (2 pi)
+  constexpr float kHigh = static_cast<float>(kTurn), kLow = static_cast<float>(kTurn - static_cast<double>(kHigh));
+  const float t = angle * kHigh;
+  const float rest = fmaf(angle, kLow, fmaf(angle, kHigh, -t));
+  float2 c;
+  sincospif(2.0f * ((t - rintf(t)) + rest), &c.y, &c.x);
+  return c;
 }
 
 // Cosines and sines of the tile's tokens, [token][pair].
@@ -58,9 +78,7 @@ __device__ __forceinline__ void fill_table(const RopeArgs& a, int t0, int tokens
   for (int i = threadIdx.x; i < tokens * half; i += kThreads) {
     const int t = i / half, p = i - t * half;
     const float at = static_cast<float>(a.pos[static_cast<long long>(t0 + t) * a.pos_stride + p % a.axes]);
-    float s, c;
-    sincosf(at * a.freq[p], &s, &c);
-    table[i] = make_float2(c, s);
+    table[i] = cos_sin(at * a.freq[p]);
   }
 }
 
@@ -78,38 +96,56 @@ __global__ void __launch_bounds__(kThreads) pv_rope_kernel(const RopeArgs a) {
   wait_prior_grid();
   const int t0 = blockIdx.x * a.tile;
   const int tokens = min(a.tile, a.rows - t0);
+  __shared__ __align__(16) float weight[2 * 256];
+  for (int i = threadIdx.x; i < a.D; i += kThreads) {
+    weight[i] = a.wq[i];
+    weight[256 + i] = a.hk ? a.wk[i] : 0.0f;
+  }
   fill_table(a, t0, tokens, table);
-  __syncthreads();
+  const int step_t = groups / heads, step_h = groups - step_t * heads;
+  int t = group / heads, h = group - t * heads;
+  // A row is loaded one round ahead of its arithmetic.
+  uint4 next0 = {}, next1 = {};
+  auto fetch = [&](int t, int h) {
+    if (!on || t >= tokens) return;
+    const View& in = h < a.hq ? a.q : a.k;
+    const char* p = in.data + (t0 + t) * in.row + (h < a.hq ? h : h - a.hq) * in.head + sub * 16;
+    next0 = *reinterpret_cast<const uint4*>(p);
+    next1 = *reinterpret_cast<const uint4*>(p + half * sizeof(T));
+  };
+  fetch(t, h);
+  __syncthreads();  // the table
   for (int r0 = 0; r0 < tokens * heads; r0 += groups) {
-    const int r = r0 + group;
-    const bool live = on && r < tokens * heads;
-    const int t = r / heads, h = r - t * heads;
+    const uint4 raw0 = next0, raw1 = next1;
+    const int t_now = t, h_now = h;
+    t += step_t;
+    h += step_h;
+    if (h >= heads) h -= heads, ++t;
+    fetch(t, h);
+    const bool live = on && t_now < tokens;
     float x[2 * V];
-    const bool isq = h < a.hq;
-    const View& in = isq ? a.q : a.k;
-    const View& out = isq ? a.oq : a.ok;
-    const int hh = isq ? h : h - a.hq;
+    Pack<T>::open(raw0, x);
+    Pack<T>::open(raw1, x + V);
     float ss = 0.0f;
-    if (live) {
-      const char* p = in.data + (t0 + t) * in.row + hh * in.head + sub * 16;
-      Pack<T>::load(p, x);
-      Pack<T>::load(p + half * sizeof(T), x + V);
 #pragma unroll
-      for (int i = 0; i < 2 * V; ++i) ss = fmaf(x[i], x[i], ss);
-    }
-    ss = group_sum(ss, lanes);
+    for (int i = 0; i < 2 * V; ++i) ss = fmaf(x[i], x[i], ss);
+    ss = group_sum(on ? ss : 0.0f, lanes);
     if (live) {
+      const bool isq = h_now < a.hq;
       const float rs = rsqrtf(fmaf(ss, inv, a.eps));
-      const float* w = (isq ? a.wq : a.wk) + sub * V;
-      const float2* cs = table + t * half + sub * V;
+      const float* w = weight + (isq ? 0 : 256) + sub * V;
+      const float4* cs = reinterpret_cast<const float4*>(table + t_now * half + sub * V);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float n0 = x[i] * rs * w[i], n1 = x[V + i] * rs * w[half + i];
-        const float2 c = cs[i];
-        x[i] = fmaf(n0, c.x, -(n1 * c.y));
-        x[V + i] = fmaf(n1, c.x, n0 * c.y);
+      for (int i = 0; i < V; i += 4) {
+        const float4 w0 = *reinterpret_cast<const float4*>(w + i), w1 = *reinterpret_cast<const float4*>(w + half + i);
+        const float4 c0 = cs[i / 2], c1 = cs[i / 2 + 1];
+        turn(x[i], x[V + i], rs * w0.x, rs * w1.x, c0.x, c0.y);
+        turn(x[i + 1], x[V + i + 1], rs * w0.y, rs * w1.y, c0.z, c0.w);
+        turn(x[i + 2], x[V + i + 2], rs * w0.z, rs * w1.z, c1.x, c1.y);
+        turn(x[i + 3], x[V + i + 3], rs * w0.w, rs * w1.w, c1.z, c1.w);
       }
-      char* p = out.data + (t0 + t) * out.row + hh * out.head + sub * 16;
+      const View& out = isq ? a.oq : a.ok;
+      char* p = out.data + (t0 + t_now) * out.row + (isq ? h_now : h_now - a.hq) * out.head + sub * 16;
       Pack<T>::store(p, x);
       Pack<T>::store(p + half * sizeof(T), x + V);
     }
@@ -123,7 +159,7 @@ __global__ void __launch_bounds__(kThreads) pv_rope_kernel(const RopeArgs a) {
 // a block's lanes are joined in shared memory, the blocks by the last one to
 // finish, both in a fixed order.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) pv_rope_backward_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) pv_rope_backward_kernel(const RopeArgs a) {
   constexpr int V = Pack<T>::kN;
   __shared__ __align__(16) float2 table[kTableFloats / 2];
   __shared__ bool last;
@@ -150,32 +186,46 @@ __global__ void __launch_bounds__(kThreads) pv_rope_backward_kernel(const RopeAr
       w[V + i] = on ? wsrc[half + sub * V + i] : 0.0f;
       acc[i] = acc[V + i] = 0.0f;
     }
+    const int step_t = groups / heads, step_h = groups - step_t * heads;
     for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
       const int t0 = tile * a.tile;
       const int tokens = min(a.tile, a.rows - t0);
-      __syncthreads();
+      int t = group / heads, h = group - t * heads;
+      // A row is loaded one round ahead of its arithmetic.
+      uint4 next[4] = {};
+      auto fetch = [&](int t, int h) {
+        if (!on || t >= tokens) return;
+        const char* p = in.data + (t0 + t) * in.row + h * in.head + sub * 16;
+        const char* pg = gr.data + (t0 + t) * gr.row + h * gr.head + sub * 16;
+        next[0] = *reinterpret_cast<const uint4*>(p);
+        next[1] = *reinterpret_cast<const uint4*>(p + half * sizeof(T));
+        next[2] = *reinterpret_cast<const uint4*>(pg);
+        next[3] = *reinterpret_cast<const uint4*>(pg + half * sizeof(T));
+      };
+      fetch(t, h);
+      __syncthreads();  // the last tile's table is no longer read
       fill_table(a, t0, tokens, table);
       __syncthreads();
       for (int r0 = 0; r0 < tokens * heads; r0 += groups) {
-        const int r = r0 + group;
-        const bool live = on && r < tokens * heads;
-        const int t = r / heads, h = r - t * heads;
         float x[2 * V], g[2 * V];
+        Pack<T>::open(next[0], x);
+        Pack<T>::open(next[1], x + V);
+        Pack<T>::open(next[2], g);
+        Pack<T>::open(next[3], g + V);
+        const int t_now = t, h_now = h;
+        const bool live = on && t_now < tokens;
+        t += step_t;
+        h += step_h;
+        if (h >= heads) h -= heads, ++t;
+        fetch(t, h);
         float ss = 0.0f, dot = 0.0f;
         if (live) {
-          const char* p = in.data + (t0 + t) * in.row + h * in.head + sub * 16;
-          const char* pg = gr.data + (t0 + t) * gr.row + h * gr.head + sub * 16;
-          Pack<T>::load(p, x);
-          Pack<T>::load(p + half * sizeof(T), x + V);
-          Pack<T>::load(pg, g);
-          Pack<T>::load(pg + half * sizeof(T), g + V);
-          const float2* cs = table + t * half + sub * V;
+          const float4* cs = reinterpret_cast<const float4*>(table + t_now * half + sub * V);
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const float2 c = cs[i];
-            const float g0 = fmaf(g[i], c.x, g[V + i] * c.y), g1 = fmaf(g[V + i], c.x, -(g[i] * c.y));
-            g[i] = g0;
-            g[V + i] = g1;
+          for (int i = 0; i < V; i += 2) {
+            const float4 c = cs[i / 2];
+            turn(g[i], g[V + i], 1.0f, 1.0f, c.x, -c.y);
+            turn(g[i + 1], g[V + i + 1], 1.0f, 1.0f, c.z, -c.w);
           }
 #pragma unroll
           for (int i = 0; i < 2 * V; ++i) {
@@ -187,14 +237,13 @@ __global__ void __launch_bounds__(kThreads) pv_rope_backward_kernel(const RopeAr
         dot = group_sum(dot, lanes);
         if (live) {
           const float rs = rsqrtf(fmaf(ss, inv, a.eps));
-          const float m = dot * inv * rs * rs;  // mean(g w n) / |x| scale: n = x rs
+          const float m = dot * inv * rs * rs;  // mean(g w n) over n: n = x rs
 #pragma unroll
           for (int i = 0; i < 2 * V; ++i) {
-            const float n = x[i] * rs;
-            acc[i] = fmaf(g[i], n, acc[i]);
+            acc[i] = fmaf(g[i], x[i] * rs, acc[i]);
             x[i] = rs * fmaf(g[i], w[i], -(m * x[i]));
           }
-          char* p = out.data + (t0 + t) * out.row + h * out.head + sub * 16;
+          char* p = out.data + (t0 + t_now) * out.row + h_now * out.head + sub * 16;
           Pack<T>::store(p, x);
           Pack<T>::store(p + half * sizeof(T), x + V);
         }

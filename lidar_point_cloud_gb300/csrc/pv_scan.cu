@@ -3,8 +3,8 @@
 //   h[t] = a[t] h[t-1] + z[t] x[t],  z = sigmoid(gate), a = 1 - z.
 //
 // One pass over the data.  A frame is cut into tiles of steps (in reading
-// order); a block holds one tile of 32 * kVec channels or fewer, each thread
-// kSteps steps of its channels in registers.  The map of a stretch of steps,
+// order); a block holds one tile of 64 channels or fewer at a time, each thread
+// kSteps steps of its one or two channels.  The map of a stretch of steps,
 // h_out = A h_in + B, is composed thread by thread in shared memory, published
 // per tile, and the state before the tile found from the published maps; then
 // every thread runs its steps from its own start and writes them.
@@ -16,8 +16,14 @@
 // its group's base.  So a link of the chain along a frame is one group, and
 // results do not depend on timing.  A published value is one 64-bit word of
 // the value and this launch's epoch: readers poll the words themselves, there
-// are no flags to clear or fences to pay for.  Tiles are handed out by a
-// ticket in chain order, so a block only ever waits for blocks that run.
+// are no flags to clear or fences to pay for.  The launch is cooperative and a
+// block takes every gridDim-th tile of one list in which a tile comes after
+// those that it waits for: the earliest tile that is not done always belongs to
+// a block that runs and works on it.  The list goes round the frames (their
+// first tiles, their second ones, ...), so that with many frames what a tile waits for
+// was done a round ago.  While a tile's
+// arithmetic and its chain go on, the block's next tile is on its way into
+// shared memory, each thread copying what it will read itself.
 //
 // The backward pass walks the tiles the other way.  With c the gradient that
 // step t hands to t - 1, e[t] = dh[t] + c[t+1], c[t] = a[t] e[t]: the same
@@ -29,6 +35,8 @@
 #include "pv_seq.cuh"
 
 #include <algorithm>
+#include <atomic>
+#include <type_traits>
 
 namespace {
 
@@ -52,11 +60,12 @@ struct ScanArgs {
   float* states;        // forward: written (may be null); backward: read
   unsigned long long* maps;   // published: [tiles][A, B][channels]
   unsigned long long* bases;  // published: [groups][channels]
-  unsigned int* ctl;    // ticket, finished blocks, epoch
+  unsigned int* ctl;    // finished blocks, epoch
   int channels, slabs, lanes_log2, frames, tiles, reverse, steps;
   int row0[PV_MAX_FRAMES + 1];   // row offsets of the frames
   int tile0[PV_MAX_FRAMES + 1];  // first tile of each frame
   int group0[PV_MAX_FRAMES + 1]; // first group of each frame
+  unsigned char order[PV_MAX_FRAMES];  // the frames by their number of tiles, most first
 };
 
 __device__ __forceinline__ void put(unsigned long long* p, float v, unsigned int epoch) {
@@ -64,16 +73,23 @@ __device__ __forceinline__ void put(unsigned long long* p, float v, unsigned int
   asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(w) : "memory");
 }
 
-// A published value; NaN if it does not come within the limit.
-__device__ __forceinline__ float take(const unsigned long long* p, unsigned int epoch) {
-  unsigned long long w, until = 0;
-  for (;;) {
-    asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(w) : "l"(p) : "memory");
-    if (static_cast<unsigned int>(w >> 32) == epoch) return __uint_as_float(static_cast<unsigned int>(w));
+__device__ __forceinline__ unsigned long long peek(const unsigned long long* p) {
+  unsigned long long w;
+  asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(w) : "l"(p) : "memory");
+  return w;
+}
+
+// The published value at p, of which `w` was read a while ago; NaN if it does
+// not come within the limit.
+__device__ __forceinline__ float take(unsigned long long w, const unsigned long long* p, unsigned int epoch) {
+  unsigned long long until = 0;
+  while (static_cast<unsigned int>(w >> 32) != epoch) {
     const unsigned long long t = now_ns();
     if (!until) until = t + kWaitNs;
     if (t > until) return __int_as_float(0x7FFFFFFF);
+    w = peek(p);
   }
+  return __uint_as_float(static_cast<unsigned int>(w));
 }
 
 // 1 / (1 + exp(-v)): -inf gives 0, +inf 1.  For 16-bit gates the fast
@@ -81,7 +97,10 @@ __device__ __forceinline__ float take(const unsigned long long* p, unsigned int 
 // gate's own rounding.
 template <typename T>
 __device__ __forceinline__ float sigmoid(float v) {
-  return __fdividef(1.0f, 1.0f + __expf(-v));
+  float e, z;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(z) : "f"(1.0f + e));
+  return z;
 }
 template <>
 __device__ __forceinline__ float sigmoid<float>(float v) {
@@ -93,18 +112,21 @@ struct Lane;  // V neighbouring channels of one row
 template <>
 struct Lane<float, 1> {
   using Raw = float;
+  static __device__ __forceinline__ Raw closed() { return __uint_as_float(0xFF800000u); }  // a gate of -inf
   static __device__ __forceinline__ void open(Raw r, float* f) { f[0] = r; }
   static __device__ __forceinline__ Raw close(const float* f) { return f[0]; }
 };
 template <typename T>
 struct Lane<T, 1> {
   using Raw = T;
+  static __device__ __forceinline__ Raw closed() { return Pack<T>::one(__uint_as_float(0xFF800000u)); }
   static __device__ __forceinline__ void open(Raw r, float* f) { f[0] = Pack<T>::to(r); }
   static __device__ __forceinline__ Raw close(const float* f) { return Pack<T>::one(f[0]); }
 };
 template <>
 struct Lane<__nv_bfloat16, 2> {
   using Raw = uint32_t;
+  static __device__ __forceinline__ Raw closed() { return 0xFF80FF80u; }
   static __device__ __forceinline__ void open(Raw r, float* f) {
     f[0] = __uint_as_float(r << 16);
     f[1] = __uint_as_float(r & 0xFFFF0000u);
@@ -114,6 +136,7 @@ struct Lane<__nv_bfloat16, 2> {
 template <>
 struct Lane<__half, 2> {
   using Raw = uint32_t;
+  static __device__ __forceinline__ Raw closed() { return 0xFC00FC00u; }
   static __device__ __forceinline__ void open(Raw r, float* f) {
     const float2 d = __half22float2(*reinterpret_cast<const __half2*>(&r));
     f[0] = d.x;
@@ -122,99 +145,28 @@ struct Lane<__half, 2> {
   static __device__ __forceinline__ Raw close(const float* f) { return Pack<__half>::two(f[0], f[1]); }
 };
 
-struct Place {
-  int tile, frame, chan, seg, segs, step0, len, row_at;
-  long long dir;
-};
-
-// The state (or gradient) handed to tile `k` of its chain: base of its group,
-// then the maps of the tiles ahead of it in the group, in order.  Called by the
-// whole block; the result for channel c of the block is carry[c].
-// index(i) = place in `maps` of chain tile i of this frame.
-template <bool kBack>
-__device__ __forceinline__ void chain(const ScanArgs& a, int tile, int frame, int slab, unsigned int epoch, int width,
-                                      float A, float B, bool owner, int c_own, float* carry, float (*fetch)[2][kMaxSlab]) {
-  const int t0 = a.tile0[frame], n = a.tile0[frame + 1] - t0;
-  const int k = kBack ? n - 1 - (tile - t0) : tile - t0;  // place along the chain
-  const int g = k / kGroup, ahead = k - g * kGroup;
-  const long long C = a.channels;
-  const int c0 = slab * width;
-  auto at = [&](int i) { return static_cast<long long>(kBack ? t0 + n - 1 - i : t0 + i); };
-  if (owner) {  // this tile's own map
-    put(a.maps + (at(k) * 2) * C + c0 + c_own, A, epoch);
-    put(a.maps + (at(k) * 2 + 1) * C + c0 + c_own, B, epoch);
+// Copies one word that only this thread reads back.  16-bit words, which the
+// asynchronous copy does not take, go through a register.
+template <typename Raw>
+__device__ __forceinline__ void stage(Raw* to, const Raw* from) {
+  if constexpr (sizeof(Raw) == 4) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(to))), "l"(from)
+                 : "memory");
+  } else {
+    *to = __ldcs(from);
   }
-  // All polls at once: every thread one (tile, channel) at a time.
-  for (int i = threadIdx.x; i < ahead * width; i += kThreads) {
-    const int j = i / width, c = i - j * width;
-    if (c0 + c < C) {
-      fetch[j][0][c] = take(a.maps + (at(g * kGroup + j) * 2) * C + c0 + c, epoch);
-      fetch[j][1][c] = take(a.maps + (at(g * kGroup + j) * 2 + 1) * C + c0 + c, epoch);
-    }
-  }
-  __syncthreads();
-  if (owner) {
-    float s;
-    // The maps ahead are joined before the base is waited for: a link of the
-    // chain is one multiply-add.
-    float GA = 1.0f, GB = 0.0f;
-    for (int j = 0; j < ahead; ++j) {
-      GB = fmaf(fetch[j][0][c_own], GB, fetch[j][1][c_own]);
-      GA *= fetch[j][0][c_own];
-    }
-    if (g == 0)
-      s = a.first ? a.first[frame * C + c0 + c_own] : 0.0f;
-    else
-      s = take(a.bases + (a.group0[frame] + g) * C + c0 + c_own, epoch);
-    s = fmaf(GA, s, GB);
-    carry[c_own] = s;
-    const float after = fmaf(A, s, B);
-    if (k == n - 1) {
-      if (a.last) a.last[frame * C + c0 + c_own] = after;
-    } else if (ahead == kGroup - 1) {
-      put(a.bases + (a.group0[frame] + g + 1) * C + c0 + c_own, after, epoch);
-    }
-    if (!kBack && a.states) a.states[static_cast<long long>(tile) * C + c0 + c_own] = s;
-  }
-  __syncthreads();
 }
+__device__ __forceinline__ void stage_close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All groups but the last one are there.
+__device__ __forceinline__ void stage_wait() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
 
-// The next tile of this launch, and the frame it belongs to.
-template <bool kBack>
-__device__ __forceinline__ void claim(const ScanArgs& a, int* tile, int* slab, int* frame, unsigned int* epoch) {
-  __shared__ int s[3];
-  __shared__ unsigned int e;
-  if (threadIdx.x == 0) {
-    const int ticket = static_cast<int>(atomicAdd(a.ctl, 1u));
-    const int t = kBack ? a.tiles - 1 - ticket / a.slabs : ticket / a.slabs;
-    int lo = 0, hi = a.frames - 1;  // the last frame whose first tile is not past t
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (a.tile0[mid] <= t)
-        lo = mid;
-      else
-        hi = mid - 1;
-    }
-    s[0] = t;
-    s[1] = ticket % a.slabs;
-    s[2] = lo;
-    e = *reinterpret_cast<volatile unsigned int*>(a.ctl + 2) + 1u;
-  }
-  __syncthreads();
-  *tile = s[0];
-  *slab = s[1];
-  *frame = s[2];
-  *epoch = e;
-}
-
-// The last block of a launch leaves the counters as it found them, the epoch one on.
+// The last block of a launch leaves the counter as it found it, the epoch one on.
 __device__ __forceinline__ void leave(const ScanArgs& a) {
   if (threadIdx.x == 0) {
     __threadfence();
-    if (atomicAdd(a.ctl + 1, 1u) == gridDim.x - 1) {
+    if (atomicAdd(a.ctl, 1u) == gridDim.x - 1) {
       a.ctl[0] = 0;
-      a.ctl[1] = 0;
-      a.ctl[2] += 1u;
+      a.ctl[1] += 1u;
     }
   }
 }
@@ -233,172 +185,313 @@ template <typename T, int V, bool kBack>
 __global__ void __launch_bounds__(kThreads, 2) pv_scan_kernel(const __grid_constant__ ScanArgs a) {
   using L = Lane<T, V>;
   using Raw = typename L::Raw;
-  extern __shared__ float dyn[];  // maps of the threads: [segs][A, B(, backward B)][width]
+  constexpr int kIn = kBack ? 3 : 2;    // tensors read
+  constexpr int kRows = kBack ? 3 : 2;  // of a thread's maps: A, B (, the gradient's B)
+  // Two stages of every thread's words, [stage][tensor][step][thread], then the
+  // threads' maps, [segment][row][channel].
+  extern __shared__ __align__(16) unsigned char dyn[];
+  Raw* const words = reinterpret_cast<Raw*>(dyn) + threadIdx.x;
+  float* const all = reinterpret_cast<float*>(dyn + sizeof(Raw) * 2 * kIn * kSteps * kThreads);
   __shared__ float carry[kMaxSlab];
   __shared__ float fetch[kGroup][2][kMaxSlab];
   wait_prior_grid();
   empty_frames(a);
-  if (a.tiles == 0) {
-    allow_next_grid();
-    return;
-  }
-  int tile, slab, frame;
-  unsigned int epoch;
-  claim<kBack>(a, &tile, &slab, &frame, &epoch);
+  const unsigned int epoch = *reinterpret_cast<volatile unsigned int*>(a.ctl + 1) + 1u;
   const int lanes = 1 << a.lanes_log2;
-  const int width = lanes * V;
+  const int width_log2 = a.lanes_log2 + (V - 1);
+  const int width = 1 << width_log2;
   const int cl = threadIdx.x & (lanes - 1);
   const int seg = threadIdx.x >> a.lanes_log2, segs = kThreads >> a.lanes_log2;
   const int C = a.channels;
-  const int ch = slab * width + cl * V;
-  const int r0 = a.row0[frame], len = a.row0[frame + 1] - r0;
-  const int i0 = (tile - a.tile0[frame]) * a.steps + seg * kSteps;  // first step of this thread
-  const int n = ch < C ? min(kSteps, len - i0) : 0;                 // its steps (may be negative)
-  const long long first_row = a.reverse ? r0 + len - 1 - i0 : r0 + i0;
   const long long dir = a.reverse ? -1 : 1;
+  const int total = a.tiles * a.slabs;
 
-  Raw rx[kSteps], rg[kSteps], rd[kSteps];
-  {
-    const T* px = static_cast<const T*>(a.x) + first_row * a.xs + ch;
-    const T* pg = static_cast<const T*>(a.gate) + first_row * a.gs + ch;
-    const T* pd = static_cast<const T*>(a.dh) + first_row * a.ds + ch;
+  struct Tile {
+    int tile, frame, slab, ch, n;  // n: steps of this thread (may be negative)
+    long long row;                 // row of its first step
+  };
+  // Place i of the list, for rising i: round `round` starts at place `before` and
+  // has the `count` frames of `order` that have that many tiles.
+  int round = 0, before = 0, count = a.frames;
+  auto tiles_in = [&](int f) { return a.tile0[f + 1] - a.tile0[f]; };
+  auto shrink = [&]() {
+    while (count > 0 && tiles_in(a.order[count - 1]) <= round) --count;
+  };
+  shrink();
+  auto tile_at = [&](int i) {
+    Tile t;
+    const int place = i / a.slabs;
+    t.slab = i - place * a.slabs;
+    while (place >= before + count) {
+      before += count;
+      ++round;
+      shrink();
+    }
+    t.frame = a.order[place - before];
+    t.tile = kBack ? a.tile0[t.frame + 1] - 1 - round : a.tile0[t.frame] + round;
+    const int r0 = a.row0[t.frame], len = a.row0[t.frame + 1] - r0;
+    const int i0 = (t.tile - a.tile0[t.frame]) * a.steps + seg * kSteps;
+    t.ch = t.slab * width + cl * V;
+    t.n = t.ch < C ? min(kSteps, len - i0) : 0;
+    t.row = a.reverse ? r0 + len - 1 - i0 : r0 + i0;
+    return t;
+  };
+  auto load = [&](const Tile& t, int at) {
+    Raw* to = words + at * (kIn * kSteps * kThreads);
+    const Raw* px = reinterpret_cast<const Raw*>(static_cast<const T*>(a.x) + t.row * a.xs + t.ch);
+    const Raw* pg = reinterpret_cast<const Raw*>(static_cast<const T*>(a.gate) + t.row * a.gs + t.ch);
+    const Raw* pd = reinterpret_cast<const Raw*>(static_cast<const T*>(a.dh) + t.row * a.ds + t.ch);
+    const long long sx = dir * a.xs / V, sg = dir * a.gs / V, sd = dir * a.ds / V;
+    if (__all_sync(0xFFFFFFFFu, t.n == kSteps)) {
+#pragma unroll
+      for (int j = 0; j < kSteps; ++j, px += sx, pg += sg, pd += sd) {
+        stage(to + j * kThreads, px);
+        stage(to + (kSteps + j) * kThreads, pg);
+        if (kBack) stage(to + (2 * kSteps + j) * kThreads, pd);
+      }
+    } else {
+      // Steps past the frame's end, and channels past the last, are steps with a
+      // closed gate and nothing to read: they leave the state alone.
+      const float zero[V] = {};
+#pragma unroll 4
+      for (int j = 0; j < kSteps; ++j, px += sx, pg += sg, pd += sd) {
+        if (j < t.n) {
+          stage(to + j * kThreads, px);
+          stage(to + (kSteps + j) * kThreads, pg);
+          if (kBack) stage(to + (2 * kSteps + j) * kThreads, pd);
+        } else {
+          to[j * kThreads] = L::close(zero);
+          to[(kSteps + j) * kThreads] = L::closed();
+          if (kBack) to[(2 * kSteps + j) * kThreads] = L::close(zero);
+        }
+      }
+    }
+  };
+
+  int at = 0;
+  Tile next{};
+  if (static_cast<int>(blockIdx.x) < total) {
+    next = tile_at(blockIdx.x);
+    load(next, 0);
+  }
+  stage_close();
+  for (int i = blockIdx.x; i < total; i += gridDim.x, at ^= 1) {
+    const Tile now = next;
+    if (i + static_cast<int>(gridDim.x) < total) {
+      next = tile_at(i + gridDim.x);
+      load(next, at ^ 1);
+    }
+    stage_close();
+    // Where the tile stands in its frame's chain, and the published words that it
+    // will need: read now, looked at (and if need be awaited) after its own maps.
+    const int t0 = a.tile0[now.frame], nt = a.tile0[now.frame + 1] - t0;
+    const int place = kBack ? nt - 1 - (now.tile - t0) : now.tile - t0;
+    const int group = place / kGroup, ahead = place - group * kGroup;
+    const int c0 = now.slab * width, own = c0 + threadIdx.x;
+    const bool owner = threadIdx.x < width && own < C;
+    auto map_at = [&](int k) {  // of the chain's tile k: A, then B, of channel 0
+      return a.maps + static_cast<long long>(kBack ? t0 + nt - 1 - k : t0 + k) * 2 * C;
+    };
+    // A thread takes channel c of the tiles j0, j0 + j_step, ... ahead.
+    constexpr int kTurns = kGroup * 32 * V / kThreads;
+    const int c = threadIdx.x & (width - 1), j0 = threadIdx.x >> width_log2, j_step = kThreads >> width_log2;
+    const int wanted = c0 + c < C ? ahead : 0;
+    const unsigned long long* const ahead_at = map_at(group * kGroup + j0) + c0 + c;
+    const long long ahead_step = static_cast<long long>(kBack ? -2 : 2) * C * j_step;
+    unsigned long long early[kTurns][2];
+#pragma unroll
+    for (int q = 0; q < kTurns; ++q) {
+      if (j0 + q * j_step < wanted) {
+        early[q][0] = peek(ahead_at + q * ahead_step);
+        early[q][1] = peek(ahead_at + q * ahead_step + C);
+      }
+    }
+    const unsigned long long* base_at = a.bases + static_cast<long long>(a.group0[now.frame] + group) * C + own;
+    unsigned long long base_word = 0;
+    float start = 0.0f, state = 0.0f;  // group 0's base; backward: the state before the tile
+    if (owner) {
+      if (group)
+        base_word = peek(base_at);
+      else if (a.first)
+        start = a.first[static_cast<long long>(now.frame) * C + own];
+      if (kBack) state = a.states[static_cast<long long>(now.tile) * C + own];
+    }
+    stage_wait();
+    const Raw* in = words + at * (kIn * kSteps * kThreads);
+    auto word = [&](int tensor, int j, float* f) { L::open(in[(tensor * kSteps + j) * kThreads], f); };
+    float z[kSteps][V];
 #pragma unroll
     for (int j = 0; j < kSteps; ++j) {
-      if (j < n) {
-        rx[j] = __ldcs(reinterpret_cast<const Raw*>(px + j * dir * a.xs));
-        rg[j] = __ldcs(reinterpret_cast<const Raw*>(pg + j * dir * a.gs));
-        if (kBack) rd[j] = __ldcs(reinterpret_cast<const Raw*>(pd + j * dir * a.ds));
-      }
+      word(1, j, z[j]);
+#pragma unroll
+      for (int v = 0; v < V; ++v) z[j][v] = sigmoid<T>(z[j][v]);
     }
-  }
-  float z[kSteps][V];
-  float A[V], B[V], Cb[V];
+    // (1 - z) v is v - z v: one multiply-add, exact at both ends of z.
+    float A[V], B[V], Cb[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = 0.0f, Cb[v] = 0.0f;
+    for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = 0.0f, Cb[v] = 0.0f;
 #pragma unroll
-  for (int j = 0; j < kSteps; ++j) {
-    float g[V], x[V];
-    if (j < n) {
-      L::open(rg[j], g);
-      L::open(rx[j], x);
+    for (int j = 0; j < kSteps; ++j) {
+      float x[V];
+      word(0, j, x);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        z[j][v] = sigmoid<T>(g[v]);
-        const float keep = 1.0f - z[j][v];
-        A[v] *= keep;
-        B[v] = fmaf(keep, B[v], z[j][v] * x[v]);
+        A[v] = fmaf(-z[j][v], A[v], A[v]);
+        B[v] = fmaf(z[j][v], x[v], fmaf(-z[j][v], B[v], B[v]));
       }
-    } else {
-#pragma unroll
-      for (int v = 0; v < V; ++v) z[j][v] = 0.0f;
     }
-  }
-  if (kBack) {
+    if (kBack) {
 #pragma unroll
-    for (int j = kSteps - 1; j >= 0; --j) {
-      if (j < n) {
+      for (int j = kSteps - 1; j >= 0; --j) {
         float d[V];
-        L::open(rd[j], d);
+        word(2, j, d);
 #pragma unroll
-        for (int v = 0; v < V; ++v) Cb[v] = (1.0f - z[j][v]) * (d[v] + Cb[v]);
+        for (int v = 0; v < V; ++v) {
+          const float e = d[v] + Cb[v];
+          Cb[v] = fmaf(-z[j][v], e, e);
+        }
       }
     }
-  }
-  constexpr int kRows = kBack ? 3 : 2;
-  float* mine = dyn + seg * kRows * width + cl * V;
+    float* const mine = all + seg * kRows * width + cl * V;
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    mine[v] = A[v];
-    mine[width + v] = B[v];
-    if (kBack) mine[2 * width + v] = Cb[v];
-  }
-  __syncthreads();
-  // One thread per channel joins the threads' maps; each map is replaced by
-  // the map of everything ahead of it in the tile (backward also: behind it).
-  const bool owner = threadIdx.x < width && slab * width + threadIdx.x < C;
-  float TA = 1.0f, TB = 0.0f;
-  if (owner) {
-    float* p = dyn + threadIdx.x;
-    if (!kBack) {
-      for (int s = 0; s < segs; ++s, p += kRows * width) {
-        const float sa = p[0], sb = p[width];
-        p[0] = TA;
-        p[width] = TB;
-        TB = fmaf(sa, TB, sb);
-        TA *= sa;
-      }
-    } else {
-      // Forward along the tile from the state that the forward pass left, and
-      // the gradient's map backward.
-      float h = a.states[static_cast<long long>(tile) * C + slab * width + threadIdx.x];
-      float* pe = p + (segs - 1) * kRows * width;
-      for (int s = 0; s < segs; ++s, p += kRows * width) {
-        const float sb = p[width];
-        p[width] = h;
-        h = fmaf(p[0], h, sb);
-      }
-      for (int s = 0; s < segs; ++s, pe -= kRows * width) {
-        const float sa = pe[0], sc = pe[2 * width];
-        pe[0] = TA;
-        pe[2 * width] = TB;
-        TB = fmaf(sa, TB, sc);
-        TA *= sa;
+    for (int v = 0; v < V; ++v) {
+      mine[v] = A[v];
+      mine[width + v] = B[v];
+      if (kBack) mine[2 * width + v] = Cb[v];
+    }
+    __syncthreads();
+    // One thread per channel joins the threads' maps; each map is replaced by
+    // the map of everything ahead of it in the tile (backward: the state before
+    // it, and the map of everything behind it).
+    float TA = 1.0f, TB = 0.0f;
+    if (owner) {
+      float* p = all + threadIdx.x;
+      if (!kBack) {
+#pragma unroll 8
+        for (int s = 0; s < segs; ++s, p += kRows * width) {
+          const float sa = p[0], sb = p[width];
+          p[0] = TA;
+          p[width] = TB;
+          TB = fmaf(sa, TB, sb);
+          TA *= sa;
+        }
+      } else {
+        // Forward along the tile from the state that the forward pass left, and
+        // the gradient's map backward.
+        float h = state;
+        float* pe = p + (segs - 1) * kRows * width;
+#pragma unroll 8
+        for (int s = 0; s < segs; ++s, p += kRows * width) {
+          const float sb = p[width];
+          p[width] = h;
+          h = fmaf(p[0], h, sb);
+        }
+#pragma unroll 8
+        for (int s = 0; s < segs; ++s, pe -= kRows * width) {
+          const float sa = pe[0], sc = pe[2 * width];
+          pe[0] = TA;
+          pe[2 * width] = TB;
+          TB = fmaf(sa, TB, sc);
+          TA *= sa;
+        }
       }
     }
-  }
-  chain<kBack>(a, tile, frame, slab, epoch, width, TA, TB, owner, threadIdx.x, carry, fetch);
-  if (n > 0) {
+    if (owner) {
+      put(map_at(place) + own, TA, epoch);
+      put(map_at(place) + C + own, TB, epoch);
+    }
+#pragma unroll
+    for (int q = 0; q < kTurns; ++q) {
+      const int j = j0 + q * j_step;
+      if (j < wanted) {
+        fetch[j][0][c] = take(early[q][0], ahead_at + q * ahead_step, epoch);
+        fetch[j][1][c] = take(early[q][1], ahead_at + q * ahead_step + C, epoch);
+      }
+    }
+    __syncthreads();
+    if (owner) {
+      // The maps ahead are joined before the base is waited for: a link of the
+      // chain is one multiply-add.
+      float GA = 1.0f, GB = 0.0f;
+#pragma unroll 5
+      for (int j = 0; j < ahead; ++j) {
+        GB = fmaf(fetch[j][0][threadIdx.x], GB, fetch[j][1][threadIdx.x]);
+        GA *= fetch[j][0][threadIdx.x];
+      }
+      if (group) start = take(base_word, base_at, epoch);
+      const float s = fmaf(GA, start, GB), after = fmaf(TA, s, TB);
+      carry[threadIdx.x] = s;
+      if (place == nt - 1) {
+        if (a.last) a.last[static_cast<long long>(now.frame) * C + own] = after;
+      } else if (ahead == kGroup - 1) {
+        put(a.bases + static_cast<long long>(a.group0[now.frame] + group + 1) * C + own, after, epoch);
+      }
+      if (!kBack && a.states) a.states[static_cast<long long>(now.tile) * C + own] = s;
+    }
+    __syncthreads();
     float s[V];
-    T* po = static_cast<T*>(a.out) + first_row * a.os + ch;
     if (!kBack) {
 #pragma unroll
       for (int v = 0; v < V; ++v) s[v] = fmaf(mine[v], carry[cl * V + v], mine[width + v]);
+      Raw* po = reinterpret_cast<Raw*>(static_cast<T*>(a.out) + now.row * a.os + now.ch);
+      const long long so = dir * a.os / V;
+      auto run = [&](auto whole) {
 #pragma unroll
-      for (int j = 0; j < kSteps; ++j) {
-        if (j < n) {
+        for (int j = 0; j < kSteps; ++j, po += so) {
           float x[V];
-          L::open(rx[j], x);
+          word(0, j, x);
 #pragma unroll
-          for (int v = 0; v < V; ++v) s[v] = fmaf(1.0f - z[j][v], s[v], z[j][v] * x[v]);
-          __stcs(reinterpret_cast<Raw*>(po + j * dir * a.os), L::close(s));
+          for (int v = 0; v < V; ++v) s[v] = fmaf(z[j][v], x[v], fmaf(-z[j][v], s[v], s[v]));
+          if (decltype(whole)::value || j < now.n) __stcs(po, L::close(s));
         }
-      }
+      };
+      if (__all_sync(0xFFFFFFFFu, now.n == kSteps))
+        run(std::true_type{});
+      else
+        run(std::false_type{});
     } else {
-      T* pq = static_cast<T*>(a.out2) + first_row * a.os2 + ch;
       float diff[kSteps][V];  // x[t] - h[t-1]
 #pragma unroll
       for (int v = 0; v < V; ++v) s[v] = mine[width + v];
 #pragma unroll
       for (int j = 0; j < kSteps; ++j) {
-        if (j < n) {
-          float x[V];
-          L::open(rx[j], x);
+        float x[V];
+        word(0, j, x);
 #pragma unroll
-          for (int v = 0; v < V; ++v) {
-            diff[j][v] = x[v] - s[v];
-            s[v] = fmaf(1.0f - z[j][v], s[v], z[j][v] * x[v]);
-          }
+        for (int v = 0; v < V; ++v) {
+          diff[j][v] = x[v] - s[v];
+          s[v] = fmaf(z[j][v], x[v], fmaf(-z[j][v], s[v], s[v]));
         }
       }
 #pragma unroll
       for (int v = 0; v < V; ++v) s[v] = fmaf(mine[v], carry[cl * V + v], mine[2 * width + v]);
+      const long long so = dir * a.os / V, sq = dir * a.os2 / V;
+      Raw* po = reinterpret_cast<Raw*>(static_cast<T*>(a.out) + now.row * a.os + now.ch) + (kSteps - 1) * so;
+      Raw* pq = reinterpret_cast<Raw*>(static_cast<T*>(a.out2) + now.row * a.os2 + now.ch) + (kSteps - 1) * sq;
+      auto run = [&](auto whole) {
 #pragma unroll
-      for (int j = kSteps - 1; j >= 0; --j) {
-        if (j < n) {
+        for (int j = kSteps - 1; j >= 0; --j, po -= so, pq -= sq) {
           float d[V], gx[V], gg[V];
-          L::open(rd[j], d);
+          word(2, j, d);
 #pragma unroll
           for (int v = 0; v < V; ++v) {
-            const float e = d[v] + s[v], keep = 1.0f - z[j][v];
+            const float e = d[v] + s[v];
             gx[v] = e * z[j][v];
-            gg[v] = gx[v] * keep * diff[j][v];
-            s[v] = keep * e;
+            s[v] = fmaf(-z[j][v], e, e);
+            gg[v] = s[v] * z[j][v] * diff[j][v];  // e z (1 - z) (x - h)
           }
-          __stcs(reinterpret_cast<Raw*>(po + j * dir * a.os), L::close(gx));
-          __stcs(reinterpret_cast<Raw*>(pq + j * dir * a.os2), L::close(gg));
+          if (decltype(whole)::value || j < now.n) {
+            __stcs(po, L::close(gx));
+            __stcs(pq, L::close(gg));
+          }
         }
-      }
+      };
+      if (__all_sync(0xFFFFFFFFu, now.n == kSteps))
+        run(std::true_type{});
+      else
+        run(std::false_type{});
     }
+    __syncthreads();  // the maps and the carry are free for the next tile
   }
   leave(a);
   allow_next_grid();
@@ -442,20 +535,35 @@ int check_params(const pv_scan_params* p) {
 bool on_device(const void* p, size_t align, int dev) { return p && aligned(p, align) && device_of(p) == dev; }
 
 template <typename T, int V, bool kBack>
-int run(ScanArgs& a, const Shape& sh, pv_stream_t stream) {
-  const int width = (1 << sh.lanes_log2) * V;
-  const size_t smem = sizeof(float) * (kThreads >> sh.lanes_log2) * (kBack ? 3 : 2) * width;
+int run(ScanArgs& a, const Shape& sh, int dev, int sms, pv_stream_t stream) {
+  auto kernel = pv_scan_kernel<T, V, kBack>;
+  const size_t smem = sizeof(typename Lane<T, V>::Raw) * 2 * (kBack ? 3 : 2) * kSteps * kThreads +
+                      sizeof(float) * (kBack ? 3 : 2) * kThreads * V;
+  // Blocks that the device holds at once, asked once per device.
+  static std::atomic<int> resident[64];
+  int per_sm = resident[dev].load();
+  if (!per_sm) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, smem) != cudaSuccess || per_sm < 1) {
+      cudaGetLastError();
+      return PV_ERR_CUDA;
+    }
+    resident[dev].store(per_sm);
+  }
+  const int64_t all = std::max<int64_t>(1, sh.tiles * sh.slabs);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned int>(std::max<int64_t>(1, sh.tiles * sh.slabs)));
+  cfg.gridDim = dim3(static_cast<unsigned int>(std::min<int64_t>(all, static_cast<int64_t>(per_sm) * sms)));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeCooperative;
+  at[0].val.cooperative = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, pv_scan_kernel<T, V, kBack>, a) != cudaSuccess) {
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) {
     cudaGetLastError();
     return PV_ERR_CUDA;
   }
@@ -466,6 +574,7 @@ template <bool kBack>
 int start(const pv_scan_params* p, const Shape& sh, ScanArgs& a, int dev, pv_stream_t stream) {
   DeviceScope scope(dev);
   if (!scope.ok()) return PV_ERR_CUDA;
+  if (dev >= 64) return PV_ERR_UNSUPPORTED;
   a.x = p->x;
   a.gate = p->gate;
   a.xs = p->x_stride;
@@ -482,7 +591,11 @@ int start(const pv_scan_params* p, const Shape& sh, ScanArgs& a, int dev, pv_str
     a.row0[b + 1] = static_cast<int>(p->offsets[b + 1]);
     a.tile0[b + 1] = a.tile0[b] + static_cast<int>(t);
     a.group0[b + 1] = a.group0[b] + static_cast<int>((t + kGroup - 1) / kGroup);
+    a.order[b] = static_cast<unsigned char>(b);
   }
+  std::stable_sort(a.order, a.order + p->frames, [&](unsigned char x, unsigned char y) {
+    return a.tile0[x + 1] - a.tile0[x] > a.tile0[y + 1] - a.tile0[y];
+  });
   Scratch scratch;
   const size_t words = static_cast<size_t>(2 * sh.tiles + sh.groups) * p->channels;
   int st = scratch.open(dev, stream, kTagged, 8 * words);
@@ -490,10 +603,13 @@ int start(const pv_scan_params* p, const Shape& sh, ScanArgs& a, int dev, pv_str
   a.ctl = static_cast<unsigned int*>(scratch.head());
   a.maps = static_cast<unsigned long long*>(scratch.body());
   a.bases = a.maps + 2 * sh.tiles * p->channels;
-  if (p->dtype == PV_F32) return run<float, 1, kBack>(a, sh, stream);
+  const int sms = sm_count(dev);
+  if (sms < 1) return PV_ERR_CUDA;
+  if (p->dtype == PV_F32) return run<float, 1, kBack>(a, sh, dev, sms, stream);
   if (p->dtype == PV_BF16)
-    return sh.vec == 2 ? run<__nv_bfloat16, 2, kBack>(a, sh, stream) : run<__nv_bfloat16, 1, kBack>(a, sh, stream);
-  return sh.vec == 2 ? run<__half, 2, kBack>(a, sh, stream) : run<__half, 1, kBack>(a, sh, stream);
+    return sh.vec == 2 ? run<__nv_bfloat16, 2, kBack>(a, sh, dev, sms, stream)
+                       : run<__nv_bfloat16, 1, kBack>(a, sh, dev, sms, stream);
+  return sh.vec == 2 ? run<__half, 2, kBack>(a, sh, dev, sms, stream) : run<__half, 1, kBack>(a, sh, dev, sms, stream);
 }
 
 }  // namespace

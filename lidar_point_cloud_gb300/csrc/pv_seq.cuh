@@ -89,10 +89,10 @@ struct Pack;  // 16 bytes of T as floats
 template <>
 struct Pack<float> {
   static constexpr int kN = 4;
-  static __device__ __forceinline__ void load(const void* p, float* f) {
-    const float4 v = *static_cast<const float4*>(p);
-    f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+  static __device__ __forceinline__ void open(uint4 v, float* f) {
+    f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y), f[2] = __uint_as_float(v.z), f[3] = __uint_as_float(v.w);
   }
+  static __device__ __forceinline__ void load(const void* p, float* f) { open(*static_cast<const uint4*>(p), f); }
   static __device__ __forceinline__ void store(void* p, const float* f) {
     *static_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
   }
@@ -103,8 +103,8 @@ struct Pack<float> {
 template <>
 struct Pack<__nv_bfloat16> {
   static constexpr int kN = 8;
-  static __device__ __forceinline__ void load(const void* p, float* f) {
-    const uint4 v = *static_cast<const uint4*>(p);
+  static __device__ __forceinline__ void load(const void* p, float* f) { open(*static_cast<const uint4*>(p), f); }
+  static __device__ __forceinline__ void open(uint4 v, float* f) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -126,8 +126,8 @@ struct Pack<__nv_bfloat16> {
 template <>
 struct Pack<__half> {
   static constexpr int kN = 8;
-  static __device__ __forceinline__ void load(const void* p, float* f) {
-    const uint4 v = *static_cast<const uint4*>(p);
+  static __device__ __forceinline__ void load(const void* p, float* f) { open(*static_cast<const uint4*>(p), f); }
+  static __device__ __forceinline__ void open(uint4 v, float* f) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
