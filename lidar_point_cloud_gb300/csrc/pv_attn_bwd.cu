@@ -8,9 +8,12 @@
 //   acc2 += P other,  acc1 += dS other1
 // with own = (q, do), other = (k, v) for dq, and the other way round for dk
 // (acc1) and dv (acc2 += P^T do).  P replaces S in tensor memory and dS dP, as
-// the next products' operands.  Warps 0-3 and 4-7 take 64 columns each, one row
-// a thread; warp 8 issues the products, warp 9 the loads, warp 10 puts what
-// belongs to the other side's rows (lse, delta, positions) into shared memory.
+// the next products' operands.  Four warpgroups take 32 columns each, one row a
+// thread (two of 64 columns, tried first, were 1.X times slower: two warps a
+// scheduler do not hide the chain of an element, and twice the straight-line code
+// starves the instruction fetch); one warp issues the products, one the loads,
+// one puts what belongs to the other side's rows (lse, delta, positions) into
+// shared memory.
 //
 // The accumulators of 128-element heads leave room for one S and one dP only,
 // so the work is staggered: while the threads make dS of a tile, the tensor cores
@@ -40,11 +43,14 @@ namespace pvs {
 
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int kRegsMath = 208, kRegsOther = 80;  // 256 x 208 + 128 x 80 = 63,488 of 384 x 168 = 64,512
+constexpr int kGroups = 4;                      // warpgroups of arithmetic
+constexpr int kMath = kGroups * 128;
+constexpr int kThreads = kMath + 128;
+// Registers of a thread: 96 at launch (640 x 96 = 61,440); 512 x 104 + 128 x 64 = 61,440.
+constexpr int kRegsMath = 104, kRegsOther = 64;
 constexpr int kOwn = 128;    // rows of a block
 constexpr int kOther = 128;  // rows of a step
-constexpr int kHalf = 64;    // columns of a thread
+constexpr int kCols = kOther / kGroups;  // columns of a thread
 constexpr int kSides = 3;    // slots of what belongs to the other side's rows
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kUp = 4.0f;  // log2 of the factor on P and dS
@@ -57,12 +63,16 @@ struct Smem {
   alignas(1024) unsigned char own[2][kTile];
   alignas(1024) unsigned char other[2][kSlots][kTile];
   float side[kSides][5][kOther];  // lse (as an offset of the exponent), delta (negated), positions
-  float rest[2][kOwn];            // dq: each warpgroup's sum of P (dP - delta)
+  float rest[kGroups][kOwn];      // dq: each warpgroup's sum of P (dP - delta)
+  float guess[kOwn];              // dq: do.o of the rounded o
   uint64_t own_full, full[2][kSlots], empty[2][kSlots], s_full, dp_full, p_full, ds_full, acc_full, side_full[kSides],
       side_empty[kSides];
   uint32_t tmem;
   int given_up;
 };
+
+// All threads of the arithmetic.
+__device__ __forceinline__ void math_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kMath) : "memory"); }
 
 struct Row {
   float pos[3];        // negated
@@ -73,112 +83,100 @@ struct Row {
   int lo, hi;          // columns seen: lo <= column < hi
 };
 
-// One row's 64 scores at column `at` of tensor memory to 16 P there, in the
+// One row's 32 scores at column `at` of tensor memory to 16 P there, in the
 // storage type.  e keeps what dS is made of: 16 P times the cap's slope; with a
 // cap, dq also needs 16 P itself (as half pairs in `whole_p`: only the small
-// sum that mends delta is made of it) and takes e for acc2.  Columns are taken 32 at a
-// time, one operation after the other over all of them: an element's chain is
-// long, 32 of them hide it.
+// sum that mends delta is made of it) and takes e for acc2.  One operation after
+// the other over all columns: an element's chain is long, 32 of them hide it.
 template <typename T, bool kDkv, bool kCap, bool kMask>
 __device__ __forceinline__ void probabilities(uint32_t at, const float (*side)[kOther], int c0, int axes, const Row& row,
-                                              float* e, uint32_t* whole_p) {
-  tmem_ld32(at, reinterpret_cast<uint32_t*>(e));
-  tmem_ld32(at + 32, reinterpret_cast<uint32_t*>(e + 32));
-  tc_wait_ld<kHalf>(reinterpret_cast<uint32_t*>(e));
+                                              float* u, uint32_t* whole_p) {
+  tmem_ld32(at, reinterpret_cast<uint32_t*>(u));
+  tc_wait_ld<kCols>(reinterpret_cast<uint32_t*>(u));
+  float steep[kCap ? kCols : 1];
+  if (kCap) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    float* u = e + h * 32;
-    const int c = c0 + h * 32;
-    float steep[kCap ? 32 : 1];
-    if (kCap) {
-#pragma unroll
-      for (int x = 0; x < 32; ++x) {
-        u[x] = tanh_half(u[x] * row.cap_in);
-        steep[x] = fmaf(-u[x], u[x], 1.0f);
-      }
+    for (int x = 0; x < kCols; ++x) {
+      u[x] = tanh_half(u[x] * row.cap_in);
+      steep[x] = fmaf(-u[x], u[x], 1.0f);
     }
-    if (axes == 1) lower<1, 32>(u, &side[2][c], kOther, row.pos, row.slope);
-    if (axes == 2) lower<2, 32>(u, &side[2][c], kOther, row.pos, row.slope);
-    if (axes == 3) lower<3, 32>(u, &side[2][c], kOther, row.pos, row.slope);
-#pragma unroll
-    for (int x = 0; x < 32; x += 4) {
-      float4 l = make_float4(row.off, row.off, row.off, row.off);
-      if (kDkv) l = *reinterpret_cast<const float4*>(&side[0][c + x]);
-      fma2(u[x], u[x + 1], u[x], u[x + 1], row.mul, row.mul, l.x, l.y);
-      fma2(u[x + 2], u[x + 3], u[x + 2], u[x + 3], row.mul, row.mul, l.z, l.w);
-    }
-#pragma unroll
-    for (int x = 0; x < 32; ++x) {
-      u[x] = exp2_fast(u[x]);
-      if (kMask) u[x] = c + x >= row.lo && c + x < row.hi ? u[x] : 0.0f;
-    }
-    uint32_t p[16];
-    if (!kCap || kDkv) {
-#pragma unroll
-      for (int x = 0; x < 32; x += 2) p[x >> 1] = Pack<T>::two(u[x], u[x + 1]);
-    }
-    if (kCap) {
-      if (!kDkv) {
-#pragma unroll
-        for (int x = 0; x < 32; x += 2) whole_p[h * 16 + (x >> 1)] = Pack<__half>::two(u[x], u[x + 1]);
-      }
-#pragma unroll
-      for (int x = 0; x < 32; ++x) u[x] *= steep[x];
-      if (!kDkv) {
-#pragma unroll
-        for (int x = 0; x < 32; x += 2) p[x >> 1] = Pack<T>::two(u[x], u[x + 1]);
-      }
-    }
-    tmem_st16(at + h * 16, p);
   }
+  if (axes == 1) lower<1, kCols>(u, &side[2][c0], kOther, row.pos, row.slope);
+  if (axes == 2) lower<2, kCols>(u, &side[2][c0], kOther, row.pos, row.slope);
+  if (axes == 3) lower<3, kCols>(u, &side[2][c0], kOther, row.pos, row.slope);
+#pragma unroll
+  for (int x = 0; x < kCols; x += 4) {
+    float4 l = make_float4(row.off, row.off, row.off, row.off);
+    if (kDkv) l = *reinterpret_cast<const float4*>(&side[0][c0 + x]);
+    fma2(u[x], u[x + 1], u[x], u[x + 1], row.mul, row.mul, l.x, l.y);
+    fma2(u[x + 2], u[x + 3], u[x + 2], u[x + 3], row.mul, row.mul, l.z, l.w);
+  }
+#pragma unroll
+  for (int x = 0; x < kCols; ++x) {
+    u[x] = exp2_fast(u[x]);
+    if (kMask) u[x] = c0 + x >= row.lo && c0 + x < row.hi ? u[x] : 0.0f;
+  }
+  uint32_t p[kCols / 2];
+  if (!kCap || kDkv) {
+#pragma unroll
+    for (int x = 0; x < kCols; x += 2) p[x >> 1] = Pack<T>::two(u[x], u[x + 1]);
+  }
+  if (kCap) {
+    if (!kDkv) {
+#pragma unroll
+      for (int x = 0; x < kCols; x += 2) whole_p[x >> 1] = Pack<__half>::two(u[x], u[x + 1]);
+    }
+#pragma unroll
+    for (int x = 0; x < kCols; ++x) u[x] *= steep[x];
+    if (!kDkv) {
+#pragma unroll
+      for (int x = 0; x < kCols; x += 2) p[x >> 1] = Pack<T>::two(u[x], u[x + 1]);
+    }
+  }
+  tmem_st16(at, p);
 }
 
 // dP at column `at` to 16 dS there.
 template <typename T, bool kDkv, bool kCap, bool kMask>
 __device__ __forceinline__ void gradients(uint32_t at, const float (*side)[kOther], int c0, Row& row, const float* e,
                                           const uint32_t* whole_p) {
-  float g[kHalf];
+  float g[kCols];
   tmem_ld32(at, reinterpret_cast<uint32_t*>(g));
-  tmem_ld32(at + 32, reinterpret_cast<uint32_t*>(g + 32));
-  tc_wait_ld<kHalf>(reinterpret_cast<uint32_t*>(g));
+  tc_wait_ld<kCols>(reinterpret_cast<uint32_t*>(g));
   float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+  uint32_t s[kCols / 2];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t s[16];
+  for (int x = 0; x < kCols; x += 4) {
+    float4 d = make_float4(row.delta, row.delta, row.delta, row.delta);
+    if (kDkv) d = *reinterpret_cast<const float4*>(&side[1][c0 + x]);
+    add2(g[x], g[x + 1], g[x], g[x + 1], d.x, d.y);
+    add2(g[x + 2], g[x + 3], g[x + 2], g[x + 3], d.z, d.w);
+    float v[4];
 #pragma unroll
-    for (int x = h * 32; x < h * 32 + 32; x += 4) {
-      float4 d = make_float4(row.delta, row.delta, row.delta, row.delta);
-      if (kDkv) d = *reinterpret_cast<const float4*>(&side[1][c0 + x]);
-      add2(g[x], g[x + 1], g[x], g[x + 1], d.x, d.y);
-      add2(g[x + 2], g[x + 3], g[x + 2], g[x + 3], d.z, d.w);
-      float v[4];
-#pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        v[y] = g[x + y] * e[x + y];
-        // (A hidden place has e = 0, but what stands at it need not be finite.)
-        if (kMask) v[y] = c0 + x + y >= row.lo && c0 + x + y < row.hi ? v[y] : 0.0f;
-      }
-      s[(x & 31) >> 1] = Pack<T>::two(v[0], v[1]);
-      s[((x & 31) >> 1) + 1] = Pack<T>::two(v[2], v[3]);
-      if (!kDkv) {
-        if (kCap) {
-          float w[4];
-#pragma unroll
-          for (int y = 0; y < 4; y += 2) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&whole_p[(x + y) >> 1]));
-            w[y] = g[x + y] * f.x;
-            w[y + 1] = g[x + y + 1] * f.y;
-          }
-#pragma unroll
-          for (int y = 0; y < 4; ++y)
-            v[y] = !kMask || (c0 + x + y >= row.lo && c0 + x + y < row.hi) ? w[y] : 0.0f;
-        }
-        add2(s0, s1, s0, s1, v[0], v[1]);
-        add2(s2, s3, s2, s3, v[2], v[3]);
-      }
+    for (int y = 0; y < 4; ++y) {
+      v[y] = g[x + y] * e[x + y];
+      // (A hidden place has e = 0, but what stands at it need not be finite.)
+      if (kMask) v[y] = c0 + x + y >= row.lo && c0 + x + y < row.hi ? v[y] : 0.0f;
     }
-    tmem_st16(at + h * 16, s);
+    s[x >> 1] = Pack<T>::two(v[0], v[1]);
+    s[(x >> 1) + 1] = Pack<T>::two(v[2], v[3]);
+    if (!kDkv) {
+      if (kCap) {
+#pragma unroll
+        for (int y = 0; y < 4; y += 2) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&whole_p[(x + y) >> 1]));
+          v[y] = g[x + y] * f.x;
+          v[y + 1] = g[x + y + 1] * f.y;
+        }
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          if (kMask) v[y] = c0 + x + y >= row.lo && c0 + x + y < row.hi ? v[y] : 0.0f;
+      }
+      add2(s0, s1, s0, s1, v[0], v[1]);
+      add2(s2, s3, s2, s3, v[2], v[3]);
+    }
   }
+  tmem_st16(at, s);
   if (!kDkv) row.total += (s0 + s1) + (s2 + s3);
 }
 
@@ -189,6 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                        const __grid_constant__ CUtensorMap mdo) {
   using S = Smem<kBlocks>;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  constexpr int kIssue = kMath / 32;  // the first warp after those of the arithmetic
   extern __shared__ __align__(1024) unsigned char raw[];
   S& sm = *reinterpret_cast<S*>(raw + ((1024 - (smem_addr(raw) & 1023)) & 1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -227,16 +226,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < S::kSlots; ++i) bar_init(&sm.full[s][i], 1), bar_init(&sm.empty[s][i], 1);
     bar_init(&sm.s_full, 1);
     bar_init(&sm.dp_full, 1);
-    bar_init(&sm.p_full, 2 * kOwn);
-    bar_init(&sm.ds_full, 2 * kOwn);
-    for (int i = 0; i < kSides; ++i) bar_init(&sm.side_full[i], 32), bar_init(&sm.side_empty[i], 2 * kOwn);
+    bar_init(&sm.p_full, kMath);
+    bar_init(&sm.ds_full, kMath);
+    for (int i = 0; i < kSides; ++i) bar_init(&sm.side_full[i], 32), bar_init(&sm.side_empty[i], kMath);
     fence_bar_init();
     tma_prefetch(&mq);
     tma_prefetch(&mk);
     tma_prefetch(&mv);
     tma_prefetch(&mdo);
   }
-  if (warp == 8) tmem_alloc<512>(&sm.tmem);
+  if (warp == kIssue) tmem_alloc<512>(&sm.tmem);
   tc_before();
   __syncthreads();
   tc_after();
@@ -245,8 +244,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool sides = kDkv || a.slopes != nullptr;
   wait_prior_grid();
 
-  if (warp >= 8) regs_down<kRegsOther>();
-  if (warp == 9) {
+  if (warp >= kIssue) regs_down<kRegsOther>();
+  if (warp == kIssue + 1) {
     // ---- loads
     if (lane == 0 && steps > 0) {
       const CUtensorMap* own_map[2] = {kDkv ? &mk : &mq, kDkv ? &mv : &mdo};
@@ -273,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
       }
     }
-  } else if (warp == 8) {
+  } else if (warp == kIssue) {
     // ---- products
     const uint32_t word_s = mma_word(kBf16, 128, kOther, false, false);
     const uint32_t word_a = mma_word(kBf16, 128, 0, false, true) | (static_cast<uint32_t>(a.Dn >> 3) << 17);
@@ -314,8 +313,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t b = operand(smem_addr(sm.other[from][slot]), kOther * 128);
         const uint32_t acc = tm + 256 + (s ? 0 : 64 * kBlocks), left = tm + s * 128;
 #pragma unroll
-        for (int x = 0; x < kOther / 16; ++x)  // the two halves' columns lie 64 apart
-          mma_ts(acc, left + (x >> 2) * 64 + (x & 3) * 8, b + x * (2048 >> 4), word_a, n > 0 || x > 0);
+        for (int x = 0; x < kOther / 16; ++x)  // a warpgroup's 32 columns lie in 16 of its own
+          mma_ts(acc, left + x / (kCols / 16) * kCols + x % (kCols / 16) * 8, b + x * (2048 >> 4), word_a, n > 0 || x > 0);
         if (kDkv && s == 0) mma_commit(&sm.empty[1][slot]);
         if (s == 1) mma_commit(&sm.empty[0][slot]);
         if (s == 1 && n == steps - 1) mma_commit(&sm.acc_full);
@@ -331,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       sums(1, n);
       if (n + 1 < steps) ok = scores(1, n + 1);
     }
-  } else if (warp == 10) {
+  } else if (warp == kIssue + 2) {
     // ---- what belongs to the other side's rows
     if (sides) {
       for (int n = 0; n < steps; ++n) {
@@ -353,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bar_arrive(&sm.side_full[slot]);
       }
     }
-  } else if (warp < 8) {
+  } else if (warp < kIssue) {
     // ---- probabilities and gradients: one own row, 64 columns of each step a thread
     regs_up<kRegsMath>();
     const int wg = warp >> 2, r = threadIdx.x & (kOwn - 1);
@@ -371,17 +370,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     row.cap_in = a.cap > 0.0f ? 2.0f * a.scale * kLog2e / a.cap : 0.0f;
     row.slope = a.slopes && !kDkv ? -a.slopes[own_head] * kLog2e / row.mul : 0.0f;
     float delta = 0.0f;
-    if (!kDkv && live) {
-      row.off = fmaf(-kLog2e, a.lse[static_cast<long long>(own_head) * a.queries + own_row], kUp);
-      const char* o = a.o.data + own_row * a.o.row + own_head * a.o.head;
-      const char* g = a.dout.data + own_row * a.dout.row + own_head * a.dout.head;
-      for (int d = 0; d < a.D; d += 8) {
-        float x[8], y[8];
-        Pack<T>::load(o + d * 2, x);
-        Pack<T>::load(g + d * 2, y);
+    if (!kDkv) {
+      if (live) row.off = fmaf(-kLog2e, a.lse[static_cast<long long>(own_head) * a.queries + own_row], kUp);
+      if (wg == 0) {
+        if (live) {
+          const char* o = a.o.data + own_row * a.o.row + own_head * a.o.head;
+          const char* g = a.dout.data + own_row * a.dout.row + own_head * a.dout.head;
+          for (int d = 0; d < a.D; d += 8) {
+            float x[8], y[8];
+            Pack<T>::load(o + d * 2, x);
+            Pack<T>::load(g + d * 2, y);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) delta = fmaf(x[e], y[e], delta);
+            for (int e = 0; e < 8; ++e) delta = fmaf(x[e], y[e], delta);
+          }
+        }
+        sm.guess[r] = delta;
       }
+      math_sync();
+      delta = sm.guess[r];
       row.delta = -delta;
     }
     // A place is seen if its column is at least `from` and below `to`.
@@ -392,14 +398,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       else
         to = live ? limit(own) : 0;
     }
-    const int c0 = wg * kHalf;
+    const int c0 = wg * kCols;
     const uint32_t s_at = mine + c0, dp_at = mine + 128 + c0;
     bool ok = true;
     // One step with the cap and the mask as compile-time choices.
     auto step = [&](auto cap, auto mask, int n, const float(*side)[kOther]) {
       constexpr bool kCap = decltype(cap)::value, kMask = decltype(mask)::value;
-      float e[kHalf];
-      uint32_t whole_p[kCap && !kDkv ? kHalf / 2 : 1];
+      float e[kCols];
+      uint32_t whole_p[kCap && !kDkv ? kCols / 2 : 1];
       probabilities<T, kDkv, kCap, kMask>(s_at, side, c0, a.axes, row, e, whole_p);
       tc_wait_st();
       tc_before();
@@ -446,19 +452,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     // dq: the sum of P (dP - delta) is what delta is off by.
     if (!kDkv) {
       sm.rest[wg][r] = row.total;
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      row.total = (sm.rest[0][r] + sm.rest[1][r]) * kDown;
+      math_sync();
+      row.total = ((sm.rest[0][r] + sm.rest[1][r]) + (sm.rest[2][r] + sm.rest[3][r])) * kDown;
       if (live && wg == 0) a.delta[static_cast<long long>(own_head) * a.queries + own_row] = delta + row.total;
     }
     const float bad = !ok || *given_up ? __int_as_float(0x7FFFFFFF) : 1.0f;  // a wait ran out: nothing here is an answer
-    const View& out = kDkv ? (wg ? a.dv : a.dk) : a.dq;
+    const int which = wg & 1;  // dk, dv: 0 and 1
+    const View& out = kDkv ? (which ? a.dv : a.dk) : a.dq;
     char* to_row = out.data + own_row * out.row + own_head * out.head;
     const bool parts = kDkv && a.head_parts > 1;
-    float* part = parts ? a.part_o + (((static_cast<long long>(blockIdx.y % a.head_parts) * 2 + wg) * a.keys + own_row) * a.Hk + own_head) * a.D
+    float* part = parts ? a.part_o + (((static_cast<long long>(blockIdx.y % a.head_parts) * 2 + which) * a.keys + own_row) * a.Hk + own_head) * a.D
                         : nullptr;
-    const float k1 = (kDkv && wg ? 1.0f : a.scale) * kDown * bad;
-    const uint32_t acc = mine + 256 + (kDkv && wg ? 64 * kBlocks : 0);
-    for (int x = kDkv ? 0 : wg * 16; x < a.Dn; x += kDkv ? 16 : 32) {
+    const float k1 = (kDkv && which ? 1.0f : a.scale) * kDown * bad;
+    const uint32_t acc = mine + 256 + (kDkv && which ? 64 * kBlocks : 0);
+    for (int x = (kDkv ? wg >> 1 : wg) * 16; x < a.Dn; x += kDkv ? 32 : 64) {
       uint32_t c[16], d[16];
       float v[16];
       if (any) {
@@ -488,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_before();
   }
   __syncthreads();
-  if (warp == 8) {
+  if (warp == kIssue) {
     if (*given_up) {
       // Loads and products still in flight end in this block's shared and tensor
       // memory: two milliseconds are a thousand times what they take.
