@@ -13,7 +13,7 @@
 // scheduler do not hide the chain of an element, and twice the straight-line code
 // starves the instruction fetch); one warp issues the products, one the loads,
 // one puts what belongs to the other side's rows (lse, delta, positions) into
-// shared memory.
+// shared memory, one clears the rows of a last tile that belong to the next frame.
 //
 // The accumulators of 128-element heads leave room for one S and one dP only,
 // so the work is staggered: while the threads make dS of a tile, the tensor cores
@@ -65,7 +65,7 @@ struct Smem {
   float side[kSides][5][kOther];  // lse (as an offset of the exponent), delta (negated), positions
   float rest[kGroups][kOwn];      // dq: each warpgroup's sum of P (dP - delta)
   float guess[kOwn];              // dq: do.o of the rounded o
-  uint64_t own_full, full[2][kSlots], empty[2][kSlots], s_full, dp_full, p_full, ds_full, acc_full, side_full[kSides],
+  uint64_t own_full, dirty[2], clean[2], full[2][kSlots], empty[2][kSlots], s_full, dp_full, p_full, ds_full, acc_full, side_full[kSides],
       side_empty[kSides];
   uint32_t tmem;
   int given_up;
@@ -222,13 +222,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     sm.given_up = 0;
     bar_init(&sm.own_full, 1);
     bar_init(&sm.acc_full, 1);
+    for (int s = 0; s < 2; ++s) bar_init(&sm.dirty[s], 1), bar_init(&sm.clean[s], 1);
     for (int s = 0; s < 2; ++s)
       for (int i = 0; i < S::kSlots; ++i) bar_init(&sm.full[s][i], 1), bar_init(&sm.empty[s][i], 1);
     bar_init(&sm.s_full, 1);
     bar_init(&sm.dp_full, 1);
-    bar_init(&sm.p_full, kMath);
-    bar_init(&sm.ds_full, kMath);
-    for (int i = 0; i < kSides; ++i) bar_init(&sm.side_full[i], 32), bar_init(&sm.side_empty[i], kMath);
+    bar_init(&sm.p_full, kMath / 32);
+    bar_init(&sm.ds_full, kMath / 32);
+    for (int i = 0; i < kSides; ++i) bar_init(&sm.side_full[i], 1), bar_init(&sm.side_empty[i], kMath / 32);
     fence_bar_init();
     tma_prefetch(&mq);
     tma_prefetch(&mk);
@@ -273,62 +274,94 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == kIssue) {
-    // ---- products
-    const uint32_t word_s = mma_word(kBf16, 128, kOther, false, false);
-    const uint32_t word_a = mma_word(kBf16, 128, 0, false, true) | (static_cast<uint32_t>(a.Dn >> 3) << 17);
-    const int ksteps = (a.D + 15) / 16;
-    bool ok = steps > 0 && warp_wait(&sm.own_full, 0, given_up);
-    // S (s = 0) or dP (s = 1) of step n, from its operand's arrival.
-    auto scores = [&](int s, int n) {
-      const int slot = n % S::kSlots;
-      if (!warp_wait(&sm.full[s][slot], (n / S::kSlots) & 1, given_up)) return false;
-      const int have = other_rows - other_row(n);
-      if (have < kOther) {
-        // Rows past the frame's end are another frame's, whatever they hold.
-        uint4* v = reinterpret_cast<uint4*>(sm.other[s][slot]);
-        for (int c = 0; c < kBlocks; ++c)
-          for (int i = have * 8 + lane; i < kOther * 8; i += 32) v[c * kOther * 8 + i] = make_uint4(0, 0, 0, 0);
-        fence_to_async();
-        __syncwarp();
-      }
-      tc_after();
-      if (elect_one()) {
-        const uint32_t own = operand(smem_addr(sm.own[s]), 16), other = operand(smem_addr(sm.other[s][slot]), 16);
+    // ---- products: one thread, with little to do between them.  It shares its
+    // scheduler with four warps of arithmetic, and the tensor cores take few
+    // products in advance: what it does between two of them, they wait for.
+    if (elect_one() && steps > 0) {
+      const uint32_t word_s = mma_word(kBf16, 128, kOther, false, false);
+      const uint32_t word_a = mma_word(kBf16, 128, 0, false, true) | (static_cast<uint32_t>(a.Dn >> 3) << 17);
+      const int ksteps = (a.D + 15) / 16;
+      const uint32_t own_op = operand(smem_addr(sm.own[0]), 16), row_op = operand(smem_addr(sm.other[0][0]), 16);
+      const uint32_t col_op = operand(smem_addr(sm.other[0][0]), kOther * 128);
+      constexpr uint32_t kStep = S::kTile >> 4, kSide = S::kSlots * kStep;
+      // The slot and its parity of the tile that S and dP (0, 1) come to next.
+      int slot[2] = {0, 0}, parity[2] = {0, 0}, left[2] = {per_head, per_head}, cleaned[2] = {0, 0};
+      const bool ragged = other_rows < (other_tile0 + per_head) * kOther;
+      // Whether the tile's operand is there (its rows past the frame's end cleared).
+      auto arrived = [&](int s) {
+        if (!bar_wait(&sm.full[s][slot[s]], parity[s], given_up)) return false;
+        if (--left[s] == 0) {
+          left[s] = per_head;
+          if (ragged) {
+            bar_arrive(&sm.dirty[s]);
+            if (!bar_wait(&sm.clean[s], cleaned[s], given_up)) return false;
+            cleaned[s] ^= 1;
+          }
+        }
+        return true;
+      };
+      auto scores = [&](int s) {  // S or dP of that tile
+        const uint32_t own = own_op + s * kStep, other = row_op + s * kSide + slot[s] * kStep;
 #pragma unroll
         for (int x = 0; x < 4 * kBlocks; ++x) {
           const uint32_t off = ((x >> 2) * kOwn * 128 + (x & 3) * 32) >> 4;
           if (x < ksteps) mma_ss(tm + s * 128, own + off, other + off, word_s, x > 0);
         }
         mma_commit(s ? &sm.dp_full : &sm.s_full);
-        if (!kDkv && s) mma_commit(&sm.empty[1][slot]);  // dq: nothing else needs v
-      }
-      __syncwarp();
-      return true;
-    };
-    // acc2 += P other (s = 0) or acc1 += dS other1 (s = 1).
-    auto sums = [&](int s, int n) {
-      const int slot = n % S::kSlots, from = kDkv && s == 0 ? 1 : 0;
-      tc_after();
-      if (elect_one()) {
-        const uint32_t b = operand(smem_addr(sm.other[from][slot]), kOther * 128);
+        if (!kDkv && s) mma_commit(&sm.empty[1][slot[1]]);  // dq: nothing else needs v
+        if (++slot[s] == S::kSlots) slot[s] = 0, parity[s] ^= 1;
+      };
+      // acc2 += P other (s = 0), acc1 += dS other1 (s = 1), of the tile in slot `at`.
+      auto sums = [&](int s, int at, bool add) {
+        const uint32_t b = col_op + (kDkv && s == 0 ? kSide : 0) + at * kStep;
         const uint32_t acc = tm + 256 + (s ? 0 : 64 * kBlocks), left = tm + s * 128;
 #pragma unroll
         for (int x = 0; x < kOther / 16; ++x)  // a warpgroup's 32 columns lie in 16 of its own
-          mma_ts(acc, left + x / (kCols / 16) * kCols + x % (kCols / 16) * 8, b + x * (2048 >> 4), word_a, n > 0 || x > 0);
-        if (kDkv && s == 0) mma_commit(&sm.empty[1][slot]);
-        if (s == 1) mma_commit(&sm.empty[0][slot]);
-        if (s == 1 && n == steps - 1) mma_commit(&sm.acc_full);
+          mma_ts(acc, left + x / (kCols / 16) * kCols + x % (kCols / 16) * 8, b + x * (2048 >> 4), word_a, add || x > 0);
+        if (kDkv && s == 0) mma_commit(&sm.empty[1][at]);
+        if (s == 1) mma_commit(&sm.empty[0][at]);
+      };
+      bool ok = bar_wait(&sm.own_full, 0, given_up) && arrived(0) && arrived(1);
+      if (ok) {
+        tc_after();
+        scores(0);
+        scores(1);
       }
-      __syncwarp();
-    };
-    ok = ok && scores(0, 0) && scores(1, 0);
-    for (int n = 0; ok && n < steps; ++n) {
-      if (!(ok = warp_wait(&sm.p_full, n & 1, given_up))) break;
-      sums(0, n);
-      if (n + 1 < steps && !(ok = scores(0, n + 1))) break;
-      if (!(ok = warp_wait(&sm.ds_full, n & 1, given_up))) break;
-      sums(1, n);
-      if (n + 1 < steps) ok = scores(1, n + 1);
+      for (int n = 0, at = 0; ok && n < steps; ++n) {
+        const bool more = n + 1 < steps;
+        if (more && !(ok = arrived(0))) break;
+        if (!(ok = bar_wait(&sm.p_full, n & 1, given_up))) break;
+        tc_after();
+        sums(0, at, n > 0);
+        if (more) scores(0);
+        if (more && !(ok = arrived(1))) break;
+        if (!(ok = bar_wait(&sm.ds_full, n & 1, given_up))) break;
+        tc_after();
+        sums(1, at, n > 0);
+        if (more)
+          scores(1);
+        else
+          mma_commit(&sm.acc_full);
+        if (++at == S::kSlots) at = 0;
+      }
+    }
+    __syncwarp();
+  } else if (warp == kIssue + 3) {
+    // ---- rows past the frame's end are another frame's, whatever they hold
+    const int have = other_rows - (other_tile0 + per_head - 1) * kOther;
+    if (per_head > 0 && have < kOther) {
+      bool ok = true;
+      for (int n = per_head - 1, k = 0; ok && n < steps; n += per_head, k ^= 1) {
+        const int slot = n % S::kSlots;
+        for (int s = 0; ok && s < 2; ++s) {
+          if (!(ok = warp_wait(&sm.dirty[s], k, given_up))) break;
+          uint4* v = reinterpret_cast<uint4*>(sm.other[s][slot]);
+          for (int c = 0; c < kBlocks; ++c)
+            for (int i = have * 8 + lane; i < kOther * 8; i += 32) v[c * kOther * 8 + i] = make_uint4(0, 0, 0, 0);
+          fence_to_async();
+          warp_arrive(&sm.clean[s]);
+        }
+      }
     }
   } else if (warp == kIssue + 2) {
     // ---- what belongs to the other side's rows
@@ -349,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             sm.side[slot][2 + c][x] =
                 in ? static_cast<float>(kDkv ? a.qpos[row * a.qpos_stride + c] : a.kpos[row * a.kpos_stride + c]) : 0.0f;
         }
-        bar_arrive(&sm.side_full[slot]);
+        warp_arrive(&sm.side_full[slot]);
       }
     }
   } else if (warp < kIssue) {
@@ -409,13 +442,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       probabilities<T, kDkv, kCap, kMask>(s_at, side, c0, a.axes, row, e, whole_p);
       tc_wait_st();
       tc_before();
-      bar_arrive(&sm.p_full);
+      warp_arrive(&sm.p_full);
       if (!(ok = warp_wait(&sm.dp_full, n & 1, given_up))) return;
       tc_after();
       gradients<T, kDkv, kCap, kMask>(dp_at, side, c0, row, e, whole_p);
       tc_wait_st();
       tc_before();
-      bar_arrive(&sm.ds_full);
+      warp_arrive(&sm.ds_full);
     };
     for (int n = 0; n < steps; ++n) {
       const int slot = n % kSides;
@@ -443,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           step(No{}, Yes{}, n, sm.side[slot]);
       }
       if (!ok) break;
-      if (sides) bar_arrive(&sm.side_empty[slot]);
+      if (sides) warp_arrive(&sm.side_empty[slot]);
     }
     // ---- outputs
     const bool any = steps > 0;

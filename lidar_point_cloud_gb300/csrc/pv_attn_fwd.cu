@@ -5,7 +5,8 @@
 // read the scores from tensor memory, keep the row's running maximum and sum,
 // and write the probabilities back over the scores as the next product's
 // operand.  Warp 8 issues the products, warp 9 the TMA loads of keys and values
-// into a ring of shared-memory slots, warp 10 puts key positions there.  While
+// into a ring of shared-memory slots, warp 10 puts key positions there, warp 11
+// clears what a frame's last tile holds of the next frame.  While
 // one tile's scores go through the exponential, the other tile's products run.
 //
 // Rows are (query, head) pairs of the heads that share a key head (the largest
@@ -49,7 +50,7 @@ struct Smem {
   alignas(1024) unsigned char q[2][kTile];
   alignas(1024) unsigned char kv[kSlots][kTile];
   float pos[kPosSlots][3][kRows];
-  uint64_t q_full, kv_full[kSlots], kv_empty[kSlots], s_full[2], p_full[2], o_full[2], pos_full[kPosSlots], pos_empty[kPosSlots];
+  uint64_t q_full, dirty, clean, kv_full[kSlots], kv_empty[kSlots], s_full[2], p_full[2], o_full[2], pos_full[kPosSlots], pos_empty[kPosSlots];
   uint32_t tmem;
   int given_up;
 };
@@ -96,9 +97,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     sm.given_up = 0;
     bar_init(&sm.q_full, 1);
+    bar_init(&sm.dirty, 1);
+    bar_init(&sm.clean, 1);
     for (int i = 0; i < S::kSlots; ++i) bar_init(&sm.kv_full[i], 1), bar_init(&sm.kv_empty[i], 1);
-    for (int t = 0; t < 2; ++t) bar_init(&sm.s_full[t], 1), bar_init(&sm.p_full[t], kRows), bar_init(&sm.o_full[t], 1);
-    for (int i = 0; i < kPosSlots; ++i) bar_init(&sm.pos_full[i], 32), bar_init(&sm.pos_empty[i], 2 * kRows);
+    for (int t = 0; t < 2; ++t) bar_init(&sm.s_full[t], 1), bar_init(&sm.p_full[t], kRows / 32), bar_init(&sm.o_full[t], 1);
+    for (int i = 0; i < kPosSlots; ++i) bar_init(&sm.pos_full[i], 1), bar_init(&sm.pos_empty[i], 2 * kRows / 32);
     fence_bar_init();
     tma_prefetch(&mq);
     tma_prefetch(&mk);
@@ -133,68 +136,76 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 8) {
-    // ---- products
-    const uint32_t word_s = mma_word(kBf16, 128, 128, false, false);
-    const uint32_t word_o = mma_word(kBf16, 128, 0, false, true) | (static_cast<uint32_t>(a.Dn >> 3) << 17);
-    const int ksteps = (a.D + 15) / 16;
-    bool ok = je > js && warp_wait(&sm.q_full, 0, given_up);
-    auto scores = [&](int t, int n) {  // S_t = Q_t K^T
-      if (elect_one()) {
-        const uint32_t q = operand(smem_addr(sm.q[t]), 16), k = operand(smem_addr(sm.kv[n % S::kSlots]), 16);
+    // ---- products: one thread, with little to do between them (the tensor cores
+    // take few in advance, and its scheduler is shared)
+    if (elect_one() && je > js) {
+      const uint32_t word_s = mma_word(kBf16, 128, 128, false, false);
+      const uint32_t word_o = mma_word(kBf16, 128, 0, false, true) | (static_cast<uint32_t>(a.Dn >> 3) << 17);
+      const int ksteps = (a.D + 15) / 16;
+      const uint32_t q_op = operand(smem_addr(sm.q[0]), 16), k_op = operand(smem_addr(sm.kv[0]), 16);
+      const uint32_t v_op = operand(smem_addr(sm.kv[0]), kRows * 128);
+      constexpr uint32_t kStep = S::kTile >> 4;
+      auto scores = [&](int t, int slot) {  // S_t = Q_t K^T
+        const uint32_t q = q_op + t * kStep, k = k_op + slot * kStep;
 #pragma unroll
         for (int x = 0; x < 4 * kBlocks; ++x) {
           const uint32_t off = ((x >> 2) * kRows * 128 + (x & 3) * 32) >> 4;
           if (x < ksteps) mma_ss(tm + t * 128, q + off, k + off, word_s, x > 0);
         }
         mma_commit(&sm.s_full[t]);
-      }
-      __syncwarp();
-    };
-    auto full = [&](int n) { return warp_wait(&sm.kv_full[n % S::kSlots], (n / S::kSlots) & 1, given_up); };
-    if (ok) ok = full(0);
-    if (ok) {
-      tc_after();
-      for (int t = 0; t < 2; ++t)
-        if (last_j[t] > js) scores(t, 0);
-      if (elect_one()) mma_commit(&sm.kv_empty[0]);
-      __syncwarp();
-    }
-    for (int j = js; ok && j < je; ++j) {
-      const int nv = 2 * (j - js) + 1, nk1 = nv + 1;
-      if (!(ok = full(nv))) break;
-      if ((j + 1) * kRows > nk) {
-        // Rows past the frame's end are another frame's: whatever they hold must
-        // not meet the zero probabilities of these places.
-        const int have = nk - j * kRows;
-        uint4* v = reinterpret_cast<uint4*>(sm.kv[nv % S::kSlots]);
-        for (int b = 0; b < kBlocks; ++b)
-          for (int i = have * 8 + lane; i < kRows * 8; i += 32) v[b * kRows * 8 + i] = make_uint4(0, 0, 0, 0);
-        fence_to_async();
-        __syncwarp();
-      }
-      if (j + 1 < je && !(ok = full(nk1))) break;
-      for (int t = 0; t < 2; ++t) {
-        if (j >= last_j[t]) continue;
-        if (!(ok = warp_wait(&sm.p_full[t], (j - js) & 1, given_up))) break;
+      };
+      // Keys lie in the even slots of the ring, values in the odd ones.
+      int slot = 0, parity = 0;
+      bool ok = bar_wait(&sm.q_full, 0, given_up) && bar_wait(&sm.kv_full[0], 0, given_up);
+      if (ok) {
         tc_after();
-        if (elect_one()) {
-          const uint32_t v = operand(smem_addr(sm.kv[nv % S::kSlots]), kRows * 128);
+        for (int t = 0; t < 2; ++t)
+          if (last_j[t] > js) scores(t, 0);
+        mma_commit(&sm.kv_empty[0]);
+      }
+      for (int j = js; ok && j < je; ++j) {
+        const int sv = slot + 1;
+        if (!(ok = bar_wait(&sm.kv_full[sv], parity, given_up))) break;
+        if ((j + 1) * kRows > nk) {
+          bar_arrive(&sm.dirty);
+          if (!(ok = bar_wait(&sm.clean, 0, given_up))) break;
+        }
+        slot += 2;
+        if (slot == S::kSlots) slot = 0, parity ^= 1;
+        if (j + 1 < je && !(ok = bar_wait(&sm.kv_full[slot], parity, given_up))) break;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (!ok || j >= last_j[t]) continue;
+          if (!(ok = bar_wait(&sm.p_full[t], (j - js) & 1, given_up))) continue;
+          tc_after();
+          const uint32_t v = v_op + sv * kStep;
 #pragma unroll
           for (int x = 0; x < kRows / 16; ++x)
             mma_ts(tm + 256 + t * 64 * kBlocks, tm + t * 128 + x * 8, v + x * (2048 >> 4), word_o, j > js || x > 0);
+          if (j + 1 < last_j[t])
+            scores(t, slot);
+          else
+            mma_commit(&sm.o_full[t]);
         }
-        __syncwarp();
-        if (j + 1 < last_j[t])
-          scores(t, nk1);
-        else if (elect_one())
-          mma_commit(&sm.o_full[t]);
-        __syncwarp();
+        if (ok) {
+          mma_commit(&sm.kv_empty[sv]);
+          if (j + 1 < je) mma_commit(&sm.kv_empty[slot]);
+        }
       }
-      if (ok && elect_one()) {
-        mma_commit(&sm.kv_empty[nv % S::kSlots]);
-        if (j + 1 < je) mma_commit(&sm.kv_empty[nk1 % S::kSlots]);
+    }
+    __syncwarp();
+  } else if (warp == 11) {
+    // ---- rows past the frame's end are another frame's: whatever they hold must
+    // not meet the zero probabilities of these places
+    if (je > js && je * kRows > nk) {
+      const int n = 2 * (je - 1 - js) + 1, have = nk - (je - 1) * kRows;
+      if (warp_wait(&sm.dirty, 0, given_up)) {
+        uint4* v = reinterpret_cast<uint4*>(sm.kv[n % S::kSlots]);
+        for (int b = 0; b < kBlocks; ++b)
+          for (int i = have * 8 + lane; i < kRows * 8; i += 32) v[b * kRows * 8 + i] = make_uint4(0, 0, 0, 0);
+        fence_to_async();
+        warp_arrive(&sm.clean);
       }
-      __syncwarp();
     }
   } else if (warp == 10) {
     // ---- key positions
@@ -208,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             sm.pos[slot][c][x] =
                 key < nk ? static_cast<float>(a.kpos[static_cast<long long>(a.k0[f] + key) * a.kpos_stride + c]) : 0.0f;
         }
-        bar_arrive(&sm.pos_full[slot]);
+        warp_arrive(&sm.pos_full[slot]);
       }
     }
   } else if (warp < 8) {
@@ -259,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           lower<2, kRows>(u, pos[0], kRows, qp, slope);
         else
           lower<3, kRows>(u, pos[0], kRows, qp, slope);
-        bar_arrive(&sm.pos_empty[n % kPosSlots]);
+        warp_arrive(&sm.pos_empty[n % kPosSlots]);
       }
       if ((j + 1) * kRows > clear) {
         const int seen = lim - j * kRows;
@@ -308,13 +319,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       sum += s0 + s1;
       tc_wait_st();
       tc_before();
-      bar_arrive(&sm.p_full[t]);
+      warp_arrive(&sm.p_full[t]);
     }
     // A tile that ends earlier lets go of the other tile's key positions.
     if (a.slopes)
       for (int j = last_j[t]; ok && j < je; ++j) {
         const int n = j - js;
-        if ((ok = warp_wait(&sm.pos_full[n % kPosSlots], (n / kPosSlots) & 1, given_up))) bar_arrive(&sm.pos_empty[n % kPosSlots]);
+        if ((ok = warp_wait(&sm.pos_full[n % kPosSlots], (n / kPosSlots) & 1, given_up))) warp_arrive(&sm.pos_empty[n % kPosSlots]);
       }
     // ---- output
     const bool any = last_j[t] > js;

@@ -59,6 +59,13 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xFFFFFFFFu, bar_wait(bar, parity, given_up));
 }
 
+// One arrival for a whole warp: 32 lanes arriving one by one at the same word
+// keep the shared memory busy for as many cycles as a product takes.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) bar_arrive(bar);
+}
+
 // Shared memory written by threads, read by TMA or the tensor cores.
 __device__ __forceinline__ void fence_to_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void fence_bar_init() { asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory"); }
