@@ -8,12 +8,16 @@
 //   acc2 += P other,  acc1 += dS other1
 // with own = (q, do), other = (k, v) for dq, and the other way round for dk
 // (acc1) and dv (acc2 += P^T do).  P replaces S in tensor memory and dS dP, as
-// the next products' operands.  Four warpgroups take 32 columns each, one row a
-// thread (two of 64 columns, tried first, were 1.X times slower: two warps a
-// scheduler do not hide the chain of an element, and twice the straight-line code
-// starves the instruction fetch); one warp issues the products, one the loads,
-// one puts what belongs to the other side's rows (lse, delta, positions) into
-// shared memory, one clears the rows of a last tile that belong to the next frame.
+// the next products' operands.  Four warpgroups take 32 columns each; one warp
+// issues the products, one the loads, one puts what belongs to the other side's
+// rows (lse, delta, positions) into shared memory, one clears the rows of a last tile
+// that belong to the next frame.
+//
+// The arithmetic reads S and dP in fragments (four rows and eight columns a
+// thread), not a row a thread: what belongs to a column is then loaded once for
+// four rows, by lanes that load different columns.  With a row a thread all lanes
+// load the same column, which takes the shared memory, that the products are fed
+// from, as long as a load of 512 different bytes.
 //
 // The accumulators of 128-element heads leave room for one S and one dP only,
 // so the work is staggered: while the threads make dS of a tile, the tensor cores
@@ -74,110 +78,124 @@ struct Smem {
 // All threads of the arithmetic.
 __device__ __forceinline__ void math_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kMath) : "memory"); }
 
-struct Row {
-  float pos[3];        // negated
-  float slope, mul;    // exponent = mul * (score + slope * distance) + off
-  float cap_in;        // score = tanh of half this times the raw one, if capped
-  float off, delta;    // dq: the row's own (delta negated); dk, dv: a column's, in shared memory
-  float total;         // dq: sum of 16 P (dP - delta)
-  int lo, hi;          // columns seen: lo <= column < hi
+// A thread's four rows: 8 x + lane / 4 of its warp's 32.
+struct Rows {
+  float pos[3][4];         // negated
+  float slope[4], mul;     // exponent = mul * (score + slope * distance) + off
+  float cap_in;            // score = tanh of half this times the raw one, if capped
+  float off[4], delta[4];  // dq: the rows' own (delta negated); dk, dv: the columns', in shared memory
+  float total[4];          // dq: sums of 16 P (dP - delta)
+  int lo[4], hi[4];        // of the thread's first column, columns seen: lo <= column < hi
 };
 
-// One row's 32 scores at column `at` of tensor memory to 16 P there, in the
-// storage type.  e keeps what dS is made of: 16 P times the cap's slope; with a
-// cap, dq also needs 16 P itself (as half pairs in `whole_p`: only the small
-// sum that mends delta is made of it) and takes e for acc2.  One operation after
-// the other over all columns: an element's chain is long, 32 of them hide it.
+constexpr int kElems = kCols / 2;  // of two of the four rows: registers of one 16-lane fragment
+__device__ __forceinline__ constexpr int row_of(int h, int x) { return 2 * h + ((x >> 1) & 1); }
+__device__ __forceinline__ constexpr int col_of(int x) { return (x >> 2) * 8 + (x & 1); }
+
+// 32 rows' scores of 32 columns, from column `at` of tensor memory on, to 16 P there, in
+// the storage type.  `side` points to what belongs to the thread's first column.
+// u keeps what dS is made of: 16 P times the cap's slope; with a cap, dq also
+// needs 16 P itself (as half pairs in `whole_p`: only the small sum that mends
+// delta is made of it) and takes u for acc2.  One operation after the other over
+// all elements: an element's chain is long, 32 of them hide it.
 template <typename T, bool kDkv, bool kCap, bool kMask>
-__device__ __forceinline__ void probabilities(uint32_t at, const float (*side)[kOther], int c0, int axes, const Row& row,
-                                              float* u, uint32_t* whole_p) {
-  tmem_ld32(at, reinterpret_cast<uint32_t*>(u));
-  tc_wait_ld<kCols>(reinterpret_cast<uint32_t*>(u));
-  float steep[kCap ? kCols : 1];
+__device__ __forceinline__ void probabilities(uint32_t at, const float* side, int axes, const Rows& row, float (*u)[kElems],
+                                              uint32_t (*whole_p)[kElems / 2]) {
+  tmem_ld_16x256b_x4(at, reinterpret_cast<uint32_t*>(u[0]));
+  tmem_ld_16x256b_x4(at + (16u << 16), reinterpret_cast<uint32_t*>(u[1]));
+  tc_wait_ld<kElems>(reinterpret_cast<uint32_t*>(u[0]));
+  tc_wait_ld<kElems>(reinterpret_cast<uint32_t*>(u[1]));
+  float steep[2][kCap ? kElems : 1];
   if (kCap) {
 #pragma unroll
-    for (int x = 0; x < kCols; ++x) {
-      u[x] = tanh_half(u[x] * row.cap_in);
-      steep[x] = fmaf(-u[x], u[x], 1.0f);
-    }
-  }
-  if (axes == 1) lower<1, kCols>(u, &side[2][c0], kOther, row.pos, row.slope);
-  if (axes == 2) lower<2, kCols>(u, &side[2][c0], kOther, row.pos, row.slope);
-  if (axes == 3) lower<3, kCols>(u, &side[2][c0], kOther, row.pos, row.slope);
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-  for (int x = 0; x < kCols; x += 4) {
-    float4 l = make_float4(row.off, row.off, row.off, row.off);
-    if (kDkv) l = *reinterpret_cast<const float4*>(&side[0][c0 + x]);
-    fma2(u[x], u[x + 1], u[x], u[x + 1], row.mul, row.mul, l.x, l.y);
-    fma2(u[x + 2], u[x + 3], u[x + 2], u[x + 3], row.mul, row.mul, l.z, l.w);
+      for (int x = 0; x < kElems; ++x) {
+        u[h][x] = tanh_half(u[h][x] * row.cap_in);
+        steep[h][x] = fmaf(-u[h][x], u[h][x], 1.0f);
+      }
   }
+  if (axes == 1) lower<1, kCols / 8>(u, side + 2 * kOther, kOther, row.pos, row.slope);
+  if (axes == 2) lower<2, kCols / 8>(u, side + 2 * kOther, kOther, row.pos, row.slope);
+  if (axes == 3) lower<3, kCols / 8>(u, side + 2 * kOther, kOther, row.pos, row.slope);
 #pragma unroll
-  for (int x = 0; x < kCols; ++x) {
-    u[x] = exp2_fast(u[x]);
-    if (kMask) u[x] = c0 + x >= row.lo && c0 + x < row.hi ? u[x] : 0.0f;
-  }
-  uint32_t p[kCols / 2];
-  if (!kCap || kDkv) {
+  for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int x = 0; x < kCols; x += 2) p[x >> 1] = Pack<T>::two(u[x], u[x + 1]);
-  }
-  if (kCap) {
-    if (!kDkv) {
-#pragma unroll
-      for (int x = 0; x < kCols; x += 2) whole_p[x >> 1] = Pack<__half>::two(u[x], u[x + 1]);
+    for (int x = 0; x < kElems; x += 2) {
+      const int r = row_of(h, x);
+      float2 l = make_float2(row.off[r], row.off[r]);
+      if (kDkv) l = *reinterpret_cast<const float2*>(side + col_of(x));
+      fma2(u[h][x], u[h][x + 1], u[h][x], u[h][x + 1], row.mul, row.mul, l.x, l.y);
     }
 #pragma unroll
-    for (int x = 0; x < kCols; ++x) u[x] *= steep[x];
-    if (!kDkv) {
+  for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int x = 0; x < kCols; x += 2) p[x >> 1] = Pack<T>::two(u[x], u[x + 1]);
+    for (int x = 0; x < kElems; ++x) {
+      u[h][x] = exp2_fast(u[h][x]);
+      if (kMask) u[h][x] = col_of(x) >= row.lo[row_of(h, x)] && col_of(x) < row.hi[row_of(h, x)] ? u[h][x] : 0.0f;
     }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t p[kElems / 2];
+    if (!kCap || kDkv) {
+#pragma unroll
+      for (int x = 0; x < kElems; x += 2) p[x >> 1] = Pack<T>::two(u[h][x], u[h][x + 1]);
+    }
+    if (kCap) {
+      if (!kDkv) {
+#pragma unroll
+        for (int x = 0; x < kElems; x += 2) whole_p[h][x >> 1] = Pack<__half>::two(u[h][x], u[h][x + 1]);
+      }
+#pragma unroll
+      for (int x = 0; x < kElems; ++x) u[h][x] *= steep[h][x];
+      if (!kDkv) {
+#pragma unroll
+        for (int x = 0; x < kElems; x += 2) p[x >> 1] = Pack<T>::two(u[h][x], u[h][x + 1]);
+      }
+    }
+    tmem_st_16x128b_x4(at + (h ? 16u << 16 : 0u), p);
   }
-  tmem_st16(at, p);
 }
 
 // dP at column `at` to 16 dS there.
 template <typename T, bool kDkv, bool kCap, bool kMask>
-__device__ __forceinline__ void gradients(uint32_t at, const float (*side)[kOther], int c0, Row& row, const float* e,
-                                          const uint32_t* whole_p) {
-  float g[kCols];
-  tmem_ld32(at, reinterpret_cast<uint32_t*>(g));
-  tc_wait_ld<kCols>(reinterpret_cast<uint32_t*>(g));
-  float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
-  uint32_t s[kCols / 2];
+__device__ __forceinline__ void gradients(uint32_t at, const float* side, Rows& row, const float (*e)[kElems],
+                                          const uint32_t (*whole_p)[kElems / 2]) {
+  float g[2][kElems];
+  tmem_ld_16x256b_x4(at, reinterpret_cast<uint32_t*>(g[0]));
+  tmem_ld_16x256b_x4(at + (16u << 16), reinterpret_cast<uint32_t*>(g[1]));
+  tc_wait_ld<kElems>(reinterpret_cast<uint32_t*>(g[0]));
+  tc_wait_ld<kElems>(reinterpret_cast<uint32_t*>(g[1]));
 #pragma unroll
-  for (int x = 0; x < kCols; x += 4) {
-    float4 d = make_float4(row.delta, row.delta, row.delta, row.delta);
-    if (kDkv) d = *reinterpret_cast<const float4*>(&side[1][c0 + x]);
-    add2(g[x], g[x + 1], g[x], g[x + 1], d.x, d.y);
-    add2(g[x + 2], g[x + 3], g[x + 2], g[x + 3], d.z, d.w);
-    float v[4];
+  for (int h = 0; h < 2; ++h) {
+    uint32_t s[kElems / 2];
+    float t[4] = {};
 #pragma unroll
-    for (int y = 0; y < 4; ++y) {
-      v[y] = g[x + y] * e[x + y];
+    for (int x = 0; x < kElems; x += 2) {
+      const int r = row_of(h, x);
+      float2 d = make_float2(row.delta[r], row.delta[r]);
+      if (kDkv) d = *reinterpret_cast<const float2*>(side + kOther + col_of(x));
+      add2(g[h][x], g[h][x + 1], g[h][x], g[h][x + 1], d.x, d.y);
       // (A hidden place has e = 0, but what stands at it need not be finite.)
-      if (kMask) v[y] = c0 + x + y >= row.lo && c0 + x + y < row.hi ? v[y] : 0.0f;
-    }
-    s[x >> 1] = Pack<T>::two(v[0], v[1]);
-    s[(x >> 1) + 1] = Pack<T>::two(v[2], v[3]);
-    if (!kDkv) {
-      if (kCap) {
-#pragma unroll
-        for (int y = 0; y < 4; y += 2) {
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&whole_p[(x + y) >> 1]));
-          v[y] = g[x + y] * f.x;
-          v[y + 1] = g[x + y + 1] * f.y;
+      const bool seen0 = !kMask || (col_of(x) >= row.lo[r] && col_of(x) < row.hi[r]);
+      const bool seen1 = !kMask || (col_of(x + 1) >= row.lo[r] && col_of(x + 1) < row.hi[r]);
+      float v0 = seen0 ? g[h][x] * e[h][x] : 0.0f, v1 = seen1 ? g[h][x + 1] * e[h][x + 1] : 0.0f;
+      s[x >> 1] = Pack<T>::two(v0, v1);
+      if (!kDkv) {
+        if (kCap) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&whole_p[h][x >> 1]));
+          v0 = seen0 ? g[h][x] * f.x : 0.0f;
+          v1 = seen1 ? g[h][x + 1] * f.y : 0.0f;
         }
-#pragma unroll
-        for (int y = 0; y < 4; ++y)
-          if (kMask) v[y] = c0 + x + y >= row.lo && c0 + x + y < row.hi ? v[y] : 0.0f;
+        add2(t[x & 2], t[(x & 2) + 1], t[x & 2], t[(x & 2) + 1], v0, v1);
       }
-      add2(s0, s1, s0, s1, v[0], v[1]);
-      add2(s2, s3, s2, s3, v[2], v[3]);
+    }
+    tmem_st_16x128b_x4(at + (h ? 16u << 16 : 0u), s);
+    if (!kDkv) {
+      row.total[2 * h] += t[0] + t[1];
+      row.total[2 * h + 1] += t[2] + t[3];
     }
   }
-  tmem_st16(at, s);
-  if (!kDkv) row.total += (s0 + s1) + (s2 + s3);
 }
 
 template <typename T, int kBlocks, bool kDkv>
@@ -386,26 +404,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp < kIssue) {
-    // ---- probabilities and gradients: one own row, 64 columns of each step a thread
+    // ---- probabilities and gradients: 32 own rows a warp, in fragments: four rows and
+    // 8 of the warpgroup's 32 columns a thread
     regs_up<kRegsMath>();
-    const int wg = warp >> 2, r = threadIdx.x & (kOwn - 1);
-    const int own = own0 + r;
+    const int wg = warp >> 2, r0 = (warp & 3) * 32, quad = lane & 3;
+    const uint32_t mine = tm + (static_cast<uint32_t>(r0) << 16);
+    // Outputs, and the first guess of delta: one row a thread.
+    const int r = r0 + lane, own = own0 + r;
     const bool live = own < own_rows;
     const long long own_row = (kDkv ? a.k0[f] : a.q0[f]) + own;
-    const uint32_t mine = tm + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    Row row{};
-    if (a.slopes && live)
-#pragma unroll
-      for (int c = 0; c < 3; ++c)
-        if (c < a.axes)
-          row.pos[c] = -static_cast<float>(kDkv ? a.kpos[own_row * a.kpos_stride + c] : a.qpos[own_row * a.qpos_stride + c]);
-    row.mul = (a.cap > 0.0f ? a.cap : a.scale) * kLog2e;
-    row.cap_in = a.cap > 0.0f ? 2.0f * a.scale * kLog2e / a.cap : 0.0f;
-    row.slope = a.slopes && !kDkv ? -a.slopes[own_head] * kLog2e / row.mul : 0.0f;
-    float delta = 0.0f;
     if (!kDkv) {
-      if (live) row.off = fmaf(-kLog2e, a.lse[static_cast<long long>(own_head) * a.queries + own_row], kUp);
       if (wg == 0) {
+        float delta = 0.0f;
         if (live) {
           const char* o = a.o.data + own_row * a.o.row + own_head * a.o.head;
           const char* g = a.dout.data + own_row * a.dout.row + own_head * a.dout.head;
@@ -420,32 +430,52 @@ __global__ void __launch_bounds__(kThreads, 1)
         sm.guess[r] = delta;
       }
       math_sync();
-      delta = sm.guess[r];
-      row.delta = -delta;
     }
+    Rows row{};
+    row.mul = (a.cap > 0.0f ? a.cap : a.scale) * kLog2e;
+    row.cap_in = a.cap > 0.0f ? 2.0f * a.scale * kLog2e / a.cap : 0.0f;
     // A place is seen if its column is at least `from` and below `to`.
-    int from = 0, to = other_rows;
-    if (a.causal) {
-      if (kDkv)
-        from = own < a.prefix[f] ? 0 : own - shift;
-      else
-        to = live ? limit(own) : 0;
+    int from[4], to[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int rx = r0 + 8 * x + (lane >> 2), ox = own0 + rx;
+      const bool in = ox < own_rows;
+      const long long at = (kDkv ? a.k0[f] : a.q0[f]) + ox;
+      from[x] = 0;
+      to[x] = other_rows;
+      if (a.causal) {
+        if (kDkv)
+          from[x] = ox < a.prefix[f] ? 0 : ox - shift;
+        else
+          to[x] = in ? limit(ox) : 0;
+      }
+      if (!kDkv) {
+        if (in) row.off[x] = fmaf(-kLog2e, a.lse[static_cast<long long>(own_head) * a.queries + at], kUp);
+        row.delta[x] = -sm.guess[rx];
+      }
+      if (a.slopes && in) {
+        if (!kDkv) row.slope[x] = -a.slopes[own_head] * kLog2e / row.mul;
+#pragma unroll
+        for (int c = 0; c < 3; ++c)
+          if (c < a.axes)
+            row.pos[c][x] = -static_cast<float>(kDkv ? a.kpos[at * a.kpos_stride + c] : a.qpos[at * a.qpos_stride + c]);
+      }
     }
     const int c0 = wg * kCols;
     const uint32_t s_at = mine + c0, dp_at = mine + 128 + c0;
     bool ok = true;
     // One step with the cap and the mask as compile-time choices.
-    auto step = [&](auto cap, auto mask, int n, const float(*side)[kOther]) {
+    auto step = [&](auto cap, auto mask, int n, const float* side) {
       constexpr bool kCap = decltype(cap)::value, kMask = decltype(mask)::value;
-      float e[kCols];
-      uint32_t whole_p[kCap && !kDkv ? kCols / 2 : 1];
-      probabilities<T, kDkv, kCap, kMask>(s_at, side, c0, a.axes, row, e, whole_p);
+      float e[2][kElems];
+      uint32_t whole_p[2][kElems / 2];
+      probabilities<T, kDkv, kCap, kMask>(s_at, side, a.axes, row, e, whole_p);
       tc_wait_st();
       tc_before();
       warp_arrive(&sm.p_full);
       if (!(ok = warp_wait(&sm.dp_full, n & 1, given_up))) return;
       tc_after();
-      gradients<T, kDkv, kCap, kMask>(dp_at, side, c0, row, e, whole_p);
+      gradients<T, kDkv, kCap, kMask>(dp_at, side, row, e, whole_p);
       tc_wait_st();
       tc_before();
       warp_arrive(&sm.ds_full);
@@ -453,27 +483,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int n = 0; n < steps; ++n) {
       const int slot = n % kSides;
       if (sides && !(ok = warp_wait(&sm.side_full[slot], (n / kSides) & 1, given_up))) break;
-      if (kDkv && a.slopes) row.slope = -a.slopes[other_head(n)] * kLog2e / row.mul;
+      if (kDkv && a.slopes) {
+        const float slope = -a.slopes[other_head(n)] * kLog2e / row.mul;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) row.slope[x] = slope;
+      }
       const int row0 = other_row(n);
       // Seen whole: nothing of the tile is hidden from any of the block's rows.
       const bool whole = row0 + kOther <= other_rows &&
                          (!a.causal || (kDkv ? limit(row0) >= min(own0 + kOwn, nk) : limit(own0) >= row0 + kOther));
-      row.lo = from - row0;
-      row.hi = to - row0;
+      if (!whole) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          row.lo[x] = from[x] - row0 - c0 - 2 * quad;
+          row.hi[x] = to[x] - row0 - c0 - 2 * quad;
+        }
+      }
       if (!(ok = warp_wait(&sm.s_full, n & 1, given_up))) break;
       tc_after();
       using Yes = std::true_type;
       using No = std::false_type;
+      const float* side = &sm.side[slot][0][c0 + 2 * quad];
       if (a.cap > 0.0f) {
         if (whole)
-          step(Yes{}, No{}, n, sm.side[slot]);
+          step(Yes{}, No{}, n, side);
         else
-          step(Yes{}, Yes{}, n, sm.side[slot]);
+          step(Yes{}, Yes{}, n, side);
       } else {
         if (whole)
-          step(No{}, No{}, n, sm.side[slot]);
+          step(No{}, No{}, n, side);
         else
-          step(No{}, Yes{}, n, sm.side[slot]);
+          step(No{}, Yes{}, n, side);
       }
       if (!ok) break;
       if (sides) warp_arrive(&sm.side_empty[slot]);
@@ -483,11 +523,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (any && ok) ok = warp_wait(&sm.acc_full, 0, given_up);
     tc_after();
     // dq: the sum of P (dP - delta) is what delta is off by.
+    float total = 0.0f;
     if (!kDkv) {
-      sm.rest[wg][r] = row.total;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        row.total[x] += __shfl_xor_sync(0xFFFFFFFFu, row.total[x], 1);
+        row.total[x] += __shfl_xor_sync(0xFFFFFFFFu, row.total[x], 2);
+        if (quad == 0) sm.rest[wg][r0 + 8 * x + (lane >> 2)] = row.total[x];
+      }
       math_sync();
-      row.total = ((sm.rest[0][r] + sm.rest[1][r]) + (sm.rest[2][r] + sm.rest[3][r])) * kDown;
-      if (live && wg == 0) a.delta[static_cast<long long>(own_head) * a.queries + own_row] = delta + row.total;
+      total = ((sm.rest[0][r] + sm.rest[1][r]) + (sm.rest[2][r] + sm.rest[3][r])) * kDown;
+      if (live && wg == 0) a.delta[static_cast<long long>(own_head) * a.queries + own_row] = sm.guess[r] + total;
     }
     const float bad = !ok || *given_up ? __int_as_float(0x7FFFFFFF) : 1.0f;  // a wait ran out: nothing here is an answer
     const int which = wg & 1;  // dk, dv: 0 and 1
@@ -510,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int y = 0; y < 16; ++y) {
         float w = any ? __uint_as_float(c[y]) : 0.0f;
-        if (!kDkv && any) w = fmaf(-row.total, __uint_as_float(d[y]), w);
+        if (!kDkv && any) w = fmaf(-total, __uint_as_float(d[y]), w);
         v[y] = w * k1;
       }
 #pragma unroll

@@ -223,100 +223,132 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp < 8) {
-    // ---- softmax: one row a thread
+    // ---- softmax: 32 rows a warp, in fragments: four rows and 32 of their keys a thread
     regs_up<kRegsSoftmax>();
-    const int t = warp >> 2, r = threadIdx.x & (kRows - 1);
-    const int i = first[t] + (r >> a.pack_log2);
-    const int h = (hb << a.pack_log2) + (r & (pack - 1));
-    const bool live = i < nq;
-    const int lim = live ? limit(i) : nk;
-    const int clear = first[t] < nq ? limit(first[t]) : nk;  // tiles that end at or below this are seen whole
-    const uint32_t mine = tm + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const uint32_t sc = mine + t * 128, oc = mine + 256 + t * 64 * kBlocks;
-    const long long qrow = a.q0[f] + i;
-    float slope = 0.0f, qp[3] = {0.0f, 0.0f, 0.0f};
-    if (a.slopes && live) {
-      slope = -a.slopes[h] * kLog2e;
-#pragma unroll
-      for (int c = 0; c < 3; ++c)
-        if (c < a.axes) qp[c] = -static_cast<float>(a.qpos[qrow * a.qpos_stride + c]);
-    }
+    const int t = warp >> 2, r0 = (warp & 3) * 32, quad = lane & 3;
+    const uint32_t mine = tm + (static_cast<uint32_t>(r0) << 16), high = mine + (16u << 16);
+    const uint32_t sc = t * 128, oc = 256 + t * 64 * kBlocks;  // columns
+    // Row `x` of the thread is r0 + 8 x + lane / 4.
+    int lim[4];
+    float slope[4], qp[3][4];
     // What a score (the raw product, or tanh of it if capped) is multiplied by to
     // be in units of log2.
     const float mul = (a.cap > 0.0f ? a.cap : a.scale) * kLog2e;
     const float cap_in = a.cap > 0.0f ? 2.0f * a.scale * kLog2e / a.cap : 0.0f;
-    slope /= mul;
-    float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int r = r0 + 8 * x + (lane >> 2), i = first[t] + (r >> a.pack_log2);
+      lim[x] = i < nq ? limit(i) : nk;
+      slope[x] = 0.0f;
+#pragma unroll
+      for (int c = 0; c < 3; ++c) qp[c][x] = 0.0f;
+      if (a.slopes && i < nq) {
+        slope[x] = -a.slopes[(hb << a.pack_log2) + (r & (pack - 1))] * kLog2e / mul;
+#pragma unroll
+        for (int c = 0; c < 3; ++c)
+          if (c < a.axes) qp[c][x] = -static_cast<float>(a.qpos[static_cast<long long>(a.q0[f] + i) * a.qpos_stride + c]);
+      }
+    }
+    const int clear = first[t] < nq ? limit(first[t]) : nk;  // tiles that end at or below this are seen whole
+    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, sum[4] = {};
     bool ok = true;
     for (int j = js; j < last_j[t]; ++j) {
       const int n = j - js;
       if (!(ok = warp_wait(&sm.s_full[t], n & 1, given_up))) break;
       tc_after();
-      float u[kRows];
-      uint32_t* ur = reinterpret_cast<uint32_t*>(u);
-#pragma unroll
-      for (int x = 0; x < kRows; x += 32) tmem_ld32(sc + x, ur + x);
-      tc_wait_ld<kRows>(ur);
+      float u[2][64];
+      tmem_ld_16x256b_x16(mine + sc, reinterpret_cast<uint32_t*>(u[0]));
+      tmem_ld_16x256b_x16(high + sc, reinterpret_cast<uint32_t*>(u[1]));
+      tc_wait_ld<64>(reinterpret_cast<uint32_t*>(u[0]));
+      tc_wait_ld<64>(reinterpret_cast<uint32_t*>(u[1]));
       if (a.cap > 0.0f) {
 #pragma unroll
-        for (int x = 0; x < kRows; ++x) u[x] = tanh_half(u[x] * cap_in);
+        for (int x = 0; x < 128; ++x) u[x >> 6][x & 63] = tanh_half(u[x >> 6][x & 63] * cap_in);
       }
       if (a.slopes) {
         if (!(ok = warp_wait(&sm.pos_full[n % kPosSlots], (n / kPosSlots) & 1, given_up))) break;
-        const float(*pos)[kRows] = sm.pos[n % kPosSlots];
+        const float* pos = &sm.pos[n % kPosSlots][0][2 * quad];
         if (a.axes == 1)
-          lower<1, kRows>(u, pos[0], kRows, qp, slope);
+          lower<1, 16>(u, pos, kRows, qp, slope);
         else if (a.axes == 2)
-          lower<2, kRows>(u, pos[0], kRows, qp, slope);
+          lower<2, 16>(u, pos, kRows, qp, slope);
         else
-          lower<3, kRows>(u, pos[0], kRows, qp, slope);
+          lower<3, 16>(u, pos, kRows, qp, slope);
         warp_arrive(&sm.pos_empty[n % kPosSlots]);
       }
       if ((j + 1) * kRows > clear) {
-        const int seen = lim - j * kRows;
 #pragma unroll
-        for (int x = 0; x < kRows; ++x) u[x] = x < seen ? u[x] : -INFINITY;
-      }
-      float m[4] = {u[0], u[1], u[2], u[3]};
-#pragma unroll
-      for (int x = 4; x < kRows; x += 8)
-#pragma unroll
-        for (int y = 0; y < 4; ++y)
-          if (x + 2 * y + 1 < kRows) m[y] = max3(m[y], u[x + 2 * y], u[x + 2 * y + 1]);
-      const float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * mul;
-      const bool rise = most > top + kLazy;  // -inf + 8 is -inf: any first score is a rise
-      if (j == js) {
-        if (rise) top = most;
-      } else if (__any_sync(0xFFFFFFFFu, rise)) {
-        const float by = rise ? exp2_fast(top - most) : 1.0f;
-        if (rise) top = most;
-        sum *= by;
-        for (int x = 0; x < a.Dn; x += 16) {
-          uint32_t o[16];
-          tmem_ld16(oc + x, o);
-          tc_wait_ld<16>(o);
-#pragma unroll
-          for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * by);
-          tmem_st16(oc + x, o);
+        for (int x = 0; x < 128; ++x) {
+          const int row = (x >> 6) * 2 + ((x >> 1) & 1), col = ((x & 63) >> 2) * 8 + (x & 1);
+          u[x >> 6][x & 63] = col < lim[row] - j * kRows - 2 * quad ? u[x >> 6][x & 63] : -INFINITY;
         }
       }
-      const float base = top == -INFINITY ? 0.0f : -top;
-      float s0 = 0.0f, s1 = 0.0f;
+      float most[4];
 #pragma unroll
-      for (int y = 0; y < kRows; y += 64) {
+      for (int row = 0; row < 4; ++row) {
+        const float* x = u[row >> 1] + 2 * (row & 1);
+        float m0 = fmaxf(x[0], x[1]), m1 = fmaxf(x[4], x[5]);
+#pragma unroll
+        for (int k = 2; k < 16; k += 2) {
+          m0 = max3(m0, x[4 * k], x[4 * k + 1]);
+          m1 = max3(m1, x[4 * k + 4], x[4 * k + 5]);
+        }
+        most[row] = fmaxf(m0, m1);
+      }
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1)
+#pragma unroll
+        for (int row = 0; row < 4; ++row) most[row] = fmaxf(most[row], __shfl_xor_sync(0xFFFFFFFFu, most[row], o));
+      bool rise = false;
+#pragma unroll
+      for (int row = 0; row < 4; ++row) {
+        most[row] *= mul;
+        rise = rise || most[row] > top[row] + kLazy;  // -inf + 8 is -inf: any first score is a rise
+      }
+      if (__any_sync(0xFFFFFFFFu, rise)) {
+        float by[4];
+#pragma unroll
+        for (int row = 0; row < 4; ++row) {
+          const bool up = most[row] > top[row] + kLazy;
+          by[row] = up ? exp2_fast(top[row] - most[row]) : 1.0f;
+          if (up) top[row] = most[row];
+          sum[row] *= by[row];
+        }
+        if (j > js)
+          for (int x = 0; x < a.Dn; x += 16) {
+            uint32_t o[2][8];
+            tmem_ld_16x256b_x2(mine + oc + x, o[0]);
+            tmem_ld_16x256b_x2(high + oc + x, o[1]);
+            tc_wait_ld<8>(o[0]);
+            tc_wait_ld<8>(o[1]);
+#pragma unroll
+            for (int y = 0; y < 16; ++y)
+              o[y >> 3][y & 7] = __float_as_uint(__uint_as_float(o[y >> 3][y & 7]) * by[(y >> 3) * 2 + ((y >> 1) & 1)]);
+            tmem_st_16x256b_x2(mine + oc + x, o[0]);
+            tmem_st_16x256b_x2(high + oc + x, o[1]);
+          }
+      }
+      float base[4];
+#pragma unroll
+      for (int row = 0; row < 4; ++row) base[row] = top[row] == -INFINITY ? 0.0f : -top[row];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
         uint32_t p[32];
+        float s[4] = {};
 #pragma unroll
         for (int x = 0; x < 64; x += 2) {
+          const int row = 2 * h + ((x >> 1) & 1);
           float e0, e1;
-          fma2(e0, e1, u[y + x], u[y + x + 1], mul, mul, base, base);
+          fma2(e0, e1, u[h][x], u[h][x + 1], mul, mul, base[row], base[row]);
           e0 = exp2_fast(e0);
           e1 = exp2_fast(e1);
-          add2(s0, s1, s0, s1, e0, e1);
+          add2(s[x & 2], s[(x & 2) + 1], s[x & 2], s[(x & 2) + 1], e0, e1);
           p[x >> 1] = pack2<T>(e0, e1);
         }
-        tmem_st32(sc + (y >> 1), p);
+        tmem_st_16x128b_x16((h ? high : mine) + sc, p);
+        sum[2 * h] += s[0] + s[1];
+        sum[2 * h + 1] += s[2] + s[3];
       }
-      sum += s0 + s1;
       tc_wait_st();
       tc_before();
       warp_arrive(&sm.p_full[t]);
@@ -327,12 +359,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n = j - js;
         if ((ok = warp_wait(&sm.pos_full[n % kPosSlots], (n / kPosSlots) & 1, given_up))) warp_arrive(&sm.pos_empty[n % kPosSlots]);
       }
-    // ---- output
+    // ---- output: one row a thread, its statistics fetched from the fragments' threads
     const bool any = last_j[t] > js;
+    float row_sum = 0.0f, row_top = 0.0f;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      sum[x] += __shfl_xor_sync(0xFFFFFFFFu, sum[x], 1);
+      sum[x] += __shfl_xor_sync(0xFFFFFFFFu, sum[x], 2);
+      const float s = __shfl_sync(0xFFFFFFFFu, sum[x], (lane & 7) * 4), m = __shfl_sync(0xFFFFFFFFu, top[x], (lane & 7) * 4);
+      if (lane >> 3 == x) row_sum = s, row_top = m;
+    }
+    const int r = r0 + lane, i = first[t] + (r >> a.pack_log2), h = (hb << a.pack_log2) + (r & (pack - 1));
+    const bool live = i < nq;
+    const long long qrow = a.q0[f] + i;
     if (any && ok) ok = warp_wait(&sm.o_full[t], 0, given_up);
     tc_after();
     const bool parts = a.part_o != nullptr;
-    float by = parts ? 1.0f : sum > 0.0f ? 1.0f / sum : 0.0f;
+    float by = parts ? 1.0f : row_sum > 0.0f ? 1.0f / row_sum : 0.0f;
     if (!ok || *given_up) by = __int_as_float(0x7FFFFFFF);  // a wait ran out: nothing here is an answer
     char* out = a.o.data + qrow * a.o.row + h * a.o.head;
     float* part = parts ? a.part_o + ((static_cast<long long>(split) * a.queries + qrow) * a.H + h) * a.D : nullptr;
@@ -340,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t o[16];
       float v[16];
       if (any) {
-        tmem_ld16(oc + x, o);
+        tmem_ld16(mine + oc + x, o);
         tc_wait_ld<16>(o);
       }
 #pragma unroll
@@ -360,9 +403,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (live) {
       const long long at = static_cast<long long>(h) * a.queries + qrow;
       if (parts)
-        a.part_ml[(static_cast<long long>(split) * a.queries + qrow) * a.H + h] = make_float2(top, sum);
+        a.part_ml[(static_cast<long long>(split) * a.queries + qrow) * a.H + h] = make_float2(row_top, row_sum);
       else if (a.lse)
-        a.lse[at] = sum > 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+        a.lse[at] = row_sum > 0.0f ? (row_top + log2f(row_sum)) * kLn2 : -INFINITY;
     }
     tc_before();
   }

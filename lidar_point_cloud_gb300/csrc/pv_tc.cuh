@@ -147,6 +147,67 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
       : "memory");
 }
 
+// Fragments of 16 lanes: register 4 k + 2 r + c of a 16x256b load is row
+// lane / 4 + 8 r, column 8 k + 2 (lane % 4) + c; register 2 k + r of a 16x128b store
+// is row lane / 4 + 8 r, column 4 k + lane % 4.
+__device__ __forceinline__ void tmem_ld_16x256b_x16(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, "
+      "%22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, "
+      "%42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, "
+      "%62, %63}, [%64];"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_ld_16x256b_x2(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st_16x256b_x2(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_16x128b_x16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, "
+      "%23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+            "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
+        "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),
+        "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+
 // ------------------------------------------------------------ tcgen05.mma
 
 // Shared-memory operand in 128-byte swizzled rows (64 16-bit elements), 8 rows
@@ -248,22 +309,33 @@ __device__ __forceinline__ void add2(float& x0, float& x1, float a0, float a1, f
 // tanh(x / (2 log2(e))) = 1 - 2 / (1 + 2^x): a few 2^-24 off, absolutely.
 __device__ __forceinline__ float tanh_half(float x) { return fmaf(-2.0f, rcp_fast(1.0f + exp2_fast(x)), 1.0f); }
 
-// u += slope * distance between a row's position (negated, in `own`) and those of
-// n columns, axis after axis `stride` floats apart.
-template <int kAxes, int n>
-__device__ __forceinline__ void lower(float* u, const float* pos, int stride, const float* own, float slope) {
+// A fragment's scores lowered by the distance of a row's position (negated, own[axis][row])
+// and a column's: u[half][4 k + 2 r + c] += slope[2 half + r] * distance, for the columns of
+// which `pos` is the first of this thread, axes `stride` floats apart.  Four rows a
+// thread share what is loaded of a column: a thread for each row would load every
+// column's position by itself, and a load that all lanes of a warp share takes the
+// shared memory as long as one of 512 different bytes.
+template <int kAxes, int kGroups8>
+__device__ __forceinline__ void lower(float (*u)[4 * kGroups8], const float* pos, int stride, const float (*own)[4],
+                                      const float* slope) {
 #pragma unroll
-  for (int x = 0; x < n; x += 4) {
-    float d[4];
+  for (int k = 0; k < kGroups8; ++k) {
+    float2 v[kAxes];
 #pragma unroll
-    for (int c = 0; c < kAxes; ++c) {
-      const float4 v = *reinterpret_cast<const float4*>(pos + c * stride + x);
-      const float e[4] = {v.x + own[c], v.y + own[c], v.z + own[c], v.w + own[c]};
+    for (int c = 0; c < kAxes; ++c) v[c] = *reinterpret_cast<const float2*>(pos + c * stride + 8 * k);
 #pragma unroll
-      for (int y = 0; y < 4; ++y) d[y] = c ? d[y] + fabsf(e[y]) : fabsf(e[y]);
+    for (int row = 0; row < 4; ++row) {
+      float d0 = 0.0f, d1 = 0.0f;
+#pragma unroll
+      for (int c = 0; c < kAxes; ++c) {
+        float e0, e1;
+        add2(e0, e1, v[c].x, v[c].y, own[c][row], own[c][row]);
+        d0 = c ? d0 + fabsf(e0) : fabsf(e0);
+        d1 = c ? d1 + fabsf(e1) : fabsf(e1);
+      }
+      float* const x = &u[row >> 1][4 * k + 2 * (row & 1)];
+      fma2(x[0], x[1], d0, d1, slope[row], slope[row], x[0], x[1]);
     }
-#pragma unroll
-    for (int y = 0; y < 4; ++y) u[x + y] = fmaf(slope, d[y], u[x + y]);
   }
 }
 
