@@ -382,23 +382,53 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == kIssue + 2) {
-    // ---- what belongs to the other side's rows
-    if (sides) {
+    // ---- what belongs to the other side's rows, each tile's loaded while the last
+    // one's are handed over
+    if (sides && steps > 0) {
+      int pos[3][4];
+      float lse[4], delta[4];
+      int head = head0, tile = 0;  // of the tile to load
+      auto load = [&]() {
+        const int row0 = (other_tile0 + tile) * kOther;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const long long row = (kDkv ? a.q0[f] : a.k0[f]) + min(row0 + x * 32 + lane, other_rows - 1);
+          if (kDkv) {
+            lse[x] = a.lse[static_cast<long long>(head) * a.queries + row];
+            delta[x] = a.delta[static_cast<long long>(head) * a.queries + row];
+          }
+          const int32_t* p = kDkv ? a.qpos + row * a.qpos_stride : a.kpos + row * a.kpos_stride;
+#pragma unroll
+          for (int c = 0; c < 3; ++c)
+            if (c < a.axes) pos[c][x] = p[c];
+        }
+        if (++tile == per_head) tile = 0, ++head;
+      };
+      load();
       for (int n = 0; n < steps; ++n) {
         const int slot = n % kSides;
-        if (!warp_wait(&sm.side_empty[slot], ((n / kSides) & 1) ^ 1, given_up)) break;
-        const int h = other_head(n), row0 = other_row(n);
+        float now[5][4];
 #pragma unroll
-        for (int x = lane; x < kOther; x += 32) {
-          const bool in = row0 + x < other_rows;
-          const long long row = (kDkv ? a.q0[f] : a.k0[f]) + row0 + x;
+        for (int x = 0; x < 4; ++x) {
           if (kDkv) {
-            sm.side[slot][0][x] = in ? fmaf(-kLog2e, a.lse[static_cast<long long>(h) * a.queries + row], kUp) : 0.0f;
-            sm.side[slot][1][x] = in ? -a.delta[static_cast<long long>(h) * a.queries + row] : 0.0f;
+            now[0][x] = fmaf(-kLog2e, lse[x], kUp);
+            now[1][x] = -delta[x];
           }
-          for (int c = 0; c < a.axes; ++c)
-            sm.side[slot][2 + c][x] =
-                in ? static_cast<float>(kDkv ? a.qpos[row * a.qpos_stride + c] : a.kpos[row * a.kpos_stride + c]) : 0.0f;
+#pragma unroll
+          for (int c = 0; c < 3; ++c)
+            if (c < a.axes) now[2 + c][x] = static_cast<float>(pos[c][x]);
+        }
+        if (n + 1 < steps) load();
+        if (!warp_wait(&sm.side_empty[slot], ((n / kSides) & 1) ^ 1, given_up)) break;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          if (kDkv) {
+            sm.side[slot][0][x * 32 + lane] = now[0][x];
+            sm.side[slot][1][x * 32 + lane] = now[1][x];
+          }
+#pragma unroll
+          for (int c = 0; c < 3; ++c)
+            if (c < a.axes) sm.side[slot][2 + c][x * 32 + lane] = now[2 + c][x];
         }
         warp_arrive(&sm.side_full[slot]);
       }
@@ -480,15 +510,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_before();
       warp_arrive(&sm.ds_full);
     };
-    for (int n = 0; n < steps; ++n) {
+    int head = head0, left = 0, row0 = 0;  // dk, dv: the other side's head and its tiles to come
+    for (int n = 0; n < steps; ++n, row0 += kOther) {
       const int slot = n % kSides;
-      if (sides && !(ok = warp_wait(&sm.side_full[slot], (n / kSides) & 1, given_up))) break;
-      if (kDkv && a.slopes) {
-        const float slope = -a.slopes[other_head(n)] * kLog2e / row.mul;
+      if (left-- == 0) {
+        left = per_head - 1;
+        row0 = other_tile0 * kOther;
+        if (kDkv && a.slopes) {
+          const float slope = -a.slopes[head] * kLog2e / row.mul;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) row.slope[x] = slope;
+          for (int x = 0; x < 4; ++x) row.slope[x] = slope;
+        }
+        ++head;
       }
-      const int row0 = other_row(n);
+      if (sides && !(ok = warp_wait(&sm.side_full[slot], (n / kSides) & 1, given_up))) break;
       // Seen whole: nothing of the tile is hidden from any of the block's rows.
       const bool whole = row0 + kOther <= other_rows &&
                          (!a.causal || (kDkv ? limit(row0) >= min(own0 + kOwn, nk) : limit(own0) >= row0 + kOther));

@@ -38,7 +38,7 @@ constexpr int kThreads = 384;
 // 128 x 80 = 63,488.
 constexpr int kRegsSoftmax = 208, kRegsOther = 80;
 constexpr int kRows = 128;      // rows of a query tile, keys of a key tile
-constexpr int kPosSlots = 2;
+constexpr int kPosSlots = 4;
 constexpr float kLazy = 8.0f;   // log2 of how far scores may rise over the kept maximum
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -208,17 +208,35 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 10) {
-    // ---- key positions
-    if (a.slopes) {
+    // ---- key positions, each tile's loaded while the last one's are handed over
+    if (a.slopes && je > js) {
+      int next[3][4];
+      auto load = [&](int j) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int key = j * kRows + x * 32 + lane;
+          const int32_t* p = a.kpos + static_cast<long long>(a.k0[f] + min(key, nk - 1)) * a.kpos_stride;
+#pragma unroll
+          for (int c = 0; c < 3; ++c)
+            if (c < a.axes) next[c][x] = p[c];
+        }
+      };
+      load(js);
       for (int j = js; j < je; ++j) {
         const int n = j - js, slot = n % kPosSlots;
+        float now[3][4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+          for (int c = 0; c < 3; ++c)
+            if (c < a.axes) now[c][x] = static_cast<float>(next[c][x]);
+        if (j + 1 < je) load(j + 1);
         if (!warp_wait(&sm.pos_empty[slot], ((n / kPosSlots) & 1) ^ 1, given_up)) break;
-        for (int x = lane; x < kRows; x += 32) {
-          const int key = j * kRows + x;
-          for (int c = 0; c < a.axes; ++c)
-            sm.pos[slot][c][x] =
-                key < nk ? static_cast<float>(a.kpos[static_cast<long long>(a.k0[f] + key) * a.kpos_stride + c]) : 0.0f;
-        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+          for (int c = 0; c < 3; ++c)
+            if (c < a.axes) sm.pos[slot][c][x * 32 + lane] = now[c][x];
         warp_arrive(&sm.pos_full[slot]);
       }
     }
