@@ -113,10 +113,21 @@ int chunk_of(const AttnArgs& a, int heads, int sms) {
   return best;
 }
 
-// Tiles of `own` rows along frames with row offsets `off`; how many there are.
-int tiles_of(AttnArgs& a, const int* off, int own) {
-  for (int b = 0; b < a.frames; ++b) a.tile0[b + 1] = a.tile0[b] + (off[b + 1] - off[b] + own - 1) / own;
-  return a.tile0[a.frames];
+// The blocks' list: count(f) tiles of each frame, the frames in the order of the rows
+// that their tiles walk (`walk`: the other side's row offsets), most first, so that
+// the last blocks to start are short ones.  Returns how many tiles there are.
+template <typename F>
+int list_tiles(AttnArgs& a, const int* walk, F count) {
+  for (int b = 0; b < a.frames; ++b) a.order[b] = static_cast<unsigned char>(b);
+  std::stable_sort(a.order, a.order + a.frames, [&](unsigned char x, unsigned char y) {
+    return walk[x + 1] - walk[x] > walk[y + 1] - walk[y];
+  });
+  int64_t n = 0;
+  for (int i = 0; i < a.frames; ++i) {
+    n += count(a.order[i]);
+    a.tile0[i + 1] = static_cast<int>(n);
+  }
+  return n * a.heads < (int64_t(1) << 31) ? static_cast<int>(n) : -1;
 }
 
 }  // namespace
@@ -177,12 +188,14 @@ extern "C" int pv_attention(const pv_attention_params* params, const pv_heads* q
   if (sms < 1) return PV_ERR_CUDA;
   a.chunk = chunk_of(a, heads, sms);
   int parts = 1;
-  for (int f = 0; f < a.frames; ++f) {
-    const int rows = static_cast<int>(((static_cast<int64_t>(a.q0[f + 1] - a.q0[f]) << a.pack_log2) + 255) / 256);
+  a.heads = heads;
+  const int tiles = list_tiles(a, a.k0, [&](int f) {
+    const int64_t rows = ((static_cast<int64_t>(a.q0[f + 1] - a.q0[f]) << a.pack_log2) + 255) / 256;
     const int splits = std::max(1, ((a.k0[f + 1] - a.k0[f] + 127) / 128 + a.chunk - 1) / a.chunk);
-    a.tile0[f + 1] = a.tile0[f] + rows * splits;
     parts = std::max(parts, splits);
-  }
+    return rows * splits;
+  });
+  if (tiles < 0) return PV_ERR_TOO_LARGE;
   Scratch scratch;
   if (parts > 1) {
     const size_t rows = static_cast<size_t>(parts) * nq * a.H;
@@ -198,7 +211,7 @@ extern "C" int pv_attention(const pv_attention_params* params, const pv_heads* q
              (st = make_map(&m.v, a.v, params->dtype, a.D, a.Hk, 1, nk, 128)) != PV_OK) {
     return st;
   }
-  return attn_forward(a, params->dtype, m, dim3(a.tile0[a.frames], heads), reinterpret_cast<cudaStream_t>(stream));
+  return attn_forward(a, params->dtype, m, dim3(tiles * heads), reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" int pv_attention_backward(const pv_attention_params* params, const pv_heads* dout, const pv_heads* q,
@@ -231,12 +244,13 @@ extern "C" int pv_attention_backward(const pv_attention_params* params, const pv
   a.dv = view_of(dv);
   const int sms = sm_count(dev);
   if (sms < 1) return PV_ERR_CUDA;
-  const int key_tiles = tiles_of(a, a.k0, 128);
+  int64_t key_tiles = 0;
+  for (int f = 0; f < a.frames; ++f) key_tiles += (a.k0[f + 1] - a.k0[f] + 127) / 128;
   // A key head's block walks the queries of all heads that share it: with few
   // blocks for the multiprocessors (under a causal mask of unequal length too) the
   // heads are cut into parts, joined by one more kernel.
   a.head_parts = 1;
-  while (a.G % (2 * a.head_parts) == 0 && static_cast<int64_t>(key_tiles) * a.Hk * a.head_parts < 4 * sms) a.head_parts *= 2;
+  while (a.G % (2 * a.head_parts) == 0 && key_tiles * a.Hk * a.head_parts < 4 * sms) a.head_parts *= 2;
   Scratch scratch;
   const size_t rows = round_up(static_cast<size_t>(nq) * a.H, 4);
   const size_t parts = a.head_parts > 1 ? static_cast<size_t>(2) * a.head_parts * nk * a.Hk * a.D : 0;
@@ -253,8 +267,12 @@ extern "C" int pv_attention_backward(const pv_attention_params* params, const pv
     return st;
   if (!nk) m.k = m.v = m.q;  // nothing is loaded through these
   if (!nq) m.q = m.dout = m.k;
-  int n = tiles_of(a, a.q0, 128);
-  if ((st = attn_backward_dq(a, params->dtype, m, dim3(n, a.H), cs)) != PV_OK) return st;
-  n = tiles_of(a, a.k0, 128);
-  return attn_backward_dkv(a, params->dtype, m, dim3(n, a.Hk * a.head_parts), cs);
+  AttnArgs b = a;
+  a.heads = a.H;
+  b.heads = a.Hk * a.head_parts;
+  const int q_tiles = list_tiles(a, a.k0, [&](int f) { return (a.q0[f + 1] - a.q0[f] + 127) / 128; });
+  const int k_tiles = list_tiles(b, a.q0, [&](int f) { return (a.k0[f + 1] - a.k0[f] + 127) / 128; });
+  if (q_tiles < 0 || k_tiles < 0) return PV_ERR_TOO_LARGE;
+  if ((st = attn_backward_dq(a, params->dtype, m, dim3(q_tiles * a.heads), cs)) != PV_OK) return st;
+  return attn_backward_dkv(b, params->dtype, m, dim3(k_tiles * b.heads), cs);
 }

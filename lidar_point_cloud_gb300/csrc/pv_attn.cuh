@@ -32,8 +32,12 @@ struct AttnArgs {
   float2* part_ml; // split keys: [split, queries, H] maximum (in units of log2) and sum
   int q0[PV_MAX_FRAMES + 1];    // row offsets of the frames
   int k0[PV_MAX_FRAMES + 1];
-  int tile0[PV_MAX_FRAMES + 1]; // first tile of each frame
   int prefix[PV_MAX_FRAMES];
+  // The blocks' list: frames by their work, most first, and the first tile of each in
+  // that order.  Block b takes tile b / heads of it for head b % heads.
+  unsigned char order[PV_MAX_FRAMES];
+  int tile0[PV_MAX_FRAMES + 1];
+  int heads;
 };
 
 struct AttnMaps {

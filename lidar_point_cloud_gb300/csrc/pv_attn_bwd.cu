@@ -211,16 +211,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   // ---- which rows
-  const int f = frame_of(a.tile0, a.frames, blockIdx.x);
+  const int tile = blockIdx.x / a.heads, place = frame_of(a.tile0, a.frames, tile), f = a.order[place];
+  const int head = blockIdx.x - tile * a.heads;
   const int nq = a.q0[f + 1] - a.q0[f], nk = a.k0[f + 1] - a.k0[f], shift = nk - nq;
-  const int local = blockIdx.x - a.tile0[f], tiles = a.tile0[f + 1] - a.tile0[f];
+  const int local = tile - a.tile0[place], tiles = a.tile0[place + 1] - a.tile0[place];
   // Under a causal mask late queries and early keys have the most work: they go first.
   const int own0 = (kDkv ? local : tiles - 1 - local) * kOwn;
   auto limit = [&](int i) { return a.causal ? max(min(max(i + shift + 1, a.prefix[f]), nk), 0) : nk; };
   // dk, dv: the query heads of a key head may be cut into parts, a block each.
-  const int own_head = kDkv ? blockIdx.y / a.head_parts : blockIdx.y;
+  const int own_head = kDkv ? head / a.head_parts : head;
   const int heads = kDkv ? a.G / a.head_parts : 1;
-  const int head0 = kDkv ? blockIdx.y * heads : own_head / a.G;
+  const int head0 = kDkv ? head * heads : own_head / a.G;
   int other_tile0 = 0, per_head;
   if (kDkv) {
     const int begin = a.causal && own0 >= a.prefix[f] ? max(own0 - shift, 0) : 0;
@@ -387,22 +388,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (sides && steps > 0) {
       int pos[3][4];
       float lse[4], delta[4];
-      int head = head0, tile = 0;  // of the tile to load
+      int h = head0, t = 0;  // head and tile to load
       auto load = [&]() {
-        const int row0 = (other_tile0 + tile) * kOther;
+        const int row0 = (other_tile0 + t) * kOther;
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           const long long row = (kDkv ? a.q0[f] : a.k0[f]) + min(row0 + x * 32 + lane, other_rows - 1);
           if (kDkv) {
-            lse[x] = a.lse[static_cast<long long>(head) * a.queries + row];
-            delta[x] = a.delta[static_cast<long long>(head) * a.queries + row];
+            lse[x] = a.lse[static_cast<long long>(h) * a.queries + row];
+            delta[x] = a.delta[static_cast<long long>(h) * a.queries + row];
           }
           const int32_t* p = kDkv ? a.qpos + row * a.qpos_stride : a.kpos + row * a.kpos_stride;
 #pragma unroll
           for (int c = 0; c < 3; ++c)
             if (c < a.axes) pos[c][x] = p[c];
         }
-        if (++tile == per_head) tile = 0, ++head;
+        if (++t == per_head) t = 0, ++h;
       };
       load();
       for (int n = 0; n < steps; ++n) {
@@ -510,18 +511,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_before();
       warp_arrive(&sm.ds_full);
     };
-    int head = head0, left = 0, row0 = 0;  // dk, dv: the other side's head and its tiles to come
+    int next_head = head0, left = 0, row0 = 0;  // dk, dv: the other side's next head, and the tiles to come of this one
     for (int n = 0; n < steps; ++n, row0 += kOther) {
       const int slot = n % kSides;
       if (left-- == 0) {
         left = per_head - 1;
         row0 = other_tile0 * kOther;
         if (kDkv && a.slopes) {
-          const float slope = -a.slopes[head] * kLog2e / row.mul;
+          const float slope = -a.slopes[next_head] * kLog2e / row.mul;
 #pragma unroll
           for (int x = 0; x < 4; ++x) row.slope[x] = slope;
         }
-        ++head;
+        ++next_head;
       }
       if (sides && !(ok = warp_wait(&sm.side_full[slot], (n / kSides) & 1, given_up))) break;
       // Seen whole: nothing of the tile is hidden from any of the block's rows.
@@ -575,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const View& out = kDkv ? (which ? a.dv : a.dk) : a.dq;
     char* to_row = out.data + own_row * out.row + own_head * out.head;
     const bool parts = kDkv && a.head_parts > 1;
-    float* part = parts ? a.part_o + (((static_cast<long long>(blockIdx.y % a.head_parts) * 2 + which) * a.keys + own_row) * a.Hk + own_head) * a.D
+    float* part = parts ? a.part_o + (((static_cast<long long>(head % a.head_parts) * 2 + which) * a.keys + own_row) * a.Hk + own_head) * a.D
                         : nullptr;
     const float k1 = (kDkv && which ? 1.0f : a.scale) * kDown * bad;
     const uint32_t acc = mine + 256 + (kDkv && which ? 64 * kBlocks : 0);

@@ -71,14 +71,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   // ---- which rows, which keys
-  const int f = frame_of(a.tile0, a.frames, blockIdx.x);
+  const int tile = blockIdx.x / a.heads, place = frame_of(a.tile0, a.frames, tile), f = a.order[place];
   const int nq = a.q0[f + 1] - a.q0[f], nk = a.k0[f + 1] - a.k0[f];
   const int pack = 1 << a.pack_log2;
   const int mblocks = (((nq << a.pack_log2) + 2 * kRows - 1) / (2 * kRows));
-  const int local = blockIdx.x - a.tile0[f];
+  const int local = tile - a.tile0[place];
   // Later rows see more keys under a causal mask: they go first.
   const int mb = mblocks - 1 - local % mblocks, split = local / mblocks;
-  const int hb = blockIdx.y;  // block of `pack` heads
+  const int hb = blockIdx.x - tile * a.heads;  // block of `pack` heads
   const int kh = (hb << a.pack_log2) / a.G;
   // Keys that query i sees: all below this.
   auto limit = [&](int i) { return a.causal ? max(min(max(i + nk - nq + 1, a.prefix[f]), nk), 0) : nk; };
@@ -311,22 +311,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           m0 = max3(m0, x[4 * k], x[4 * k + 1]);
           m1 = max3(m1, x[4 * k + 4], x[4 * k + 5]);
         }
-        most[row] = fmaxf(m0, m1);
+        most[row] = fmaxf(m0, m1) * mul;
       }
-#pragma unroll
-      for (int o = 1; o < 4; o <<= 1)
-#pragma unroll
-        for (int row = 0; row < 4; ++row) most[row] = fmaxf(most[row], __shfl_xor_sync(0xFFFFFFFFu, most[row], o));
-      bool rise = false;
-#pragma unroll
-      for (int row = 0; row < 4; ++row) {
-        most[row] *= mul;
-        rise = rise || most[row] > top[row] + kLazy;  // -inf + 8 is -inf: any first score is a rise
-      }
+      // -inf + 8 is -inf: any first score is a rise.  Only if some thread's own share of a
+      // row rises are the shares of a row joined.
+      const bool rise = most[0] > top[0] + kLazy || most[1] > top[1] + kLazy || most[2] > top[2] + kLazy || most[3] > top[3] + kLazy;
       if (__any_sync(0xFFFFFFFFu, rise)) {
         float by[4];
 #pragma unroll
         for (int row = 0; row < 4; ++row) {
+          most[row] = fmaxf(most[row], __shfl_xor_sync(0xFFFFFFFFu, most[row], 1));
+          most[row] = fmaxf(most[row], __shfl_xor_sync(0xFFFFFFFFu, most[row], 2));
           const bool up = most[row] > top[row] + kLazy;
           by[row] = up ? exp2_fast(top[row] - most[row]) : 1.0f;
           if (up) top[row] = most[row];
