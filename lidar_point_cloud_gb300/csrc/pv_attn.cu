@@ -83,28 +83,34 @@ int pack_of(int G) {
   return p;
 }
 
-// How many key tiles a block takes.  A block's time goes by its key tiles, and
-// the blocks run in rounds of one a multiprocessor: of the counts that leave
-// some `kLeast` tiles a block, the one with the shortest rounds, where a join
-// and its second launch are worth `kJoin` tiles.
+// How many key tiles a block takes, by an estimate in units of a key tile's time (some
+// 1.5 us).  The blocks run in rounds of one a multiprocessor, a block's time being
+// its key tiles and some kBlock more to begin and end; with many blocks, longest first,
+// the rounds blur.  Keys cut into parts cost the parts' outputs (32-bit, written and
+// read again at some 5 TB/s) and kJoin for one more launch.
 int chunk_of(const AttnArgs& a, int heads, int sms) {
-  constexpr int kLeast = 2, kJoin = 4;
+  constexpr double kBlock = 2.0, kJoin = 2.0, kBytes = 7.5e6;
   int most = 1;
   for (int f = 0; f < a.frames; ++f) most = std::max(most, (a.k0[f + 1] - a.k0[f] + 127) / 128);
   auto cost = [&](int chunk) {
-    int64_t blocks = 0;
+    int64_t blocks = 0, work = 0;
     for (int f = 0; f < a.frames; ++f) {
-      const int64_t rows = static_cast<int64_t>(a.q0[f + 1] - a.q0[f]) << a.pack_log2;
+      const int64_t rows = ((static_cast<int64_t>(a.q0[f + 1] - a.q0[f]) << a.pack_log2) + 255) / 256;
       const int tiles = (a.k0[f + 1] - a.k0[f] + 127) / 128;
-      blocks += (rows + 255) / 256 * std::max(1, (tiles + chunk - 1) / chunk);
+      blocks += rows * std::max(1, (tiles + chunk - 1) / chunk);
+      work += rows * tiles;
     }
-    return (blocks * heads + sms - 1) / sms * (chunk + 1) + (chunk < most ? kJoin : 0);
+    const double rounds = static_cast<double>(blocks * heads) / sms;
+    const double even = static_cast<double>(work * heads) / sms + rounds * kBlock;
+    const double time = rounds >= 4.0 ? even + 0.5 * chunk : std::max(even, std::ceil(rounds) * (chunk + kBlock));
+    const int parts = (most + chunk - 1) / chunk;
+    return time + (parts > 1 ? kJoin + 8.0 * parts * a.queries * a.H * a.D / kBytes : 0.0);
   };
   int best = most;
-  int64_t least = cost(most);
-  for (int parts = 2; parts <= 64 && (most + parts - 1) / parts >= kLeast; ++parts) {
+  double least = cost(most);
+  for (int parts = 2; parts <= 64 && parts <= most; ++parts) {
     const int chunk = (most + parts - 1) / parts;
-    const int64_t c = cost(chunk);
+    const double c = cost(chunk);
     if (c < least) {
       least = c;
       best = chunk;
