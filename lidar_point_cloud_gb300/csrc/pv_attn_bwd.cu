@@ -94,13 +94,13 @@ __device__ __forceinline__ constexpr int col_of(int x) { return (x >> 2) * 8 + (
 
 // 32 rows' scores of 32 columns, from column `at` of tensor memory on, to 16 P there, in
 // the storage type.  `side` points to what belongs to the thread's first column.
-// u keeps what dS is made of: 16 P times the cap's slope; with a cap, dq also
-// needs 16 P itself (as half pairs in `whole_p`: only the small sum that mends
-// delta is made of it) and takes u for acc2.  One operation after the other over
-// all elements: an element's chain is long, 32 of them hide it.
+// u keeps what dS is made of: 16 P times the cap's slope; with a cap, dq takes that
+// for acc2 too, and what the slope took from 16 P, for the sum of P dP, goes to `rest`
+// as half pairs (a small share, of which the rounding does not show).  One operation
+// after the other over all elements: an element's chain is long, 32 of them hide it.
 template <typename T, bool kDkv, bool kCap, bool kMask>
 __device__ __forceinline__ void probabilities(uint32_t at, const float* side, int axes, const Rows& row, float (*u)[kElems],
-                                              uint32_t (*whole_p)[kElems / 2]) {
+                                              uint32_t (*rest)[kElems / 2]) {
   tmem_ld_16x256b_x4(at, reinterpret_cast<uint32_t*>(u[0]));
   tmem_ld_16x256b_x4(at + (16u << 16), reinterpret_cast<uint32_t*>(u[1]));
   tc_wait_ld<kElems>(reinterpret_cast<uint32_t*>(u[0]));
@@ -142,15 +142,15 @@ __device__ __forceinline__ void probabilities(uint32_t at, const float* side, in
       for (int x = 0; x < kElems; x += 2) p[x >> 1] = Pack<T>::two(u[h][x], u[h][x + 1]);
     }
     if (kCap) {
-      if (!kDkv) {
 #pragma unroll
-        for (int x = 0; x < kElems; x += 2) whole_p[h][x >> 1] = Pack<__half>::two(u[h][x], u[h][x + 1]);
-      }
-#pragma unroll
-      for (int x = 0; x < kElems; ++x) u[h][x] *= steep[h][x];
-      if (!kDkv) {
-#pragma unroll
-        for (int x = 0; x < kElems; x += 2) p[x >> 1] = Pack<T>::two(u[h][x], u[h][x + 1]);
+      for (int x = 0; x < kElems; x += 2) {
+        const float e0 = u[h][x] * steep[h][x], e1 = u[h][x + 1] * steep[h][x + 1];
+        if (!kDkv) {
+          rest[h][x >> 1] = Pack<__half>::two(u[h][x] - e0, u[h][x + 1] - e1);
+          p[x >> 1] = Pack<T>::two(e0, e1);
+        }
+        u[h][x] = e0;
+        u[h][x + 1] = e1;
       }
     }
     tmem_st_16x128b_x4(at + (h ? 16u << 16 : 0u), p);
@@ -160,7 +160,7 @@ __device__ __forceinline__ void probabilities(uint32_t at, const float* side, in
 // dP at column `at` to 16 dS there.
 template <typename T, bool kDkv, bool kCap, bool kMask>
 __device__ __forceinline__ void gradients(uint32_t at, const float* side, Rows& row, const float (*e)[kElems],
-                                          const uint32_t (*whole_p)[kElems / 2]) {
+                                          const uint32_t (*rest)[kElems / 2]) {
   float g[2][kElems];
   tmem_ld_16x256b_x4(at, reinterpret_cast<uint32_t*>(g[0]));
   tmem_ld_16x256b_x4(at + (16u << 16), reinterpret_cast<uint32_t*>(g[1]));
@@ -183,9 +183,9 @@ __device__ __forceinline__ void gradients(uint32_t at, const float* side, Rows& 
       s[x >> 1] = Pack<T>::two(v0, v1);
       if (!kDkv) {
         if (kCap) {
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&whole_p[h][x >> 1]));
-          v0 = seen0 ? g[h][x] * f.x : 0.0f;
-          v1 = seen1 ? g[h][x + 1] * f.y : 0.0f;
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&rest[h][x >> 1]));
+          v0 = seen0 ? g[h][x] * (e[h][x] + f.x) : 0.0f;
+          v1 = seen1 ? g[h][x + 1] * (e[h][x + 1] + f.y) : 0.0f;
         }
         add2(t[x & 2], t[(x & 2) + 1], t[x & 2], t[(x & 2) + 1], v0, v1);
       }
@@ -499,14 +499,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto step = [&](auto cap, auto mask, int n, const float* side) {
       constexpr bool kCap = decltype(cap)::value, kMask = decltype(mask)::value;
       float e[2][kElems];
-      uint32_t whole_p[2][kElems / 2];
-      probabilities<T, kDkv, kCap, kMask>(s_at, side, a.axes, row, e, whole_p);
+      uint32_t rest[2][kElems / 2];
+      probabilities<T, kDkv, kCap, kMask>(s_at, side, a.axes, row, e, rest);
       tc_wait_st();
       tc_before();
       warp_arrive(&sm.p_full);
       if (!(ok = warp_wait(&sm.dp_full, n & 1, given_up))) return;
       tc_after();
-      gradients<T, kDkv, kCap, kMask>(dp_at, side, row, e, whole_p);
+      gradients<T, kDkv, kCap, kMask>(dp_at, side, row, e, rest);
       tc_wait_st();
       tc_before();
       warp_arrive(&sm.ds_full);
