@@ -47,11 +47,22 @@ struct RopeArgs {
   float* dwk;
 };
 
-// A pair weighted and turned.
-__device__ __forceinline__ void turn(float& x0, float& x1, float w0, float w1, float c, float s) {
-  const float n0 = x0 * w0, n1 = x1 * w1;
-  x0 = fmaf(n0, c, -(n1 * s));
-  x1 = fmaf(n1, c, n0 * s);
+// Two pairs turned, two operations an instruction where the signs allow.
+__device__ __forceinline__ void turn(float* x, float* y, float c0, float c1, float s0, float s1) {
+  float a0, a1, b0, b1;
+  mul2(a0, a1, x[0], x[1], s0, s1);
+  mul2(b0, b1, x[0], x[1], c0, c1);
+  x[0] = fmaf(-y[0], s0, b0);
+  x[1] = fmaf(-y[1], s1, b1);
+  fma2(y[0], y[1], y[0], y[1], c0, c1, a0, a1);
+}
+__device__ __forceinline__ void turn_back(float* x, float* y, float c0, float c1, float s0, float s1) {
+  float a0, a1, b0, b1;
+  mul2(a0, a1, y[0], y[1], s0, s1);
+  mul2(b0, b1, y[0], y[1], c0, c1);
+  y[0] = fmaf(-x[0], s0, b0);
+  y[1] = fmaf(-x[1], s1, b1);
+  fma2(x[0], x[1], x[0], x[1], c0, c1, a0, a1);
 }
 
 __device__ __forceinline__ float group_sum(float v, int lanes) {
@@ -72,20 +83,22 @@ __device__ __forceinline__ float2 cos_sin(float angle) {
   return c;
 }
 
-// Cosines and sines of the tile's tokens, [token][pair].
-__device__ __forceinline__ void fill_table(const RopeArgs& a, int t0, int tokens, float2* table) {
+// Cosines and sines of the tile's tokens, [cosine, sine][token][pair].
+__device__ __forceinline__ void fill_table(const RopeArgs& a, int t0, int tokens, float* table) {
   const int half = a.D >> 1;
   for (int i = threadIdx.x; i < tokens * half; i += kThreads) {
     const int t = i / half, p = i - t * half;
     const float at = static_cast<float>(a.pos[static_cast<long long>(t0 + t) * a.pos_stride + p % a.axes]);
-    table[i] = cos_sin(at * a.freq[p]);
+    const float2 c = cos_sin(at * a.freq[p]);
+    table[i] = c.x;
+    table[kTableFloats / 2 + i] = c.y;
   }
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) pv_rope_kernel(const RopeArgs a) {
   constexpr int V = Pack<T>::kN;
-  __shared__ __align__(16) float2 table[kTableFloats / 2];
+  __shared__ __align__(16) float table[kTableFloats];
   const int half = a.D >> 1;
   const int lanes = 1 << a.lanes_log2;
   const int sub = threadIdx.x & (lanes - 1);
@@ -126,23 +139,28 @@ __global__ void __launch_bounds__(kThreads) pv_rope_kernel(const RopeArgs a) {
     float x[2 * V];
     Pack<T>::open(raw0, x);
     Pack<T>::open(raw1, x + V);
-    float ss = 0.0f;
+    float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 2 * V; ++i) ss = fmaf(x[i], x[i], ss);
-    ss = group_sum(on ? ss : 0.0f, lanes);
+    for (int i = 0; i < 2 * V; i += 2) fma2(s0, s1, x[i], x[i + 1], x[i], x[i + 1], s0, s1);
+    const float ss = group_sum(on ? s0 + s1 : 0.0f, lanes);
     if (live) {
       const bool isq = h_now < a.hq;
       const float rs = rsqrtf(fmaf(ss, inv, a.eps));
       const float* w = weight + (isq ? 0 : 256) + sub * V;
-      const float4* cs = reinterpret_cast<const float4*>(table + t_now * half + sub * V);
+      const float* cs = table + t_now * half + sub * V;
+#pragma unroll
+      for (int i = 0; i < 2 * V; i += 2) mul2(x[i], x[i + 1], x[i], x[i + 1], rs, rs);
 #pragma unroll
       for (int i = 0; i < V; i += 4) {
         const float4 w0 = *reinterpret_cast<const float4*>(w + i), w1 = *reinterpret_cast<const float4*>(w + half + i);
-        const float4 c0 = cs[i / 2], c1 = cs[i / 2 + 1];
-        turn(x[i], x[V + i], rs * w0.x, rs * w1.x, c0.x, c0.y);
-        turn(x[i + 1], x[V + i + 1], rs * w0.y, rs * w1.y, c0.z, c0.w);
-        turn(x[i + 2], x[V + i + 2], rs * w0.z, rs * w1.z, c1.x, c1.y);
-        turn(x[i + 3], x[V + i + 3], rs * w0.w, rs * w1.w, c1.z, c1.w);
+        const float4 c = *reinterpret_cast<const float4*>(cs + i);
+        const float4 n = *reinterpret_cast<const float4*>(cs + kTableFloats / 2 + i);
+        mul2(x[i], x[i + 1], x[i], x[i + 1], w0.x, w0.y);
+        mul2(x[i + 2], x[i + 3], x[i + 2], x[i + 3], w0.z, w0.w);
+        mul2(x[V + i], x[V + i + 1], x[V + i], x[V + i + 1], w1.x, w1.y);
+        mul2(x[V + i + 2], x[V + i + 3], x[V + i + 2], x[V + i + 3], w1.z, w1.w);
+        turn(x + i, x + V + i, c.x, c.y, n.x, n.y);
+        turn(x + i + 2, x + V + i + 2, c.z, c.w, n.z, n.w);
       }
       const View& out = isq ? a.oq : a.ok;
       char* p = out.data + (t0 + t_now) * out.row + (isq ? h_now : h_now - a.hq) * out.head + sub * 16;
@@ -161,7 +179,7 @@ __global__ void __launch_bounds__(kThreads) pv_rope_kernel(const RopeArgs a) {
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) pv_rope_backward_kernel(const RopeArgs a) {
   constexpr int V = Pack<T>::kN;
-  __shared__ __align__(16) float2 table[kTableFloats / 2];
+  __shared__ __align__(16) float table[kTableFloats];
   __shared__ bool last;
   const int half = a.D >> 1;
   const int lanes = 1 << a.lanes_log2;
@@ -171,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 2) pv_rope_backward_kernel(const Rop
   const float inv = 1.0f / static_cast<float>(a.D);
   wait_prior_grid();
   const int tiles = (a.rows + a.tile - 1) / a.tile;
-  float* sums = reinterpret_cast<float*>(table);
+  float* sums = table;
   for (int side = 0; side < 2; ++side) {
     const View& in = side ? a.k : a.q;
     const View& gr = side ? a.gk : a.gq;
@@ -218,30 +236,37 @@ __global__ void __launch_bounds__(kThreads, 2) pv_rope_backward_kernel(const Rop
         h += step_h;
         if (h >= heads) h -= heads, ++t;
         fetch(t, h);
-        float ss = 0.0f, dot = 0.0f;
+        float s0 = 0.0f, s1 = 0.0f, d0 = 0.0f, d1 = 0.0f;
         if (live) {
-          const float4* cs = reinterpret_cast<const float4*>(table + t_now * half + sub * V);
+          const float* cs = table + t_now * half + sub * V;
 #pragma unroll
-          for (int i = 0; i < V; i += 2) {
-            const float4 c = cs[i / 2];
-            turn(g[i], g[V + i], 1.0f, 1.0f, c.x, -c.y);
-            turn(g[i + 1], g[V + i + 1], 1.0f, 1.0f, c.z, -c.w);
+          for (int i = 0; i < V; i += 4) {
+            const float4 c = *reinterpret_cast<const float4*>(cs + i);
+            const float4 n = *reinterpret_cast<const float4*>(cs + kTableFloats / 2 + i);
+            turn_back(g + i, g + V + i, c.x, c.y, n.x, n.y);
+            turn_back(g + i + 2, g + V + i + 2, c.z, c.w, n.z, n.w);
           }
 #pragma unroll
-          for (int i = 0; i < 2 * V; ++i) {
-            ss = fmaf(x[i], x[i], ss);
-            dot = fmaf(g[i] * w[i], x[i], dot);
+          for (int i = 0; i < 2 * V; i += 2) {
+            float u0, u1;
+            fma2(s0, s1, x[i], x[i + 1], x[i], x[i + 1], s0, s1);
+            mul2(u0, u1, g[i], g[i + 1], w[i], w[i + 1]);
+            fma2(d0, d1, u0, u1, x[i], x[i + 1], d0, d1);
           }
         }
-        ss = group_sum(ss, lanes);
-        dot = group_sum(dot, lanes);
+        const float ss = group_sum(s0 + s1, lanes);
+        const float dot = group_sum(d0 + d1, lanes);
         if (live) {
           const float rs = rsqrtf(fmaf(ss, inv, a.eps));
-          const float m = dot * inv * rs * rs;  // mean(g w n) over n: n = x rs
+          const float m = -(dot * inv * rs * rs);  // mean(g w n) over n: n = x rs
 #pragma unroll
-          for (int i = 0; i < 2 * V; ++i) {
-            acc[i] = fmaf(g[i], x[i] * rs, acc[i]);
-            x[i] = rs * fmaf(g[i], w[i], -(m * x[i]));
+          for (int i = 0; i < 2 * V; i += 2) {
+            float u0, u1;
+            mul2(u0, u1, x[i], x[i + 1], rs, rs);
+            fma2(acc[i], acc[i + 1], g[i], g[i + 1], u0, u1, acc[i], acc[i + 1]);
+            mul2(u0, u1, x[i], x[i + 1], m, m);
+            fma2(u0, u1, g[i], g[i + 1], w[i], w[i + 1], u0, u1);
+            mul2(x[i], x[i + 1], u0, u1, rs, rs);
           }
           char* p = out.data + (t0 + t_now) * out.row + h_now * out.head + sub * 16;
           Pack<T>::store(p, x);

@@ -107,12 +107,36 @@ __device__ __forceinline__ float sigmoid<float>(float v) {
   return 1.0f / (1.0f + expf(-v));
 }
 
+// r = a b + c, r = a + b and r = a b for a thread's one or two channels.
+template <int V>
+__device__ __forceinline__ void vfma(float* r, const float* a, const float* b, const float* c) {
+  if (V == 2)
+    fma2(r[0], r[V - 1], a[0], a[V - 1], b[0], b[V - 1], c[0], c[V - 1]);
+  else
+    r[0] = fmaf(a[0], b[0], c[0]);
+}
+template <int V>
+__device__ __forceinline__ void vadd(float* r, const float* a, const float* b) {
+  if (V == 2)
+    add2(r[0], r[V - 1], a[0], a[V - 1], b[0], b[V - 1]);
+  else
+    r[0] = a[0] + b[0];
+}
+template <int V>
+__device__ __forceinline__ void vmul(float* r, const float* a, const float* b) {
+  if (V == 2)
+    mul2(r[0], r[V - 1], a[0], a[V - 1], b[0], b[V - 1]);
+  else
+    r[0] = a[0] * b[0];
+}
+
 template <typename T, int V>
 struct Lane;  // V neighbouring channels of one row
 template <>
 struct Lane<float, 1> {
   using Raw = float;
   static __device__ __forceinline__ Raw closed() { return __uint_as_float(0xFF800000u); }  // a gate of -inf
+  static __device__ __forceinline__ Raw minus(Raw r) { return -r; }
   static __device__ __forceinline__ void open(Raw r, float* f) { f[0] = r; }
   static __device__ __forceinline__ Raw close(const float* f) { return f[0]; }
 };
@@ -120,6 +144,7 @@ template <typename T>
 struct Lane<T, 1> {
   using Raw = T;
   static __device__ __forceinline__ Raw closed() { return Pack<T>::one(__uint_as_float(0xFF800000u)); }
+  static __device__ __forceinline__ Raw minus(Raw r) { return -r; }
   static __device__ __forceinline__ void open(Raw r, float* f) { f[0] = Pack<T>::to(r); }
   static __device__ __forceinline__ Raw close(const float* f) { return Pack<T>::one(f[0]); }
 };
@@ -127,6 +152,7 @@ template <>
 struct Lane<__nv_bfloat16, 2> {
   using Raw = uint32_t;
   static __device__ __forceinline__ Raw closed() { return 0xFF80FF80u; }
+  static __device__ __forceinline__ Raw minus(Raw r) { return r ^ 0x80008000u; }
   static __device__ __forceinline__ void open(Raw r, float* f) {
     f[0] = __uint_as_float(r << 16);
     f[1] = __uint_as_float(r & 0xFFFF0000u);
@@ -137,6 +163,7 @@ template <>
 struct Lane<__half, 2> {
   using Raw = uint32_t;
   static __device__ __forceinline__ Raw closed() { return 0xFC00FC00u; }
+  static __device__ __forceinline__ Raw minus(Raw r) { return r ^ 0x80008000u; }
   static __device__ __forceinline__ void open(Raw r, float* f) {
     const float2 d = __half22float2(*reinterpret_cast<const __half2*>(&r));
     f[0] = d.x;
@@ -319,37 +346,35 @@ __global__ void __launch_bounds__(kThreads, 2) pv_scan_kernel(const __grid_const
     stage_wait();
     const Raw* in = words + at * (kIn * kSteps * kThreads);
     auto word = [&](int tensor, int j, float* f) { L::open(in[(tensor * kSteps + j) * kThreads], f); };
-    float z[kSteps][V];
+    auto minus_x = [&](int j, float* f) { L::open(L::minus(in[j * kThreads]), f); };
+    // The gates negated, and the inputs: with a step's state as (-z) s + s, then
+    // (-z) (-x) on top, every operation is a multiply-add of what is at hand (two channels
+    // an instruction), exact at both ends of z.
+    float nz[kSteps][V];
 #pragma unroll
     for (int j = 0; j < kSteps; ++j) {
-      word(1, j, z[j]);
+      word(1, j, nz[j]);
 #pragma unroll
-      for (int v = 0; v < V; ++v) z[j][v] = sigmoid<T>(z[j][v]);
+      for (int v = 0; v < V; ++v) nz[j][v] = -sigmoid<T>(nz[j][v]);
     }
-    // (1 - z) v is v - z v: one multiply-add, exact at both ends of z.
     float A[V], B[V], Cb[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = 0.0f, Cb[v] = 0.0f;
 #pragma unroll
     for (int j = 0; j < kSteps; ++j) {
       float x[V];
-      word(0, j, x);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        A[v] = fmaf(-z[j][v], A[v], A[v]);
-        B[v] = fmaf(z[j][v], x[v], fmaf(-z[j][v], B[v], B[v]));
-      }
+      minus_x(j, x);
+      vfma<V>(A, nz[j], A, A);
+      vfma<V>(B, nz[j], B, B);
+      vfma<V>(B, nz[j], x, B);
     }
     if (kBack) {
 #pragma unroll
       for (int j = kSteps - 1; j >= 0; --j) {
         float d[V];
         word(2, j, d);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const float e = d[v] + Cb[v];
-          Cb[v] = fmaf(-z[j][v], e, e);
-        }
+        vadd<V>(d, d, Cb);
+        vfma<V>(Cb, nz[j], d, d);
       }
     }
     float* const mine = all + seg * kRows * width + cl * V;
@@ -439,9 +464,9 @@ __global__ void __launch_bounds__(kThreads, 2) pv_scan_kernel(const __grid_const
 #pragma unroll
         for (int j = 0; j < kSteps; ++j, po += so) {
           float x[V];
-          word(0, j, x);
-#pragma unroll
-          for (int v = 0; v < V; ++v) s[v] = fmaf(z[j][v], x[v], fmaf(-z[j][v], s[v], s[v]));
+          minus_x(j, x);
+          vfma<V>(s, nz[j], s, s);
+          vfma<V>(s, nz[j], x, s);
           if (decltype(whole)::value || j < now.n) __stcs(po, L::close(s));
         }
       };
@@ -450,18 +475,16 @@ __global__ void __launch_bounds__(kThreads, 2) pv_scan_kernel(const __grid_const
       else
         run(std::false_type{});
     } else {
-      float diff[kSteps][V];  // x[t] - h[t-1]
+      float diff[kSteps][V];  // h[t-1] - x[t]
 #pragma unroll
       for (int v = 0; v < V; ++v) s[v] = mine[width + v];
 #pragma unroll
       for (int j = 0; j < kSteps; ++j) {
         float x[V];
-        word(0, j, x);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          diff[j][v] = x[v] - s[v];
-          s[v] = fmaf(z[j][v], x[v], fmaf(-z[j][v], s[v], s[v]));
-        }
+        minus_x(j, x);
+        vadd<V>(diff[j], s, x);
+        vfma<V>(s, nz[j], s, s);
+        vfma<V>(s, nz[j], x, s);
       }
 #pragma unroll
       for (int v = 0; v < V; ++v) s[v] = fmaf(mine[v], carry[cl * V + v], mine[2 * width + v]);
@@ -473,15 +496,13 @@ __global__ void __launch_bounds__(kThreads, 2) pv_scan_kernel(const __grid_const
         for (int j = kSteps - 1; j >= 0; --j, po -= so, pq -= sq) {
           float d[V], gx[V], gg[V];
           word(2, j, d);
-#pragma unroll
-          for (int v = 0; v < V; ++v) {
-            const float e = d[v] + s[v];
-            gx[v] = e * z[j][v];
-            s[v] = fmaf(-z[j][v], e, e);
-            gg[v] = s[v] * z[j][v] * diff[j][v];  // e z (1 - z) (x - h)
-          }
+          vadd<V>(d, d, s);
+          vmul<V>(gx, d, nz[j]);  // -e z
+          vfma<V>(s, nz[j], d, d);
+          vmul<V>(gg, nz[j], diff[j]);
+          vmul<V>(gg, gg, s);  // e z (1 - z) (x - h)
           if (decltype(whole)::value || j < now.n) {
-            __stcs(po, L::close(gx));
+            __stcs(po, L::minus(L::close(gx)));
             __stcs(pq, L::close(gg));
           }
         }
