@@ -258,11 +258,18 @@ extern "C" int pv_attention_backward(const pv_attention_params* params, const pv
   a.head_parts = 1;
   while (a.G % (2 * a.head_parts) == 0 && key_tiles * a.Hk * a.head_parts < 4 * sms) a.head_parts *= 2;
   Scratch scratch;
-  const size_t rows = round_up(static_cast<size_t>(nq) * a.H, 4);
+  // (One tile more than the rows: the last copy of a row of sides is a whole one too.)
+  int64_t side_rows = 0;
+  for (int f = 0; f < a.frames; ++f) {
+    a.side0[f] = static_cast<int>(side_rows);
+    side_rows += (a.q0[f + 1] - a.q0[f] + 3) / 4 * 4;
+  }
+  a.sides_row = side_rows + 128;
+  const size_t sides = static_cast<size_t>(a.sides_row) * (2 * a.H + 3);
   const size_t parts = a.head_parts > 1 ? static_cast<size_t>(2) * a.head_parts * nk * a.Hk * a.D : 0;
-  if ((st = scratch.open(dev, stream, kPlain, sizeof(float) * (rows + parts))) != PV_OK) return st;
-  a.delta = static_cast<float*>(scratch.body());
-  a.part_o = a.delta + rows;
+  if ((st = scratch.open(dev, stream, kPlain, sizeof(float) * (sides + parts))) != PV_OK) return st;
+  a.sides = static_cast<float*>(scratch.body());
+  a.part_o = a.sides + sides;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   AttnMaps m{};
   if (nq && ((st = make_map(&m.q, a.q, params->dtype, a.D, a.H, 1, nq, 128)) != PV_OK ||

@@ -16,7 +16,11 @@ struct View {
 struct AttnArgs {
   View q, k, v, o, dout, dq, dk, dv;
   float* lse;            // [H, queries]
-  float* delta;          // [H, queries]: sum of P dP (backward)
+  // Backward, what dq leaves of the queries for dk and dv, rows of `sides_row` floats in
+  // which each frame begins on 16 bytes (side0): [H] the exponent's offset from lse, [H]
+  // delta (negated), [3] positions.
+  float* sides;
+  long long sides_row;
   const float* slopes;
   const int32_t* qpos;
   const int32_t* kpos;
@@ -33,6 +37,7 @@ struct AttnArgs {
   int q0[PV_MAX_FRAMES + 1];    // row offsets of the frames
   int k0[PV_MAX_FRAMES + 1];
   int prefix[PV_MAX_FRAMES];
+  int side0[PV_MAX_FRAMES];
   // The blocks' list: frames by their work, most first, and the first tile of each in
   // that order.  Block b takes tile b / heads of it for head b % heads.
   unsigned char order[PV_MAX_FRAMES];

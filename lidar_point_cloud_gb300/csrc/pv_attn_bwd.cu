@@ -31,7 +31,8 @@
 // keys share is larger than all other roundings.  The dq kernel therefore takes
 // that delta as a first guess, sums P dP in 32 bits on the way (which is delta as
 // the products have it), and mends dq by the difference times acc2 = P k; it
-// leaves the summed delta for the dk, dv kernel.  That is one product more than
+// leaves the summed delta (with the queries' lse and positions, laid out for bulk
+// copies) for the dk, dv kernel.  That is one product more than
 // the four that dq needs least, and no more exponentials.
 //
 // P and dS are held 16 times their values in the storage type: float16 runs out
@@ -66,7 +67,7 @@ struct Smem {
   static constexpr int kSlots = kBlocks == 1 ? 4 : 2;
   alignas(1024) unsigned char own[2][kTile];
   alignas(1024) unsigned char other[2][kSlots][kTile];
-  float side[kSides][5][kOther];  // lse (as an offset of the exponent), delta (negated), positions
+  alignas(16) float side[kSides][5][kOther];  // lse (as an offset of the exponent), delta (negated), positions
   float rest[kGroups][kOwn];      // dq: each warpgroup's sum of P (dP - delta)
   float guess[kOwn];              // dq: do.o of the rounded o
   uint64_t own_full, dirty[2], clean[2], full[2][kSlots], empty[2][kSlots], s_full, dp_full, p_full, ds_full, acc_full, side_full[kSides],
@@ -232,9 +233,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const int steps = per_head * heads;
   const int own_rows = kDkv ? nk : nq, other_rows = kDkv ? nq : nk;
-  // Head of the other side at step n, and its first row.
-  auto other_head = [&](int n) { return kDkv ? head0 + n / per_head : head0; };
-  auto other_row = [&](int n) { return (other_tile0 + (kDkv ? n % per_head : n)) * kOther; };
 
   // ---- set up
   if (threadIdx.x == 0) {
@@ -278,18 +276,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int s = 0; s < 2; ++s)
         for (int b = 0; b < kBlocks; ++b)
           tma_load4(sm.own[s] + b * kOwn * 128, own_map[s], b * 64, 0, own_heads[s] ? own_head : 0, own_base, &sm.own_full);
-      for (int n = 0; n < steps; ++n) {
-        const int slot = n % S::kSlots, h = other_head(n), row = other_base + other_row(n);
-        bool ok = true;
+      int slot = 0, phase = 1, h = head0, left = per_head;
+      const int first_row = other_base + other_tile0 * kOther;
+      int row = first_row;
+      bool ok = true;
+      for (int n = 0; ok && n < steps; ++n) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          if (!ok || !(ok = bar_wait(&sm.empty[s][slot], ((n / S::kSlots) & 1) ^ 1, given_up))) continue;
+          if (!ok || !(ok = bar_wait(&sm.empty[s][slot], phase, given_up))) continue;
           bar_expect(&sm.full[s][slot], S::kTile);
+#pragma unroll
           for (int b = 0; b < kBlocks; ++b)
             tma_load4(sm.other[s][slot] + b * kOther * 128, other_map[s], b * 64, 0, other_heads[s] ? h : 0, row,
                       &sm.full[s][slot]);
         }
-        if (!ok) break;
+        row += kOther;
+        if (--left == 0) left = per_head, row = first_row, ++h;
+        if (++slot == S::kSlots) slot = 0, phase ^= 1;
       }
     }
   } else if (warp == kIssue) {
@@ -383,54 +386,56 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == kIssue + 2) {
-    // ---- what belongs to the other side's rows, each tile's loaded while the last
-    // one's are handed over
-    if (sides && steps > 0) {
+    // ---- what belongs to the other side's rows
+    if (kDkv) {
+      // The dq kernel left it as it is needed: whole pieces, past a frame's end too (what
+      // is there is hidden).
+      if (lane == 0 && steps > 0) {
+        int slot = 0, phase = 1, h = head0, left = per_head;
+        const int first_row = a.side0[f] + other_tile0 * kOther;
+        const float* const pos = a.sides + 2 * a.H * a.sides_row;
+        int row = first_row;
+        for (int n = 0; n < steps; ++n) {
+          if (!bar_wait(&sm.side_empty[slot], phase, given_up)) break;
+          bar_expect(&sm.side_full[slot], (2 + a.axes) * kOther * 4);
+          const float* const off = a.sides + h * a.sides_row + row;
+          tma_copy(sm.side[slot][0], off, kOther * 4, &sm.side_full[slot]);
+          tma_copy(sm.side[slot][1], off + a.H * a.sides_row, kOther * 4, &sm.side_full[slot]);
+          for (int c = 0; c < a.axes; ++c)
+            tma_copy(sm.side[slot][2 + c], pos + c * a.sides_row + row, kOther * 4, &sm.side_full[slot]);
+          row += kOther;
+          if (--left == 0) left = per_head, row = first_row, ++h;
+          if (++slot == kSides) slot = 0, phase ^= 1;
+        }
+      }
+    } else if (a.slopes && steps > 0) {
+      // Positions, each tile's loaded while the last one's are handed over.
       int pos[3][4];
-      float lse[4], delta[4];
-      int h = head0, t = 0;  // head and tile to load
-      auto load = [&]() {
-        const int row0 = (other_tile0 + t) * kOther;
+      auto load = [&](int tile) {
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          const long long row = (kDkv ? a.q0[f] : a.k0[f]) + min(row0 + x * 32 + lane, other_rows - 1);
-          if (kDkv) {
-            lse[x] = a.lse[static_cast<long long>(h) * a.queries + row];
-            delta[x] = a.delta[static_cast<long long>(h) * a.queries + row];
-          }
-          const int32_t* p = kDkv ? a.qpos + row * a.qpos_stride : a.kpos + row * a.kpos_stride;
+          const long long row = a.k0[f] + min(tile * kOther + x * 32 + lane, nk - 1);
 #pragma unroll
           for (int c = 0; c < 3; ++c)
-            if (c < a.axes) pos[c][x] = p[c];
+            if (c < a.axes) pos[c][x] = a.kpos[row * a.kpos_stride + c];
         }
-        if (++t == per_head) t = 0, ++h;
       };
-      load();
+      load(0);
       for (int n = 0; n < steps; ++n) {
         const int slot = n % kSides;
-        float now[5][4];
+        float now[3][4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          if (kDkv) {
-            now[0][x] = fmaf(-kLog2e, lse[x], kUp);
-            now[1][x] = -delta[x];
-          }
+        for (int x = 0; x < 4; ++x)
 #pragma unroll
           for (int c = 0; c < 3; ++c)
-            if (c < a.axes) now[2 + c][x] = static_cast<float>(pos[c][x]);
-        }
-        if (n + 1 < steps) load();
+            if (c < a.axes) now[c][x] = static_cast<float>(pos[c][x]);
+        if (n + 1 < steps) load(n + 1);
         if (!warp_wait(&sm.side_empty[slot], ((n / kSides) & 1) ^ 1, given_up)) break;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          if (kDkv) {
-            sm.side[slot][0][x * 32 + lane] = now[0][x];
-            sm.side[slot][1][x * 32 + lane] = now[1][x];
-          }
+        for (int x = 0; x < 4; ++x)
 #pragma unroll
           for (int c = 0; c < 3; ++c)
-            if (c < a.axes) sm.side[slot][2 + c][x * 32 + lane] = now[2 + c][x];
-        }
+            if (c < a.axes) sm.side[slot][2 + c][x * 32 + lane] = now[c][x];
         warp_arrive(&sm.side_full[slot]);
       }
     }
@@ -569,7 +574,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       math_sync();
       total = ((sm.rest[0][r] + sm.rest[1][r]) + (sm.rest[2][r] + sm.rest[3][r])) * kDown;
-      if (live && wg == 0) a.delta[static_cast<long long>(own_head) * a.queries + own_row] = sm.guess[r] + total;
+      if (live && wg == 0) {
+        float* const side = a.sides + own_head * a.sides_row + a.side0[f] + own;
+        side[0] = fmaf(-kLog2e, a.lse[static_cast<long long>(own_head) * a.queries + own_row], kUp);
+        side[a.H * a.sides_row] = -(sm.guess[r] + total);
+        if (own_head == 0)
+          for (int c = 0; c < a.axes; ++c)
+            side[(2 * a.H + c) * a.sides_row] = static_cast<float>(a.qpos[own_row * a.qpos_stride + c]);
+      }
     }
     const float bad = !ok || *given_up ? __int_as_float(0x7FFFFFFF) : 1.0f;  // a wait ran out: nothing here is an answer
     const int which = wg & 1;  // dk, dv: 0 and 1
