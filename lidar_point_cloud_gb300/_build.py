@@ -16,7 +16,8 @@ CSRC = os.path.join(PKG, "csrc")
 # attention), with pv_seq.cuh, pv_seq.cu and pv_attn.cuh shared.
 SRCS = [os.path.join(CSRC, f) for f in ("pv_ordered.cu", "pv_ordered_half.cu", "pv_unordered.cu", "pv_downsample.cu",
                                          "pv_downsample_half.cu", "pv_host.cu", "pv_fps.cu", "pv_seq.cu", "pv_rope.cu",
-                                         "pv_scan.cu", "pv_attn.cu", "pv_attn_fwd.cu", "pv_attn_bwd.cu")]
+                                         "pv_scan.cu", "pv_attn.cu", "pv_attn_fwd.cu", "pv_attn_fwd_half.cu",
+                                         "pv_attn_bwd.cu", "pv_attn_bwd_half.cu")]
 HEADERS = [os.path.join(CSRC, f) for f in ("pv_device.cuh", "pv_seq.cuh", "pv_attn.cuh", "pv_tc.cuh")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libpv.so")

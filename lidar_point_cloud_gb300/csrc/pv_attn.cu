@@ -217,7 +217,8 @@ extern "C" int pv_attention(const pv_attention_params* params, const pv_heads* q
              (st = make_map(&m.v, a.v, params->dtype, a.D, a.Hk, 1, nk, 128)) != PV_OK) {
     return st;
   }
-  return attn_forward(a, params->dtype, m, dim3(tiles * heads), reinterpret_cast<cudaStream_t>(stream));
+  const bool bf16 = params->dtype == PV_BF16;
+  return (bf16 ? attn_forward_bf16 : attn_forward_half)(a, m, dim3(tiles * heads), reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" int pv_attention_backward(const pv_attention_params* params, const pv_heads* dout, const pv_heads* q,
@@ -286,6 +287,7 @@ extern "C" int pv_attention_backward(const pv_attention_params* params, const pv
   const int q_tiles = list_tiles(a, a.k0, [&](int f) { return (a.q0[f + 1] - a.q0[f] + 127) / 128; });
   const int k_tiles = list_tiles(b, a.q0, [&](int f) { return (a.k0[f + 1] - a.k0[f] + 127) / 128; });
   if (q_tiles < 0 || k_tiles < 0) return PV_ERR_TOO_LARGE;
-  if ((st = attn_backward_dq(a, params->dtype, m, dim3(q_tiles * a.heads), cs)) != PV_OK) return st;
-  return attn_backward_dkv(b, params->dtype, m, dim3(k_tiles * b.heads), cs);
+  const bool bf16 = params->dtype == PV_BF16;
+  if ((st = (bf16 ? attn_backward_dq_bf16 : attn_backward_dq_half)(a, m, dim3(q_tiles * a.heads), cs)) != PV_OK) return st;
+  return (bf16 ? attn_backward_dkv_bf16 : attn_backward_dkv_half)(b, m, dim3(k_tiles * b.heads), cs);
 }

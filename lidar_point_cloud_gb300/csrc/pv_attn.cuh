@@ -6,6 +6,9 @@
 
 #include <cuda.h>
 
+#include <map>
+#include <utility>
+
 namespace pvs {
 
 struct View {
@@ -53,10 +56,40 @@ struct AttnMaps {
 // elements: dimensions (D, pack, heads / pack, rows), elements past D read as 0.
 int make_map(CUtensorMap* map, const View& v, int dtype, int D, int heads, int pack, int64_t total, int rows);
 
-// Kernel launches of pv_attn_fwd.cu and pv_attn_bwd.cu.
-int attn_forward(AttnArgs& a, int dtype, const AttnMaps& m, dim3 grid, cudaStream_t s);
-int attn_backward_dq(const AttnArgs& a, int dtype, const AttnMaps& m, dim3 grid, cudaStream_t s);   // and delta
-int attn_backward_dkv(const AttnArgs& a, int dtype, const AttnMaps& m, dim3 grid, cudaStream_t s);  // after it
+// Kernel launches of pv_attn_fwd.cu and pv_attn_bwd.cu, each compiled once for
+// bfloat16 and once, through its _half.cu, for float16.
+#ifdef PV_ATTN_HALF
+using Storage = __half;
+#define PV_ATTN_NAME(name) name##_half
+#else
+using Storage = __nv_bfloat16;
+#define PV_ATTN_NAME(name) name##_bf16
+#endif
+int attn_forward_bf16(const AttnArgs& a, const AttnMaps& m, dim3 grid, cudaStream_t s);
+int attn_forward_half(const AttnArgs& a, const AttnMaps& m, dim3 grid, cudaStream_t s);
+int attn_backward_dq_bf16(const AttnArgs& a, const AttnMaps& m, dim3 grid, cudaStream_t s);   // and the sides
+int attn_backward_dq_half(const AttnArgs& a, const AttnMaps& m, dim3 grid, cudaStream_t s);
+int attn_backward_dkv_bf16(const AttnArgs& a, const AttnMaps& m, dim3 grid, cudaStream_t s);  // after it
+int attn_backward_dkv_half(const AttnArgs& a, const AttnMaps& m, dim3 grid, cudaStream_t s);
+
+// Lets a kernel take `bytes` of dynamic shared memory on the current device.  Asked once
+// per kernel and device; a second time does no harm.
+template <typename K>
+int allow_smem(K kernel, int bytes) {
+  static std::map<std::pair<const void*, int>, bool> done;
+  static std::mutex mu;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return PV_ERR_CUDA;
+  std::lock_guard<std::mutex> lk(mu);
+  bool& ready = done[std::make_pair(reinterpret_cast<const void*>(kernel), dev)];
+  if (ready) return PV_OK;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+    cudaGetLastError();
+    return PV_ERR_CUDA;
+  }
+  ready = true;
+  return PV_OK;
+}
 
 template <typename K, typename... A>
 int launch_pdl(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t s, const A&... args) {

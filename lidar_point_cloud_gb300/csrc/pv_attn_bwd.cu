@@ -99,7 +99,7 @@ __device__ __forceinline__ constexpr int col_of(int x) { return (x >> 2) * 8 + (
 // for acc2 too, and what the slope took from 16 P, for the sum of P dP, goes to `rest`
 // as half pairs (a small share, of which the rounding does not show).  One operation
 // after the other over all elements: an element's chain is long, 32 of them hide it.
-template <typename T, bool kDkv, bool kCap, bool kMask>
+template <typename T, bool kDkv, bool kCap, bool kSlopes, bool kMask>
 __device__ __forceinline__ void probabilities(uint32_t at, const float* side, int axes, const Rows& row, float (*u)[kElems],
                                               uint32_t (*rest)[kElems / 2]) {
   tmem_ld_16x256b_x4(at, reinterpret_cast<uint32_t*>(u[0]));
@@ -116,9 +116,11 @@ __device__ __forceinline__ void probabilities(uint32_t at, const float* side, in
         steep[h][x] = fmaf(-u[h][x], u[h][x], 1.0f);
       }
   }
-  if (axes == 1) lower<1, kCols / 8>(u, side + 2 * kOther, kOther, row.pos, row.slope);
-  if (axes == 2) lower<2, kCols / 8>(u, side + 2 * kOther, kOther, row.pos, row.slope);
-  if (axes == 3) lower<3, kCols / 8>(u, side + 2 * kOther, kOther, row.pos, row.slope);
+  if (kSlopes) {
+    if (axes == 1) lower<1, kCols / 8>(u, side + 2 * kOther, kOther, row.pos, row.slope);
+    if (axes == 2) lower<2, kCols / 8>(u, side + 2 * kOther, kOther, row.pos, row.slope);
+    if (axes == 3) lower<3, kCols / 8>(u, side + 2 * kOther, kOther, row.pos, row.slope);
+  }
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -199,7 +201,10 @@ __device__ __forceinline__ void gradients(uint32_t at, const float* side, Rows& 
   }
 }
 
-template <typename T, int kBlocks, bool kDkv>
+// The cap and the slopes are compile-time choices: code that a launch does not run
+// still costs it instruction fetches (2 x 4096 tokens, 64-element heads, forward and
+// backward: 411 us with both as branches, 3XX us so).
+template <typename T, int kBlocks, bool kDkv, bool kCap, bool kSlopes>
 __global__ void __launch_bounds__(kThreads, 1)
     pv_attn_bwd_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap mq,
                        const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
@@ -259,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_after();
   const uint32_t tm = sm.tmem;  // columns: S 0, dP 128, acc1 256, acc2 256 + 64 kBlocks
   volatile int* given_up = &sm.given_up;
-  const bool sides = kDkv || a.slopes != nullptr;
+  constexpr bool sides = kDkv || kSlopes;
   wait_prior_grid();
 
   if (warp >= kIssue) regs_down<kRegsOther>();
@@ -397,18 +402,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         int row = first_row;
         for (int n = 0; n < steps; ++n) {
           if (!bar_wait(&sm.side_empty[slot], phase, given_up)) break;
-          bar_expect(&sm.side_full[slot], (2 + a.axes) * kOther * 4);
+          bar_expect(&sm.side_full[slot], (2 + (kSlopes ? a.axes : 0)) * kOther * 4);
           const float* const off = a.sides + h * a.sides_row + row;
           tma_copy(sm.side[slot][0], off, kOther * 4, &sm.side_full[slot]);
           tma_copy(sm.side[slot][1], off + a.H * a.sides_row, kOther * 4, &sm.side_full[slot]);
-          for (int c = 0; c < a.axes; ++c)
+          for (int c = 0; kSlopes && c < a.axes; ++c)
             tma_copy(sm.side[slot][2 + c], pos + c * a.sides_row + row, kOther * 4, &sm.side_full[slot]);
           row += kOther;
           if (--left == 0) left = per_head, row = first_row, ++h;
           if (++slot == kSides) slot = 0, phase ^= 1;
         }
       }
-    } else if (a.slopes && steps > 0) {
+    } else if (kSlopes && steps > 0) {
       // Positions, each tile's loaded while the last one's are handed over.
       int pos[3][4];
       auto load = [&](int tile) {
@@ -468,8 +473,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       math_sync();
     }
     Rows row{};
-    row.mul = (a.cap > 0.0f ? a.cap : a.scale) * kLog2e;
-    row.cap_in = a.cap > 0.0f ? 2.0f * a.scale * kLog2e / a.cap : 0.0f;
+    row.mul = (kCap ? a.cap : a.scale) * kLog2e;
+    row.cap_in = kCap ? 2.0f * a.scale * kLog2e / a.cap : 0.0f;
     // A place is seen if its column is at least `from` and below `to`.
     int from[4], to[4];
 #pragma unroll
@@ -489,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (in) row.off[x] = fmaf(-kLog2e, a.lse[static_cast<long long>(own_head) * a.queries + at], kUp);
         row.delta[x] = -sm.guess[rx];
       }
-      if (a.slopes && in) {
+      if (kSlopes && in) {
         if (!kDkv) row.slope[x] = -a.slopes[own_head] * kLog2e / row.mul;
 #pragma unroll
         for (int c = 0; c < 3; ++c)
@@ -500,12 +505,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int c0 = wg * kCols;
     const uint32_t s_at = mine + c0, dp_at = mine + 128 + c0;
     bool ok = true;
-    // One step with the cap and the mask as compile-time choices.
-    auto step = [&](auto cap, auto mask, int n, const float* side) {
-      constexpr bool kCap = decltype(cap)::value, kMask = decltype(mask)::value;
+    // One step, with the mask a compile-time choice.
+    auto step = [&](auto mask, int n, const float* side) {
+      constexpr bool kMask = decltype(mask)::value;
       float e[2][kElems];
       uint32_t rest[2][kElems / 2];
-      probabilities<T, kDkv, kCap, kMask>(s_at, side, a.axes, row, e, rest);
+      probabilities<T, kDkv, kCap, kSlopes, kMask>(s_at, side, a.axes, row, e, rest);
       tc_wait_st();
       tc_before();
       warp_arrive(&sm.p_full);
@@ -522,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (left-- == 0) {
         left = per_head - 1;
         row0 = other_tile0 * kOther;
-        if (kDkv && a.slopes) {
+        if (kDkv && kSlopes) {
           const float slope = -a.slopes[next_head] * kLog2e / row.mul;
 #pragma unroll
           for (int x = 0; x < 4; ++x) row.slope[x] = slope;
@@ -542,20 +547,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!(ok = warp_wait(&sm.s_full, n & 1, given_up))) break;
       tc_after();
-      using Yes = std::true_type;
-      using No = std::false_type;
       const float* side = &sm.side[slot][0][c0 + 2 * quad];
-      if (a.cap > 0.0f) {
-        if (whole)
-          step(Yes{}, No{}, n, side);
-        else
-          step(Yes{}, Yes{}, n, side);
-      } else {
-        if (whole)
-          step(No{}, No{}, n, side);
-        else
-          step(No{}, Yes{}, n, side);
-      }
+      if (whole)
+        step(std::false_type{}, n, side);
+      else
+        step(std::true_type{}, n, side);
       if (!ok) break;
       if (sides) warp_arrive(&sm.side_empty[slot]);
     }
@@ -661,42 +657,34 @@ __global__ void __launch_bounds__(256) pv_attn_bwd_join_kernel(const __grid_cons
   allow_next_grid();
 }
 
-template <typename T, int kBlocks, bool kDkv>
+template <int kBlocks, bool kDkv, bool kCap, bool kSlopes>
 int launch_bwd(const AttnArgs& a, const AttnMaps& m, dim3 grid, cudaStream_t s) {
   if (grid.x == 0) return PV_OK;
-  auto kernel = pv_attn_bwd_kernel<T, kBlocks, kDkv>;
+  auto kernel = pv_attn_bwd_kernel<Storage, kBlocks, kDkv, kCap, kSlopes>;
   const int smem = static_cast<int>(sizeof(Smem<kBlocks>)) + 1024;
-  static bool ready[64];  // set once per device; a second set does no harm
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (!ready[dev & 63]) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
-      cudaGetLastError();
-      return PV_ERR_CUDA;
-    }
-    ready[dev & 63] = true;
-  }
-  return launch_pdl(kernel, grid, kThreads, smem, s, a, m.q, m.k, m.v, m.dout);
+  const int st = allow_smem(kernel, smem);
+  return st == PV_OK ? launch_pdl(kernel, grid, kThreads, smem, s, a, m.q, m.k, m.v, m.dout) : st;
 }
 
-template <typename T, bool kDkv>
-int side(const AttnArgs& a, const AttnMaps& m, dim3 grid, cudaStream_t s) {
-  return a.D > 64 ? launch_bwd<T, 2, kDkv>(a, m, grid, s) : launch_bwd<T, 1, kDkv>(a, m, grid, s);
+template <int kBlocks, bool kDkv>
+int with_scores(const AttnArgs& a, const AttnMaps& m, dim3 grid, cudaStream_t s) {
+  if (a.cap > 0.0f)
+    return a.slopes ? launch_bwd<kBlocks, kDkv, true, true>(a, m, grid, s) : launch_bwd<kBlocks, kDkv, true, false>(a, m, grid, s);
+  return a.slopes ? launch_bwd<kBlocks, kDkv, false, true>(a, m, grid, s) : launch_bwd<kBlocks, kDkv, false, false>(a, m, grid, s);
 }
 
 }  // namespace
 
-int attn_backward_dq(const AttnArgs& a, int dtype, const AttnMaps& m, dim3 grid, cudaStream_t s) {
-  return dtype == PV_BF16 ? side<__nv_bfloat16, false>(a, m, grid, s) : side<__half, false>(a, m, grid, s);
+int PV_ATTN_NAME(attn_backward_dq)(const AttnArgs& a, const AttnMaps& m, dim3 grid, cudaStream_t s) {
+  return a.D > 64 ? with_scores<2, false>(a, m, grid, s) : with_scores<1, false>(a, m, grid, s);
 }
 
-int attn_backward_dkv(const AttnArgs& a, int dtype, const AttnMaps& m, dim3 grid, cudaStream_t s) {
-  const int st = dtype == PV_BF16 ? side<__nv_bfloat16, true>(a, m, grid, s) : side<__half, true>(a, m, grid, s);
+int PV_ATTN_NAME(attn_backward_dkv)(const AttnArgs& a, const AttnMaps& m, dim3 grid, cudaStream_t s) {
+  const int st = a.D > 64 ? with_scores<2, true>(a, m, grid, s) : with_scores<1, true>(a, m, grid, s);
   if (st != PV_OK || a.head_parts < 2 || grid.x == 0) return st;
   const long long words = static_cast<long long>(a.keys) * a.Hk * a.D / 4;
   const dim3 g(static_cast<unsigned int>(std::min<long long>((words + 255) / 256, 4096)));
-  return dtype == PV_BF16 ? launch_pdl(pv_attn_bwd_join_kernel<__nv_bfloat16>, g, 256, 0, s, a)
-                          : launch_pdl(pv_attn_bwd_join_kernel<__half>, g, 256, 0, s, a);
+  return launch_pdl(pv_attn_bwd_join_kernel<Storage>, g, 256, 0, s, a);
 }
 
 }  // namespace pvs

@@ -1,0 +1,3 @@
+// The backward attention kernels for float16 (pv_attn_bwd.cu is for bfloat16).
+#define PV_ATTN_HALF
+#include "pv_attn_bwd.cu"

@@ -68,7 +68,7 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return Pack<T>::two(a, b);
 }
 
-template <typename T, int kBlocks, bool kSlopes>
+template <typename T, int kBlocks, bool kCap, bool kSlopes>
 __global__ void __launch_bounds__(kThreads, 1)
     pv_attn_fwd_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap mq,
                        const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
@@ -335,8 +335,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int clear = first[t] < nq ? limit(first[t]) : nk;  // tiles that end at or below this are seen whole
     // What a score (the raw product, or tanh of it if capped) is multiplied by to
     // be in units of log2.
-    const float mul = (a.cap > 0.0f ? a.cap : a.scale) * kLog2e;
-    const float cap_in = a.cap > 0.0f ? 2.0f * a.scale * kLog2e / a.cap : 0.0f;
+    const float mul = (kCap ? a.cap : a.scale) * kLog2e;
+    const float cap_in = kCap ? 2.0f * a.scale * kLog2e / a.cap : 0.0f;
     bool ok = true;
     // The score buffer of step n, and the phase of its barriers: with a ring, steps of
     // both tiles before this one count.
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         slope[x] = 0.0f;
 #pragma unroll
         for (int c = 0; c < 3; ++c) qp[c][x] = 0.0f;
-        if (a.slopes && i < nq) {
+        if (i < nq) {
           slope[x] = -a.slopes[(hb << a.pack_log2) + (r & (pack - 1))] * kLog2e / mul;
 #pragma unroll
           for (int c = 0; c < 3; ++c)
@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld_16x256b_x16(high + sc, reinterpret_cast<uint32_t*>(u[1]));
         tc_wait_ld<64>(reinterpret_cast<uint32_t*>(u[0]));
         tc_wait_ld<64>(reinterpret_cast<uint32_t*>(u[1]));
-        if (a.cap > 0.0f) {
+        if (kCap) {
 #pragma unroll
           for (int x = 0; x < 128; ++x) u[x >> 6][x & 63] = tanh_half(u[x >> 6][x & 63] * cap_in);
         }
@@ -506,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int x = 0; x < kRows; x += 32) tmem_ld32(sc + x, ur + x);
         tc_wait_ld<kRows>(ur);
-        if (a.cap > 0.0f) {
+        if (kCap) {
 #pragma unroll
           for (int x = 0; x < kRows; ++x) u[x] = tanh_half(u[x] * cap_in);
         }
@@ -654,39 +654,27 @@ __global__ void __launch_bounds__(128) pv_attn_join_kernel(const __grid_constant
   allow_next_grid();
 }
 
-template <typename T, int kBlocks, bool kSlopes>
-int launch_fwd(const AttnArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, dim3 grid, cudaStream_t s) {
-  auto kernel = pv_attn_fwd_kernel<T, kBlocks, kSlopes>;
+template <int kBlocks, bool kCap, bool kSlopes>
+int launch_fwd(const AttnArgs& a, const AttnMaps& m, dim3 grid, cudaStream_t s) {
+  auto kernel = pv_attn_fwd_kernel<Storage, kBlocks, kCap, kSlopes>;
   const int smem = static_cast<int>(sizeof(Smem<kBlocks>)) + 1024;
-  static bool ready[64];  // set once per device; a second set does no harm
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (!ready[dev & 63]) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
-      cudaGetLastError();
-      return PV_ERR_CUDA;
-    }
-    ready[dev & 63] = true;
-  }
-  return launch_pdl(kernel, grid, kThreads, smem, s, a, q, k, v);
+  const int st = allow_smem(kernel, smem);
+  return st == PV_OK ? launch_pdl(kernel, grid, kThreads, smem, s, a, m.q, m.k, m.v) : st;
+}
+
+template <int kBlocks>
+int with_scores(const AttnArgs& a, const AttnMaps& m, dim3 grid, cudaStream_t s) {
+  if (a.cap > 0.0f) return a.slopes ? launch_fwd<kBlocks, true, true>(a, m, grid, s) : launch_fwd<kBlocks, true, false>(a, m, grid, s);
+  return a.slopes ? launch_fwd<kBlocks, false, true>(a, m, grid, s) : launch_fwd<kBlocks, false, false>(a, m, grid, s);
 }
 
 }  // namespace
 
-template <typename T>
-int forward(const AttnArgs& a, const AttnMaps& m, dim3 grid, cudaStream_t s) {
-  if (a.slopes)
-    return a.D > 64 ? launch_fwd<T, 2, true>(a, m.q, m.k, m.v, grid, s) : launch_fwd<T, 1, true>(a, m.q, m.k, m.v, grid, s);
-  return a.D > 64 ? launch_fwd<T, 2, false>(a, m.q, m.k, m.v, grid, s) : launch_fwd<T, 1, false>(a, m.q, m.k, m.v, grid, s);
-}
-
-int attn_forward(AttnArgs& a, int dtype, const AttnMaps& m, dim3 grid, cudaStream_t s) {
-  const int st = dtype == PV_BF16 ? forward<__nv_bfloat16>(a, m, grid, s) : forward<__half>(a, m, grid, s);
+int PV_ATTN_NAME(attn_forward)(const AttnArgs& a, const AttnMaps& m, dim3 grid, cudaStream_t s) {
+  const int st = a.D > 64 ? with_scores<2>(a, m, grid, s) : with_scores<1>(a, m, grid, s);
   if (st != PV_OK || !a.part_o) return st;
   const long long warps = static_cast<long long>(a.queries) * a.H;
-  const dim3 g(static_cast<unsigned int>((warps + 3) / 4));
-  return dtype == PV_BF16 ? launch_pdl(pv_attn_join_kernel<__nv_bfloat16>, g, 128, 0, s, a)
-                          : launch_pdl(pv_attn_join_kernel<__half>, g, 128, 0, s, a);
+  return launch_pdl(pv_attn_join_kernel<Storage>, dim3(static_cast<unsigned int>((warps + 3) / 4)), 128, 0, s, a);
 }
 
 }  // namespace pvs
