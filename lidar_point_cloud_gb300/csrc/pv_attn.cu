@@ -17,6 +17,8 @@
 #include <atomic>
 #include <cmath>
 #include <initializer_list>
+#include <utility>
+#include <vector>
 
 namespace {
 
@@ -83,32 +85,82 @@ int pack_of(int G) {
   return p;
 }
 
-// How many key tiles a block takes, by an estimate in units of a key tile's time (some
-// 1.5 us).  The blocks run in rounds of one a multiprocessor, a block's time being
-// its key tiles and some kBlock more to begin and end; with many blocks, longest first,
-// the rounds blur.  Keys cut into parts cost the parts' outputs (32-bit, written and
-// read again at some 5 TB/s) and kJoin for one more launch.
-int chunk_of(const AttnArgs& a, int heads, int sms) {
-  constexpr double kBlock = 2.0, kJoin = 2.0, kBytes = 7.5e6;
-  int most = 1;
-  for (int f = 0; f < a.frames; ++f) most = std::max(most, (a.k0[f + 1] - a.k0[f] + 127) / 128);
-  auto cost = [&](int chunk) {
-    int64_t blocks = 0, work = 0;
-    for (int f = 0; f < a.frames; ++f) {
-      const int64_t rows = ((static_cast<int64_t>(a.q0[f + 1] - a.q0[f]) << a.pack_log2) + 255) / 256;
-      const int tiles = (a.k0[f + 1] - a.k0[f] + 127) / 128;
-      blocks += rows * std::max(1, (tiles + chunk - 1) / chunk);
-      work += rows * tiles;
+struct Jobs {
+  int length;  // key tiles
+  int64_t count;
+};
+
+// When the last of the blocks ends, one a multiprocessor, longest first.  Multiprocessors
+// of equal load are one entry of a heap, so that a call of one frame costs a few steps.
+double makespan(std::vector<Jobs>& jobs, std::vector<std::pair<double, int64_t>>& loads, int sms) {
+  constexpr double kBlock = 2.0;  // what a block needs to begin and end, in key tiles
+  const auto later = [](const auto& x, const auto& y) { return x.first > y.first; };
+  if (jobs.size() > 1)
+    std::sort(jobs.begin(), jobs.end(), [](const Jobs& x, const Jobs& y) { return x.length > y.length; });
+  loads.assign(1, {0.0, sms});
+  double end = 0.0;
+  for (const Jobs& job : jobs) {
+    const double length = job.length + kBlock;
+    int64_t left = job.count;
+    const int64_t whole = left / sms;  // rounds that load every multiprocessor alike
+    if (whole > 1) {
+      for (auto& l : loads) end = std::max(end, l.first += (whole - 1) * length);
+      left -= (whole - 1) * sms;
     }
-    const double rounds = static_cast<double>(blocks * heads) / sms;
-    const double even = static_cast<double>(work * heads) / sms + rounds * kBlock;
-    const double time = rounds >= 4.0 ? even + 0.5 * chunk : std::max(even, std::ceil(rounds) * (chunk + kBlock));
+    while (left > 0) {
+      std::pop_heap(loads.begin(), loads.end(), later);
+      auto& least = loads.back();
+      const int64_t n = std::min(left, least.second);
+      const std::pair<double, int64_t> now(least.first + length, n);
+      if ((least.second -= n) == 0)
+        loads.pop_back();
+      else
+        std::push_heap(loads.begin(), loads.end(), later);
+      loads.push_back(now);
+      std::push_heap(loads.begin(), loads.end(), later);
+      end = std::max(end, now.first);
+      left -= n;
+    }
+  }
+  return end;
+}
+
+// How many key tiles a block takes: the count with the earliest end, in units of a key
+// tile's time (some 1.7 us).  Keys cut into parts cost the parts' outputs (32-bit,
+// written and read again, some 4 TB/s) and kJoin for one more launch.
+int chunk_of(const AttnArgs& a, int heads, int sms) {
+  constexpr double kJoin = 2.0, kBytes = 6.8e6;
+  int most = 1;
+  int64_t work = 0, blocks = 0;
+  for (int f = 0; f < a.frames; ++f) {
+    const int64_t rows = ((static_cast<int64_t>(a.q0[f + 1] - a.q0[f]) << a.pack_log2) + 255) / 256;
+    const int tiles = (a.k0[f + 1] - a.k0[f] + 127) / 128;
+    most = std::max(most, tiles);
+    work += rows * tiles * heads;
+    blocks += rows * heads;
+  }
+  // With many blocks the rounds blur; with much work nothing is left to be won.
+  if (blocks >= 4 * static_cast<int64_t>(sms)) return most;
+  std::vector<Jobs> jobs;
+  std::vector<std::pair<double, int64_t>> loads;
+  jobs.reserve(2 * a.frames);
+  loads.reserve(32);
+  auto cost = [&](int chunk) {
+    jobs.clear();
+    for (int f = 0; f < a.frames; ++f) {
+      const int64_t rows = ((static_cast<int64_t>(a.q0[f + 1] - a.q0[f]) << a.pack_log2) + 255) / 256 * heads;
+      const int tiles = (a.k0[f + 1] - a.k0[f] + 127) / 128;
+      if (rows && tiles / chunk) jobs.push_back({chunk, rows * (tiles / chunk)});
+      if (rows && tiles % chunk) jobs.push_back({tiles % chunk, rows});
+    }
     const int parts = (most + chunk - 1) / chunk;
-    return time + (parts > 1 ? kJoin + 8.0 * parts * a.queries * a.H * a.D / kBytes : 0.0);
+    return makespan(jobs, loads, sms) + (parts > 1 ? kJoin + 8.0 * parts * a.queries * a.H * a.D / kBytes : 0.0);
   };
   int best = most;
   double least = cost(most);
-  for (int parts = 2; parts <= 64 && parts <= most; ++parts) {
+  const double floor = static_cast<double>(work) / sms;
+  for (int parts : {2, 3, 4, 5, 6, 7, 8, 9, 10, 12, 14, 16, 18, 20, 24, 28, 32, 40, 48, 64}) {
+    if (parts > most || least < 1.1 * floor) break;
     const int chunk = (most + parts - 1) / parts;
     const double c = cost(chunk);
     if (c < least) {

@@ -620,38 +620,66 @@ __global__ void __launch_bounds__(kThreads, 1)
   allow_next_grid();
 }
 
-// Joins the parts of a row: weights 2^(top - highest top), in order.
-template <typename T>
+// Joins the parts of a row: weights 2^(top - highest top), in order.  kLanes lanes a row,
+// four elements a lane; a part's maximum and sum are read by one of them, the outputs
+// eight parts at a time.
+template <typename T, int kLanes>
 __global__ void __launch_bounds__(128) pv_attn_join_kernel(const __grid_constant__ AttnArgs a) {
   wait_prior_grid();
-  const long long w = (static_cast<long long>(blockIdx.x) * 128 + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
-  if (w < static_cast<long long>(a.queries) * a.H) {
-    const int row = static_cast<int>(w / a.H), h = static_cast<int>(w % a.H);
-    const int f = frame_of(a.q0, a.frames, row);
-    const int nk = a.k0[f + 1] - a.k0[f];
-    const int splits = max(1, ((nk + kRows - 1) / kRows + a.chunk - 1) / a.chunk);
-    float top = -INFINITY;
-    for (int s = 0; s < splits; ++s) top = fmaxf(top, a.part_ml[(static_cast<long long>(s) * a.queries + row) * a.H + h].x);
-    float sum = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int s = 0; s < splits; ++s) {
-      const long long at = (static_cast<long long>(s) * a.queries + row) * a.H + h;
-      const float2 ml = a.part_ml[at];
-      const float by = ml.x == -INFINITY ? 0.0f : exp2_fast(ml.x - top);
-      sum = fmaf(ml.y, by, sum);
+  const long long step = static_cast<long long>(a.queries) * a.H;
+  const long long first = (static_cast<long long>(blockIdx.x) * 128 + threadIdx.x) / kLanes;
+  const int lane = threadIdx.x % kLanes;
+  const bool any = first < step, on = any && lane * 4 < a.D;
+  const int row = any ? static_cast<int>(first / a.H) : 0, h = any ? static_cast<int>(first % a.H) : 0;
+  const int f = frame_of(a.q0, a.frames, row);
+  const int tiles = (a.k0[f + 1] - a.k0[f] + kRows - 1) / kRows;
+  const int parts = any ? max(1, (tiles + a.chunk - 1) / a.chunk) : 0;
+  const float* at = a.part_o + first * a.D + lane * 4;
+  float top = -INFINITY, sum = 0.0f, v[4] = {};
+  for (int x = 0; __any_sync(0xFFFFFFFFu, x < parts); x += kLanes) {
+    const float2 ml = x + lane < parts ? a.part_ml[first + (x + lane) * step] : make_float2(-INFINITY, 0.0f);
+    float m = fmaxf(top, ml.x);
 #pragma unroll
-      for (int x = 0; x < 4; ++x)
-        if (lane * 4 + x < a.D) v[x] = fmaf(a.part_o[at * a.D + lane * 4 + x], by, v[x]);
+    for (int o = kLanes / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    const float keep = top == -INFINITY ? 0.0f : exp2_fast(top - m), by = ml.x == -INFINITY ? 0.0f : exp2_fast(ml.x - m);
+    float s = ml.y * by;
+#pragma unroll
+    for (int o = kLanes / 2; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    top = m;
+    sum = fmaf(sum, keep, s);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) v[c] *= keep;
+#pragma unroll 1
+    for (int p0 = 0; p0 < kLanes && __any_sync(0xFFFFFFFFu, x + p0 < parts); p0 += 8) {
+      float4 o[8];
+#pragma unroll
+      for (int p = 0; p < 8; ++p)
+        if (on && x + p0 + p < parts) o[p] = *reinterpret_cast<const float4*>(at + (x + p0 + p) * step * a.D);
+#pragma unroll
+      for (int p = 0; p < 8; ++p) {
+        const float b = __shfl_sync(0xFFFFFFFFu, by, p0 + p, kLanes);
+        if (on && x + p0 + p < parts) {
+          v[0] = fmaf(o[p].x, b, v[0]);
+          v[1] = fmaf(o[p].y, b, v[1]);
+          v[2] = fmaf(o[p].z, b, v[2]);
+          v[3] = fmaf(o[p].w, b, v[3]);
+        }
+      }
     }
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-    T* out = reinterpret_cast<T*>(a.o.data + row * a.o.row + h * a.o.head);
-#pragma unroll
-    for (int x = 0; x < 4; ++x)
-      if (lane * 4 + x < a.D) out[lane * 4 + x] = Pack<T>::one(v[x] * inv);
-    if (a.lse && lane == 0)
-      a.lse[static_cast<long long>(h) * a.queries + row] = sum > 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY;
   }
+  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+  if (on)
+    *reinterpret_cast<uint2*>(a.o.data + row * a.o.row + h * a.o.head + lane * 8) =
+        make_uint2(pack2<T>(v[0] * inv, v[1] * inv), pack2<T>(v[2] * inv, v[3] * inv));
+  if (any && a.lse && lane == 0)
+    a.lse[static_cast<long long>(h) * a.queries + row] = sum > 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY;
   allow_next_grid();
+}
+
+template <int kLanes>
+int launch_join(const AttnArgs& a, cudaStream_t s) {
+  const long long threads = static_cast<long long>(a.queries) * a.H * kLanes;
+  return launch_pdl(pv_attn_join_kernel<Storage, kLanes>, dim3(static_cast<unsigned>((threads + 127) / 128)), 128, 0, s, a);
 }
 
 template <int kBlocks, bool kCap, bool kSlopes>
@@ -673,8 +701,7 @@ int with_scores(const AttnArgs& a, const AttnMaps& m, dim3 grid, cudaStream_t s)
 int PV_ATTN_NAME(attn_forward)(const AttnArgs& a, const AttnMaps& m, dim3 grid, cudaStream_t s) {
   const int st = a.D > 64 ? with_scores<2>(a, m, grid, s) : with_scores<1>(a, m, grid, s);
   if (st != PV_OK || !a.part_o) return st;
-  const long long warps = static_cast<long long>(a.queries) * a.H;
-  return launch_pdl(pv_attn_join_kernel<Storage>, dim3(static_cast<unsigned int>((warps + 3) / 4)), 128, 0, s, a);
+  return a.D > 64 ? launch_join<32>(a, s) : a.D > 32 ? launch_join<16>(a, s) : launch_join<8>(a, s);
 }
 
 }  // namespace pvs
