@@ -203,7 +203,7 @@ __device__ __forceinline__ void gradients(uint32_t at, const float* side, Rows& 
 
 // The cap and the slopes are compile-time choices: code that a launch does not run
 // still costs it instruction fetches (2 x 4096 tokens, 64-element heads, forward and
-// backward: 411 us with both as branches, 3XX us so).
+// backward: 411 us with both as branches, 375 us so).
 template <typename T, int kBlocks, bool kDkv, bool kCap, bool kSlopes>
 __global__ void __launch_bounds__(kThreads, 1)
     pv_attn_bwd_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap mq,

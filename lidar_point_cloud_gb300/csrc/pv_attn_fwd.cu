@@ -1,10 +1,10 @@
 // Attention inside frames, forward, on the tensor cores.
 //
 // A block takes two tiles of 128 query rows and walks the frame's keys in
-// tiles of 128.  Warps 0-3 and 4-7 own a query tile each, one row a thread: they
-// read the scores from tensor memory, keep the row's running maximum and sum,
-// and write the probabilities back over the scores as the next product's
-// operand.  Warp 8 issues the products, warp 9 the TMA loads of keys and values
+// tiles of 128.  Warps 0-3 and 4-7 own a query tile each: they read the scores from
+// tensor memory (a row a thread, or, with distances, fragments of four rows), keep
+// the rows' running maxima and sums, and write the probabilities back over the
+// scores as the next product's operand.  Warp 8 issues the products, warp 9 the TMA loads of keys and values
 // into a ring of shared-memory slots, warp 10 puts key positions there, warp 11
 // clears what a frame's last tile holds of the next frame.  While
 // one tile's scores go through the exponential, the other tile's products run.
