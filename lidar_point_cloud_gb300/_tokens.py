@@ -100,10 +100,18 @@ def _offsets(seq: Sequence[int], rows: int, name: str):
     return off, n
 
 
-def _stream(stream, t) -> int:
-    if stream is None:
-        return _torch()._C._cuda_getCurrentRawStream(t.get_device())
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+def _stream(t) -> int:
+    return _torch()._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def _on(stream, t):
+    """`stream` (a torch stream or a handle) made the current one, so that outputs come
+    from its memory: what another stream still uses is not handed to it."""
+    torch = _torch()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        stream = torch.cuda.ExternalStream(handle, device=t.device)
+    return torch.cuda.stream(stream)
 
 
 def _check(status: int, where: str) -> None:
@@ -144,6 +152,9 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps: float = 1e-
     coordinates as they stand, e.g. ``coords[:, 1:]``).  ``out`` = (q, k)
     buffers, which may be the inputs.  Returns (q, k).
     """
+    if stream is not None:
+        with _on(stream, q):
+            return qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps, out)
     hq, hk = _heads(q, "q"), _heads(k, "k", q, 1)
     p = _rope_params(q, k, q_weight, k_weight, positions, inv_freq, eps)
     if out is None:
@@ -151,7 +162,7 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps: float = 1e-
     else:
         oq, ok = out
         hoq, hok = _heads(oq, "out q", q), _heads(ok, "out k", k)
-    _check(load().pv_qk_norm_rope(p, hq, hk, hoq, hok, _stream(stream, q)), "pv_qk_norm_rope")
+    _check(load().pv_qk_norm_rope(p, hq, hk, hoq, hok, _stream(q)), "pv_qk_norm_rope")
     return oq, ok
 
 
@@ -159,6 +170,9 @@ def qk_norm_rope_backward(dout_q, dout_k, q, k, q_weight, k_weight, positions, i
                           stream=None):
     """Gradients of :func:`qk_norm_rope` from those of its outputs and its
     inputs: (dq, dk, dq_weight, dk_weight), the last two float32."""
+    if stream is not None:
+        with _on(stream, q):
+            return qk_norm_rope_backward(dout_q, dout_k, q, k, q_weight, k_weight, positions, inv_freq, eps)
     torch = _torch()
     hq, hk = _heads(q, "q"), _heads(k, "k", q, 1)
     p = _rope_params(q, k, q_weight, k_weight, positions, inv_freq, eps)
@@ -167,7 +181,7 @@ def qk_norm_rope_backward(dout_q, dout_k, q, k, q_weight, k_weight, positions, i
     dw = torch.empty((2, D), dtype=torch.float32, device=q.device)
     at = dw.data_ptr()
     _check(load().pv_qk_norm_rope_backward(p, _heads(dout_q, "dout_q", q), _heads(dout_k, "dout_k", k), hq, hk, hdq, hdk,
-                                           at, at + 4 * D, _stream(stream, q)), "pv_qk_norm_rope_backward")
+                                           at, at + 4 * D, _stream(q)), "pv_qk_norm_rope_backward")
     return dq, dk, dw[0], dw[1]
 
 
@@ -222,16 +236,20 @@ def attention(q, k, v, q_offsets, k_offsets, scale: Optional[float] = None, cap:
     gives 0.  Returns out [queries, H, D], with ``return_lse`` also the float32
     [H, queries] logarithms of the softmax sums for :func:`attention_backward`.
     """
+    if stream is not None:
+        with _on(stream, q):
+            return attention(q, k, v, q_offsets, k_offsets, scale, cap, slopes, q_positions, k_positions, causal, prefix,
+                             return_lse, out)
     hq, hk, hv = _heads(q, "q"), _heads(k, "k", q, 1), _heads(v, "v", k)
     p, _alive = _attention_params(q, k, v, q_offsets, k_offsets, scale, cap, slopes, q_positions, k_positions, causal,
                                   prefix)
     o, ho = _new(q) if out is None else (out, _heads(out, "out", q))
     if not return_lse:
-        _check(load().pv_attention(p, hq, hk, hv, ho, None, _stream(stream, q)), "pv_attention")
+        _check(load().pv_attention(p, hq, hk, hv, ho, None, _stream(q)), "pv_attention")
         return o
     torch = _torch()
     lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
-    _check(load().pv_attention(p, hq, hk, hv, ho, lse.data_ptr(), _stream(stream, q)), "pv_attention")
+    _check(load().pv_attention(p, hq, hk, hv, ho, lse.data_ptr(), _stream(q)), "pv_attention")
     return o, lse
 
 
@@ -240,13 +258,17 @@ def attention_backward(dout, q, k, v, out, lse, q_offsets, k_offsets, scale: Opt
                        stream=None):
     """Gradients (dq, dk, dv) of :func:`attention` from that of its output,
     its inputs, ``out`` and ``lse``; the other arguments as there."""
+    if stream is not None:
+        with _on(stream, q):
+            return attention_backward(dout, q, k, v, out, lse, q_offsets, k_offsets, scale, cap, slopes, q_positions,
+                                      k_positions, causal, prefix)
     hq, hk, hv = _heads(q, "q"), _heads(k, "k", q, 1), _heads(v, "v", k)
     p, _alive = _attention_params(q, k, v, q_offsets, k_offsets, scale, cap, slopes, q_positions, k_positions, causal,
                                   prefix)
     (dq, hdq), (dk, hdk), (dv, hdv) = _new(q), _new(k), _new(k)
     _check(load().pv_attention_backward(
         p, _heads(dout, "dout", q), hq, hk, hv, _heads(out, "out", q),
-        _floats(lse, (q.shape[1], q.shape[0]), q.get_device(), "lse"), hdq, hdk, hdv, _stream(stream, q)),
+        _floats(lse, (q.shape[1], q.shape[0]), q.get_device(), "lse"), hdq, hdk, hdv, _stream(q)),
         "pv_attention_backward")
     return dq, dk, dv
 
@@ -295,6 +317,9 @@ def gated_scan(x, gate, offsets, h0=None, reverse: bool = False, return_states: 
     with ``return_states`` also the states that :func:`gated_scan_backward`
     starts from.
     """
+    if stream is not None:
+        with _on(stream, x):
+            return gated_scan(x, gate, offsets, h0, reverse, return_states, out)
     torch = _torch()
     p, _alive = _scan_params(x, gate, offsets, reverse)
     C = x.shape[1]
@@ -308,13 +333,16 @@ def gated_scan(x, gate, offsets, h0=None, reverse: bool = False, return_states: 
     last = torch.empty(state, dtype=torch.float32, device=x.device)
     states = torch.empty((_states(lib, p), C), dtype=torch.float32, device=x.device) if return_states else None
     _check(lib.pv_gated_scan(p, None if h0 is None else _floats(h0, state, x.get_device(), "h0"), h, hs, last.data_ptr(),
-                             states.data_ptr() if return_states else None, _stream(stream, x)), "pv_gated_scan")
+                             states.data_ptr() if return_states else None, _stream(x)), "pv_gated_scan")
     return (out, last, states) if return_states else (out, last)
 
 
 def gated_scan_backward(dh, dlast, x, gate, states, offsets, reverse: bool = False, stream=None):
     """Gradients (dx, dgate, dh0) of :func:`gated_scan` from those of h and of
     the last states (``dlast`` None: zeros), its inputs and its ``states``."""
+    if stream is not None:
+        with _on(stream, x):
+            return gated_scan_backward(dh, dlast, x, gate, states, offsets, reverse)
     p, _alive = _scan_params(x, gate, offsets, reverse)
     C, dev = x.shape[1], x.get_device()
     state = (p.frames, C)
@@ -326,5 +354,5 @@ def gated_scan_backward(dh, dlast, x, gate, states, offsets, reverse: bool = Fal
     _check(lib.pv_gated_scan_backward(
         p, dhp, dhs, None if dlast is None else _floats(dlast, state, dev, "dlast"),
         _floats(states, (_states(lib, p), C), dev, "states"), dx.data_ptr(), C, dgate.data_ptr(), C, dh0.data_ptr(),
-        _stream(stream, x)), "pv_gated_scan_backward")
+        _stream(x)), "pv_gated_scan_backward")
     return dx, dgate, dh0
