@@ -85,6 +85,8 @@ int pack_of(int G) {
   return p;
 }
 
+constexpr double kBlock = 2.0;  // what a block needs to begin and end, in key tiles
+
 struct Jobs {
   int length;  // key tiles
   int64_t count;
@@ -93,7 +95,6 @@ struct Jobs {
 // When the last of the blocks ends, one a multiprocessor, longest first.  Multiprocessors
 // of equal load are one entry of a heap, so that a call of one frame costs a few steps.
 double makespan(std::vector<Jobs>& jobs, std::vector<std::pair<double, int64_t>>& loads, int sms) {
-  constexpr double kBlock = 2.0;  // what a block needs to begin and end, in key tiles
   const auto later = [](const auto& x, const auto& y) { return x.first > y.first; };
   if (jobs.size() > 1)
     std::sort(jobs.begin(), jobs.end(), [](const Jobs& x, const Jobs& y) { return x.length > y.length; });
@@ -127,46 +128,61 @@ double makespan(std::vector<Jobs>& jobs, std::vector<std::pair<double, int64_t>>
 
 // How many key tiles a block takes: the count with the earliest end, in units of a key
 // tile's time (some 1.7 us).  Keys cut into parts cost the parts' outputs (32-bit,
-// written and read again, some 4 TB/s) and kJoin for one more launch.
+// written and read again, some 4 TB/s) and kJoin for one more launch.  A schedule is played
+// through only while its least possible end (all multiprocessors busy throughout, or the
+// longest block alone) is below the best found, the likeliest first: a few of the list.
 int chunk_of(const AttnArgs& a, int heads, int sms) {
   constexpr double kJoin = 2.0, kBytes = 6.8e6;
-  int most = 1;
+  constexpr int kParts[] = {1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 12, 14, 16, 18, 20, 24, 28, 32, 40, 48, 64};
+  constexpr int kTries = sizeof(kParts) / sizeof(kParts[0]);
+  int rows[PV_MAX_FRAMES], tiles[PV_MAX_FRAMES];  // blocks' rows of all heads, key tiles
+  int most = 1, frames = 0;
   int64_t work = 0, blocks = 0;
   for (int f = 0; f < a.frames; ++f) {
-    const int64_t rows = ((static_cast<int64_t>(a.q0[f + 1] - a.q0[f]) << a.pack_log2) + 255) / 256;
-    const int tiles = (a.k0[f + 1] - a.k0[f] + 127) / 128;
-    most = std::max(most, tiles);
-    work += rows * tiles * heads;
-    blocks += rows * heads;
+    const int64_t r = ((static_cast<int64_t>(a.q0[f + 1] - a.q0[f]) << a.pack_log2) + 255) / 256 * heads;
+    const int t = (a.k0[f + 1] - a.k0[f] + 127) / 128;
+    most = std::max(most, t);
+    work += r * t;
+    blocks += r;
+    // With many blocks the rounds blur; with much work nothing is left to be won.
+    if (blocks >= 4 * static_cast<int64_t>(sms)) continue;
+    if (r && t) rows[frames] = static_cast<int>(r), tiles[frames++] = t;
   }
-  // With many blocks the rounds blur; with much work nothing is left to be won.
-  if (blocks >= 4 * static_cast<int64_t>(sms)) return most;
+  if (blocks >= 4 * static_cast<int64_t>(sms) || !frames) return most;
+  struct Try {
+    double least;
+    int chunk;
+  } tries[kTries];
+  int n = 0;
+  auto extra = [&](int chunk) {
+    const int parts = (most + chunk - 1) / chunk;
+    return parts > 1 ? kJoin + 8.0 * parts * a.queries * a.H * a.D / kBytes : 0.0;
+  };
+  for (int parts : kParts) {
+    if (parts > most) break;
+    const int chunk = (most + parts - 1) / parts;
+    if (n && tries[n - 1].chunk == chunk) continue;
+    int64_t count = 0;
+    for (int f = 0; f < frames; ++f) count += static_cast<int64_t>(rows[f]) * ((tiles[f] + chunk - 1) / chunk);
+    const double even = (static_cast<double>(work) + count * kBlock) / sms;
+    tries[n++] = {std::max(even, chunk + kBlock) + extra(chunk), chunk};
+  }
+  std::stable_sort(tries, tries + n, [](const Try& x, const Try& y) { return x.least < y.least; });
   std::vector<Jobs> jobs;
   std::vector<std::pair<double, int64_t>> loads;
-  jobs.reserve(2 * a.frames);
+  jobs.reserve(2 * frames);
   loads.reserve(32);
-  auto cost = [&](int chunk) {
-    jobs.clear();
-    for (int f = 0; f < a.frames; ++f) {
-      const int64_t rows = ((static_cast<int64_t>(a.q0[f + 1] - a.q0[f]) << a.pack_log2) + 255) / 256 * heads;
-      const int tiles = (a.k0[f + 1] - a.k0[f] + 127) / 128;
-      if (rows && tiles / chunk) jobs.push_back({chunk, rows * (tiles / chunk)});
-      if (rows && tiles % chunk) jobs.push_back({tiles % chunk, rows});
-    }
-    const int parts = (most + chunk - 1) / chunk;
-    return makespan(jobs, loads, sms) + (parts > 1 ? kJoin + 8.0 * parts * a.queries * a.H * a.D / kBytes : 0.0);
-  };
   int best = most;
-  double least = cost(most);
-  const double floor = static_cast<double>(work) / sms;
-  for (int parts : {2, 3, 4, 5, 6, 7, 8, 9, 10, 12, 14, 16, 18, 20, 24, 28, 32, 40, 48, 64}) {
-    if (parts > most || least < 1.1 * floor) break;
-    const int chunk = (most + parts - 1) / parts;
-    const double c = cost(chunk);
-    if (c < least) {
-      least = c;
-      best = chunk;
+  double least = INFINITY;
+  for (int i = 0; i < n && tries[i].least < least; ++i) {
+    const int chunk = tries[i].chunk;
+    jobs.clear();
+    for (int f = 0; f < frames; ++f) {
+      if (tiles[f] / chunk) jobs.push_back({chunk, static_cast<int64_t>(rows[f]) * (tiles[f] / chunk)});
+      if (tiles[f] % chunk) jobs.push_back({tiles[f] % chunk, rows[f]});
     }
+    const double cost = makespan(jobs, loads, sms) + extra(chunk);
+    if (cost < least) least = cost, best = chunk;
   }
   return best;
 }
