@@ -10,7 +10,7 @@
 // every thread runs its steps from its own start and writes them.
 //
 // The state before a tile is always worked out in the same order, whatever
-// blocks finish first: tiles come in groups of kGroup, the state before a
+// blocks finish first: tiles come in groups of kGroup or fewer, the state before a
 // group (its base) is published by the last tile of the group before, and a
 // tile composes the maps of the tiles ahead of it in its group, in order, onto
 // its group's base.  So a link of the chain along a frame is one group, and
@@ -44,7 +44,7 @@ using namespace pvs;
 
 constexpr int kThreads = 256;
 constexpr int kSteps = 16;   // steps of a thread
-constexpr int kGroup = 16;   // tiles of a group
+constexpr int kGroup = 8;    // tiles of a group at most
 constexpr int kMaxSlab = 64; // channels of a block: 32 lanes of 2
 constexpr unsigned long long kWaitNs = 1000000000ull;  // bounded waits: 1 s
 
@@ -61,7 +61,7 @@ struct ScanArgs {
   unsigned long long* maps;   // published: [tiles][A, B][channels]
   unsigned long long* bases;  // published: [groups][channels]
   unsigned int* ctl;    // finished blocks, epoch
-  int channels, slabs, lanes_log2, frames, tiles, reverse, steps;
+  int channels, slabs, lanes_log2, frames, tiles, reverse, steps, group_log2;
   int row0[PV_MAX_FRAMES + 1];   // row offsets of the frames
   int tile0[PV_MAX_FRAMES + 1];  // first tile of each frame
   int group0[PV_MAX_FRAMES + 1]; // first group of each frame
@@ -313,7 +313,8 @@ __global__ void __launch_bounds__(kThreads, 2) pv_scan_kernel(const __grid_const
     // will need: read now, looked at (and if need be awaited) after its own maps.
     const int t0 = a.tile0[now.frame], nt = a.tile0[now.frame + 1] - t0;
     const int place = kBack ? nt - 1 - (now.tile - t0) : now.tile - t0;
-    const int group = place / kGroup, ahead = place - group * kGroup;
+    const int group = place >> a.group_log2, ahead = place - (group << a.group_log2);
+    const bool closes = ahead + 1 == 1 << a.group_log2;  // the last of its group
     const int c0 = now.slab * width, own = c0 + threadIdx.x;
     const bool owner = threadIdx.x < width && own < C;
     auto map_at = [&](int k) {  // of the chain's tile k: A, then B, of channel 0
@@ -323,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 2) pv_scan_kernel(const __grid_const
     constexpr int kTurns = kGroup * 32 * V / kThreads;
     const int c = threadIdx.x & (width - 1), j0 = threadIdx.x >> width_log2, j_step = kThreads >> width_log2;
     const int wanted = c0 + c < C ? ahead : 0;
-    const unsigned long long* const ahead_at = map_at(group * kGroup + j0) + c0 + c;
+    const unsigned long long* const ahead_at = map_at((group << a.group_log2) + j0) + c0 + c;
     const long long ahead_step = static_cast<long long>(kBack ? -2 : 2) * C * j_step;
     unsigned long long early[kTurns][2];
 #pragma unroll
@@ -421,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 2) pv_scan_kernel(const __grid_const
         }
       }
     }
-    if (owner) {
+    if (owner && !closes) {
       put(map_at(place) + own, TA, epoch);
       put(map_at(place) + C + own, TB, epoch);
     }
@@ -433,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 2) pv_scan_kernel(const __grid_const
         fetch[j][1][c] = take(early[q][1], ahead_at + q * ahead_step + C, epoch);
       }
     }
-    __syncthreads();
+    if (ahead) __syncthreads();
     if (owner) {
       // The maps ahead are joined before the base is waited for: a link of the
       // chain is one multiply-add.
@@ -448,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 2) pv_scan_kernel(const __grid_const
       carry[threadIdx.x] = s;
       if (place == nt - 1) {
         if (a.last) a.last[static_cast<long long>(now.frame) * C + own] = after;
-      } else if (ahead == kGroup - 1) {
+      } else if (closes) {
         put(a.bases + static_cast<long long>(a.group0[now.frame] + group + 1) * C + own, after, epoch);
       }
       if (!kBack && a.states) a.states[static_cast<long long>(now.tile) * C + own] = s;
@@ -512,7 +513,8 @@ __global__ void __launch_bounds__(kThreads, 2) pv_scan_kernel(const __grid_const
       else
         run(std::false_type{});
     }
-    __syncthreads();  // the maps and the carry are free for the next tile
+    // (No barrier here: of what the next tile writes before its first one, the other threads
+    // read nothing any more.)
   }
   leave(a);
   allow_next_grid();
@@ -522,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 2) pv_scan_kernel(const __grid_const
 
 struct Shape {
   int vec, lanes_log2, steps, slabs, elem;
-  int64_t tiles, groups;
+  int64_t tiles;
 };
 
 // Two 16-bit channels share a 32-bit word where every row begins on one.
@@ -536,11 +538,10 @@ int shape_of(const pv_scan_params* p, bool pairs, Shape* s) {
   while ((1 << s->lanes_log2) < 32 && (int64_t(1) << s->lanes_log2) < words) ++s->lanes_log2;
   s->steps = (kThreads >> s->lanes_log2) * kSteps;
   s->slabs = static_cast<int>((words + (1 << s->lanes_log2) - 1) >> s->lanes_log2);
-  s->tiles = s->groups = 0;
+  s->tiles = 0;
   for (int b = 0; b < p->frames; ++b) {
     const int64_t t = (p->offsets[b + 1] - p->offsets[b] + s->steps - 1) / s->steps;
     s->tiles += t;
-    s->groups += (t + kGroup - 1) / kGroup;
   }
   return s->tiles * s->slabs < (int64_t(1) << 31) ? PV_OK : PV_ERR_TOO_LARGE;
 }
@@ -607,25 +608,34 @@ int start(const pv_scan_params* p, const Shape& sh, ScanArgs& a, int dev, pv_str
   a.tiles = static_cast<int>(sh.tiles);
   a.reverse = p->reverse != 0;
   a.steps = sh.steps;
+  const int sms = sm_count(dev);
+  if (sms < 1) return PV_ERR_CUDA;
+  int frames = 0;
+  for (int b = 0; b < p->frames; ++b) frames += p->offsets[b + 1] > p->offsets[b];
+  // Groups shorten a chain whose tiles are worked on side by side, and cost their maps'
+  // publishing and joining: half as many tiles as one chain has in flight.  (Forward and
+  // backward, bf16, 512 channels, groups of 1 and 8: 32 frames of up to 9,000 steps,
+  // 256 chains, 427 and 448 us; one frame of 60,000, 8 chains, 457 and 214 us.)
+  const int64_t chains = std::max<int64_t>(1, static_cast<int64_t>(frames) * sh.slabs);
+  a.group_log2 = 0;
+  while ((1 << a.group_log2) < kGroup && (chains << a.group_log2) * 4 <= 2 * sms) ++a.group_log2;
   for (int b = 0; b < p->frames; ++b) {
     const int64_t t = (p->offsets[b + 1] - p->offsets[b] + sh.steps - 1) / sh.steps;
     a.row0[b + 1] = static_cast<int>(p->offsets[b + 1]);
     a.tile0[b + 1] = a.tile0[b] + static_cast<int>(t);
-    a.group0[b + 1] = a.group0[b] + static_cast<int>((t + kGroup - 1) / kGroup);
+    a.group0[b + 1] = a.group0[b] + static_cast<int>((t + (1 << a.group_log2) - 1) >> a.group_log2);
     a.order[b] = static_cast<unsigned char>(b);
   }
   std::stable_sort(a.order, a.order + p->frames, [&](unsigned char x, unsigned char y) {
     return a.tile0[x + 1] - a.tile0[x] > a.tile0[y + 1] - a.tile0[y];
   });
   Scratch scratch;
-  const size_t words = static_cast<size_t>(2 * sh.tiles + sh.groups) * p->channels;
+  const size_t words = static_cast<size_t>(2 * sh.tiles + a.group0[p->frames]) * p->channels;
   int st = scratch.open(dev, stream, kTagged, 8 * words);
   if (st != PV_OK) return st;
   a.ctl = static_cast<unsigned int*>(scratch.head());
   a.maps = static_cast<unsigned long long*>(scratch.body());
   a.bases = a.maps + 2 * sh.tiles * p->channels;
-  const int sms = sm_count(dev);
-  if (sms < 1) return PV_ERR_CUDA;
   if (p->dtype == PV_F32) return run<float, 1, kBack>(a, sh, dev, sms, stream);
   if (p->dtype == PV_BF16)
     return sh.vec == 2 ? run<__nv_bfloat16, 2, kBack>(a, sh, dev, sms, stream)
