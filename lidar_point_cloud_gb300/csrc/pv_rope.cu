@@ -9,7 +9,9 @@
 // are worked out once for all heads, into shared memory.
 //
 // Bound by memory: each element is read once and written once (backward: two
-// reads and one write).
+// reads and one write).  Measured at 96,001 rows of 2 x 8 heads of 64, bf16: forward
+// 70 us (5.6 TB/s), backward 152 us (3.9 TB/s; its weight sums take the registers of
+// half the warps).
 
 #include "pv_seq.cuh"
 

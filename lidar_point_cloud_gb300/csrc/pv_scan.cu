@@ -31,6 +31,11 @@
 // h[t-1] is rebuilt inside the tile and x, gate and dh are read once.
 //
 // Bound by memory: forward 2 reads and 1 write per element, backward 3 and 2.
+// Measured at 204,057 steps of 512 channels in 32 frames, bf16: forward 150 us,
+// backward 250 us, 4.2 TB/s of these bytes; half of the issue slots, the barriers of
+// a tile the largest stall.  Two blocks a multiprocessor: three (forward, 85 registers
+// a thread) wait more for one another (425 us for both passes against 408), as do
+// blocks of 128 threads (420) and as many blocks as chains (462).
 
 #include "pv_seq.cuh"
 
