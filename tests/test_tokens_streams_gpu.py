@@ -54,3 +54,23 @@ def test_outputs_are_not_memory_that_another_stream_may_still_use():
     assert h.data_ptr() != at
     h, _ = pv.gated_scan(x, x, [0, 4096])
     assert h.data_ptr() == at
+
+
+def test_captured_in_a_graph():
+    # Warm workspaces: nothing is allocated but outputs, nothing synchronizes.
+    t = inputs()
+    want = run(*t)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run(*t)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        got = run(*t)
+    for _ in range(3):
+        for x in got:
+            x.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
