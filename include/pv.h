@@ -306,7 +306,9 @@ typedef enum pv_dtype { PV_F32 = 0, PV_BF16 = 1, PV_F16 = 2 } pv_dtype;
 
 /* Rows of heads: element (row, head, d) is data[row * row_stride + head *
  * head_stride + d], strides in elements.  data and both strides are multiples
- * of 16 bytes, so slices of a fused projection can be passed as they are. */
+ * of 16 bytes, so slices of a fused projection can be passed as they are.  What a
+ * call reads may have a stride of 0 (one row or head seen as many), but for the rows
+ * of q, k, v and dout of attention, if there is more than one; what it writes may not. */
 typedef struct pv_heads {
   void* data;
   int64_t row_stride;

@@ -30,10 +30,12 @@ def _dtype(t, name: str, wide: bool = True) -> int:
     return code
 
 
-def _heads(t, name: str, like=None, heads: Optional[int] = None) -> Heads:
+def _heads(t, name: str, like=None, heads: Optional[int] = None, apart: bool = False) -> Heads:
     """[rows, heads, head_dim] as the library reads it: any strides that are
     multiples of 16 bytes, the last dimension dense.  `like`: the tensor whose
-    dtype, device and head_dim (and, with no `heads`, shape) it must have."""
+    dtype, device and head_dim (and, with no `heads`, shape) it must have.
+    `apart`: a tensor expanded over its rows (as the gradient of a sum over them
+    is) is copied, for calls whose rows have to lie apart."""
     shape = t.shape
     if len(shape) != 3:
         raise ValueError(f"{name} must have shape [rows, heads, head_dim]")
@@ -46,12 +48,19 @@ def _heads(t, name: str, like=None, heads: Optional[int] = None) -> Heads:
         if shape[2] != like.shape[2] or (heads is None and shape != like.shape):
             raise ValueError(f"{name} has the wrong shape {tuple(shape)}")
     row, head, one = t.stride()
+    copy = apart and row == 0 and shape[0] > 1
+    if copy:
+        t = t.contiguous()
+        row, head, one = t.stride()
     at = t.data_ptr()
     size = t.element_size()
     if (at | row * size | head * size) & 15 or one != 1 or row < 0:
         if t.numel() and not (one != 1 and shape[2] == 1 and not (at | row * size | head * size) & 15):
             raise ValueError(f"{name}: head_dim must be dense, its rows and heads on 16-byte boundaries")
-    return Heads(at, row, head)
+    h = Heads(at, row, head)
+    if copy:
+        h.kept = t  # until the call that reads it has been enqueued
+    return h
 
 
 def _dense(like):
@@ -240,7 +249,7 @@ def attention(q, k, v, q_offsets, k_offsets, scale: Optional[float] = None, cap:
         with _on(stream, q):
             return attention(q, k, v, q_offsets, k_offsets, scale, cap, slopes, q_positions, k_positions, causal, prefix,
                              return_lse, out)
-    hq, hk, hv = _heads(q, "q"), _heads(k, "k", q, 1), _heads(v, "v", k)
+    hq, hk, hv = _heads(q, "q", apart=True), _heads(k, "k", q, 1, apart=True), _heads(v, "v", k, apart=True)
     p, _alive = _attention_params(q, k, v, q_offsets, k_offsets, scale, cap, slopes, q_positions, k_positions, causal,
                                   prefix)
     o, ho = _new(q) if out is None else (out, _heads(out, "out", q))
@@ -262,12 +271,12 @@ def attention_backward(dout, q, k, v, out, lse, q_offsets, k_offsets, scale: Opt
         with _on(stream, q):
             return attention_backward(dout, q, k, v, out, lse, q_offsets, k_offsets, scale, cap, slopes, q_positions,
                                       k_positions, causal, prefix)
-    hq, hk, hv = _heads(q, "q"), _heads(k, "k", q, 1), _heads(v, "v", k)
+    hq, hk, hv = _heads(q, "q", apart=True), _heads(k, "k", q, 1, apart=True), _heads(v, "v", k, apart=True)
     p, _alive = _attention_params(q, k, v, q_offsets, k_offsets, scale, cap, slopes, q_positions, k_positions, causal,
                                   prefix)
     (dq, hdq), (dk, hdk), (dv, hdv) = _new(q), _new(k), _new(k)
     _check(load().pv_attention_backward(
-        p, _heads(dout, "dout", q), hq, hk, hv, _heads(out, "out", q),
+        p, _heads(dout, "dout", q, apart=True), hq, hk, hv, _heads(out, "out", q),
         _floats(lse, (q.shape[1], q.shape[0]), q.get_device(), "lse"), hdq, hdk, hdv, _stream(q)),
         "pv_attention_backward")
     return dq, dk, dv

@@ -50,6 +50,13 @@ int check_params(const pv_attention_params* p, int* dev, const void* some) {
   return PV_OK;
 }
 
+// Tiles of rows are loaded by a tensor map, whose rows lie apart: a row stride of 0 (one
+// row seen as many) is for a single row only.
+int check_tiles(const pv_heads* h, int64_t rows, int heads, int dev) {
+  const int st = check_heads(h, rows, heads, 2, dev);
+  return st == PV_OK && rows > 1 && h->row_stride == 0 ? PV_ERR_INVALID : st;
+}
+
 AttnArgs args_of(const pv_attention_params* p) {
   AttnArgs a{};
   a.slopes = p->slopes;
@@ -220,7 +227,8 @@ int pvs::make_map(CUtensorMap* map, const View& v, int dtype, int D, int heads, 
     fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
     encode.store(fn);
   }
-  // A head stride of zero is one head that every head reads.
+  // A head stride of zero is one head that every head reads; a row stride of zero has one
+  // row (check_tiles).
   const cuuint64_t head = v.head ? v.head : 16;
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(v.head ? pack : 1),
                               static_cast<cuuint64_t>(v.head ? heads / pack : 1), static_cast<cuuint64_t>(total)};
@@ -242,10 +250,11 @@ extern "C" int pv_attention(const pv_attention_params* params, const pv_heads* q
   if (nq == 0 && !out->data) return PV_OK;
   if ((st = check_params(params, &dev, out->data)) != PV_OK) return st;
   const int64_t nk = params->k_offsets[params->frames];
-  for (const pv_heads* h : {q, out})
-    if ((st = check_heads(h, nq, params->q_heads, 2, dev)) != PV_OK) return st;
+  if ((st = check_tiles(q, nq, params->q_heads, dev)) != PV_OK ||
+      (st = check_out_heads(out, nq, params->q_heads, 2, dev)) != PV_OK)
+    return st;
   for (const pv_heads* h : {k, v})
-    if ((st = check_heads(h, nk, params->k_heads, 2, dev)) != PV_OK) return st;
+    if ((st = check_tiles(h, nk, params->k_heads, dev)) != PV_OK) return st;
   if (lse && (!aligned(lse, 4) || device_of(lse) != dev)) return PV_ERR_INVALID;
   if (nq == 0) return PV_OK;
   DeviceScope scope(dev);
@@ -300,10 +309,15 @@ extern "C" int pv_attention_backward(const pv_attention_params* params, const pv
   const int64_t nq = params->q_offsets[params->frames], nk = params->k_offsets[params->frames];
   if (nq == 0 && nk == 0) return PV_OK;
   if ((st = check_params(params, &dev, nq ? dq->data : dk->data)) != PV_OK) return st;
-  for (const pv_heads* h : {dout, q, out, dq})
-    if ((st = check_heads(h, nq, params->q_heads, 2, dev)) != PV_OK) return st;
-  for (const pv_heads* h : {k, v, dk, dv})
-    if ((st = check_heads(h, nk, params->k_heads, 2, dev)) != PV_OK) return st;
+  for (const pv_heads* h : {dout, q})
+    if ((st = check_tiles(h, nq, params->q_heads, dev)) != PV_OK) return st;
+  for (const pv_heads* h : {k, v})
+    if ((st = check_tiles(h, nk, params->k_heads, dev)) != PV_OK) return st;
+  if ((st = check_heads(out, nq, params->q_heads, 2, dev)) != PV_OK ||
+      (st = check_out_heads(dq, nq, params->q_heads, 2, dev)) != PV_OK)
+    return st;
+  for (const pv_heads* h : {dk, dv})
+    if ((st = check_out_heads(h, nk, params->k_heads, 2, dev)) != PV_OK) return st;
   if (nq && (!lse || !aligned(lse, 4) || device_of(lse) != dev)) return PV_ERR_INVALID;
   DeviceScope scope(dev);
   if (!scope.ok()) return PV_ERR_CUDA;

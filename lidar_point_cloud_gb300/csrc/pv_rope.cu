@@ -414,10 +414,10 @@ extern "C" int pv_qk_norm_rope(const pv_rope_params* params, const pv_heads* q, 
   if (st != PV_OK) return st;
   const int elem = dtype_size(params->dtype);
   if ((st = check_heads(q, params->rows, params->q_heads, elem, dev)) != PV_OK ||
-      (st = check_heads(out_q, params->rows, params->q_heads, elem, dev)) != PV_OK)
+      (st = check_out_heads(out_q, params->rows, params->q_heads, elem, dev)) != PV_OK)
     return st;
   if (params->k_heads && ((st = check_heads(k, params->rows, params->k_heads, elem, dev)) != PV_OK ||
-                          (st = check_heads(out_k, params->rows, params->k_heads, elem, dev)) != PV_OK))
+                          (st = check_out_heads(out_k, params->rows, params->k_heads, elem, dev)) != PV_OK))
     return st;
   if (params->rows == 0) return PV_OK;
   DeviceScope scope(dev);
@@ -443,11 +443,14 @@ extern "C" int pv_qk_norm_rope_backward(const pv_rope_params* params, const pv_h
   int dev = 0, st = check_params(params, &dev);
   if (st != PV_OK) return st;
   const int elem = dtype_size(params->dtype);
-  for (const pv_heads* h : {dout_q, q, dq})
+  for (const pv_heads* h : {dout_q, q})
     if ((st = check_heads(h, params->rows, params->q_heads, elem, dev)) != PV_OK) return st;
-  if (params->k_heads)
-    for (const pv_heads* h : {dout_k, k, dk})
+  if ((st = check_out_heads(dq, params->rows, params->q_heads, elem, dev)) != PV_OK) return st;
+  if (params->k_heads) {
+    for (const pv_heads* h : {dout_k, k})
       if ((st = check_heads(h, params->rows, params->k_heads, elem, dev)) != PV_OK) return st;
+    if ((st = check_out_heads(dk, params->rows, params->k_heads, elem, dev)) != PV_OK) return st;
+  }
   if (!dq_weight || !aligned(dq_weight, 4) || device_of(dq_weight) != dev) return PV_ERR_INVALID;
   if (params->k_heads && (!dk_weight || !aligned(dk_weight, 4) || device_of(dk_weight) != dev)) return PV_ERR_INVALID;
   DeviceScope scope(dev);

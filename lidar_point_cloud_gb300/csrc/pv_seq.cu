@@ -57,6 +57,12 @@ int check_heads(const pv_heads* h, int64_t rows, int heads, int elem, int dev) {
   return device_of(h->data) == dev ? PV_OK : PV_ERR_INVALID;
 }
 
+int check_out_heads(const pv_heads* h, int64_t rows, int heads, int elem, int dev) {
+  const int st = check_heads(h, rows, heads, elem, dev);
+  if (st != PV_OK || rows == 0) return st;
+  return (rows > 1 && h->row_stride == 0) || (heads > 1 && h->head_stride == 0) ? PV_ERR_INVALID : PV_OK;
+}
+
 int Scratch::open(int dev, pv_stream_t stream, ScratchKind kind, size_t bytes) {
   {
     std::lock_guard<std::mutex> lk(g_seq_mu);

@@ -32,6 +32,9 @@ int check_offsets(const int64_t* off, int n);
 // no rows or no heads the data pointer is not looked at.
 int check_heads(const pv_heads* h, int64_t rows, int heads, int elem, int dev);
 
+// The same for what a call writes: its rows and heads do not share memory by a stride of 0.
+int check_out_heads(const pv_heads* h, int64_t rows, int heads, int elem, int dev);
+
 // Makes `dev` current for a scope.
 class DeviceScope {
  public:
