@@ -101,7 +101,10 @@ typedef enum pv_status {
  * does not synchronize: V is read back by the caller when it needs it.
  * The library keeps a grow-only workspace per (device, stream); calls on one
  * stream run one after another, calls on different streams do not share
- * state.  A call that grows the workspace synchronizes the stream once.
+ * state.  A call that grows the workspace synchronizes the stream once.  A call
+ * captured into a graph leaves the address of its stream's workspace there: the graph
+ * is not to be replayed after a later call has grown that workspace or
+ * pv_release_workspace has freed it, nor beside other work that uses it.
  * Returns PV_OK or a negative pv_status found on the host.
  */
 int pv_voxelize(const float* points, int64_t num_points, const float point_cloud_range[6],
@@ -295,7 +298,10 @@ int pv_voxelize_static(const float* points, int64_t num_points, const float poin
  *
  * All of them are asynchronous on `stream`, allocate nothing once their
  * per-(device, stream) workspace is warm (a call that grows it synchronizes
- * the stream once), give the same bits for the same inputs on every call, and
+ * the stream once; a call captured into a graph takes a workspace of the capture's
+ * own, which the graph and what is instantiated from it keep until they are destroyed,
+ * so such graphs run beside one another and beside other calls, but not two
+ * instances of one graph at a time), give the same bits for the same inputs on every call, and
  * check their arguments on the host as pv_voxelize does: a status is returned
  * and nothing is enqueued.  Row offsets are HOST arrays, read before the call
  * returns.  Sums, softmax statistics, norms and recurrent states are held in
@@ -467,7 +473,7 @@ int pv_query_plan(int64_t num_points, const float point_cloud_range[6], const fl
                   int max_points, int max_voxels, const pv_options* options, pv_plan* plan_out);
 
 /* Frees every cached workspace of every device and stream (waits for them
- * to be idle first).  Returns PV_OK or PV_ERR_CUDA. */
+ * to be idle first), but for those of the token operators that a graph owns.  Returns PV_OK or PV_ERR_CUDA. */
 int pv_release_workspace(void);
 
 /* Static, human-readable name of a status. */

@@ -3,6 +3,8 @@
 
 #include "pv_seq.cuh"
 
+#include <atomic>
+#include <list>
 #include <map>
 #include <new>
 #include <tuple>
@@ -14,11 +16,48 @@ struct SeqSpace {
   int device = 0;
   unsigned char* mem = nullptr;
   size_t cap = 0;
+  // Of a captured call: which capture's, and whether its graph still is.
+  ScratchKind kind = kPlain;
+  unsigned long long capture = 0;
+  pv_stream_t stream = nullptr;
+  std::atomic<bool> owned{false};
 };
 
 namespace {
 std::mutex g_seq_mu;
 std::map<std::tuple<int, pv_stream_t, int>, SeqSpace*> g_seq;
+std::list<SeqSpace*> g_captured;
+
+// Runs when the last graph that owns the space is gone (no CUDA calls are allowed here).
+void CUDART_CB give_back(void* space) { static_cast<SeqSpace*>(space)->owned.store(false); }
+
+// Lets this thread allocate while one of its streams is captured.
+class RelaxedCapture {
+ public:
+  RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode_); }
+  ~RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode_); }
+
+ private:
+  cudaStreamCaptureMode mode_ = cudaStreamCaptureModeRelaxed;
+};
+
+// Zeroed memory, now: by a stream that no capture sees.
+int zeroed_now(void** mem, size_t bytes) {
+  if (cudaMalloc(mem, bytes) != cudaSuccess) {
+    cudaGetLastError();
+    return PV_ERR_ALLOC;
+  }
+  cudaStream_t s = nullptr;
+  bool ok = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking) == cudaSuccess;
+  ok = ok && cudaMemsetAsync(*mem, 0, bytes, s) == cudaSuccess && cudaStreamSynchronize(s) == cudaSuccess;
+  if (s) cudaStreamDestroy(s);
+  if (!ok) {
+    cudaGetLastError();
+    cudaFree(*mem);
+    return PV_ERR_CUDA;
+  }
+  return PV_OK;
+}
 std::mutex g_sms_mu;
 int g_sms[64];
 }  // namespace
@@ -64,6 +103,16 @@ int check_out_heads(const pv_heads* h, int64_t rows, int heads, int elem, int de
 }
 
 int Scratch::open(int dev, pv_stream_t stream, ScratchKind kind, size_t bytes) {
+  const size_t need = round_up(kHead + bytes, size_t(1) << 16);
+  cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
+  unsigned long long capture = 0;
+  cudaGraph_t graph = nullptr;
+  // (Refused for the legacy stream beside a capture: the launch will be, too.)
+  if (cudaStreamGetCaptureInfo(reinterpret_cast<cudaStream_t>(stream), &capturing, &capture, &graph, nullptr, nullptr,
+                               nullptr) != cudaSuccess)
+    cudaGetLastError();
+  else if (capturing == cudaStreamCaptureStatusActive)
+    return open_captured(dev, stream, kind, need, capture, graph);
   {
     std::lock_guard<std::mutex> lk(g_seq_mu);
     SeqSpace*& sp = g_seq[std::make_tuple(dev, stream, static_cast<int>(kind))];
@@ -73,7 +122,6 @@ int Scratch::open(int dev, pv_stream_t stream, ScratchKind kind, size_t bytes) {
     sp->mu.lock();
     sp_ = sp;
   }
-  const size_t need = round_up(kHead + bytes, size_t(1) << 16);
   if (sp_->cap >= need) return PV_OK;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (sp_->mem && cudaStreamSynchronize(s) != cudaSuccess) return PV_ERR_CUDA;
@@ -92,6 +140,54 @@ int Scratch::open(int dev, pv_stream_t stream, ScratchKind kind, size_t bytes) {
   }
   sp_->mem = static_cast<unsigned char*>(mem);
   sp_->cap = need;
+  return PV_OK;
+}
+
+int Scratch::open_captured(int dev, pv_stream_t stream, ScratchKind kind, size_t need, unsigned long long capture,
+                           cudaGraph_t graph) {
+  std::lock_guard<std::mutex> lk(g_seq_mu);
+  SeqSpace* idle = nullptr;
+  for (SeqSpace* sp : g_captured) {
+    if (sp->device != dev || sp->kind != kind || sp->cap < need) continue;
+    if (!sp->owned.load()) {
+      if (!idle || sp->cap < idle->cap) idle = sp;
+    } else if (sp->capture == capture && sp->stream == stream) {
+      sp->mu.lock();
+      sp_ = sp;
+      return PV_OK;
+    }
+  }
+  RelaxedCapture relaxed;
+  if (!idle) {
+    idle = new (std::nothrow) SeqSpace();
+    if (!idle) return PV_ERR_ALLOC;
+    void* mem = nullptr;
+    const int st = zeroed_now(&mem, need);
+    if (st != PV_OK) {
+      delete idle;
+      return st;
+    }
+    idle->device = dev;
+    idle->mem = static_cast<unsigned char*>(mem);
+    idle->cap = need;
+    idle->kind = kind;
+    g_captured.push_back(idle);
+  }
+  cudaUserObject_t owner = nullptr;
+  if (cudaUserObjectCreate(&owner, idle, give_back, 1, cudaUserObjectNoDestructorSync) != cudaSuccess) {
+    cudaGetLastError();
+    return PV_ERR_CUDA;
+  }
+  idle->owned.store(true);
+  if (cudaGraphRetainUserObject(graph, owner, 1, cudaGraphUserObjectMove) != cudaSuccess) {
+    cudaGetLastError();
+    cudaUserObjectRelease(owner, 1);  // gives it back
+    return PV_ERR_CUDA;
+  }
+  idle->capture = capture;
+  idle->stream = stream;
+  idle->mu.lock();
+  sp_ = idle;
   return PV_OK;
 }
 
@@ -114,6 +210,15 @@ int release_scratch() {
     delete sp;
   }
   g_seq.clear();
+  // (What a graph owns stays with it.  A captured call enqueues while it owns its space.)
+  g_captured.remove_if([&](SeqSpace* sp) {
+    if (sp->owned.load()) return false;
+    DeviceScope scope(sp->device);
+    if (!scope.ok() || cudaDeviceSynchronize() != cudaSuccess) st = PV_ERR_CUDA;
+    cudaFree(sp->mem);
+    delete sp;
+    return true;
+  });
   return st;
 }
 

@@ -57,10 +57,17 @@ class DeviceScope {
 // enqueues its work, so the launches of two threads on one stream do not mix.
 // A head that is zero at first (counters that each launch leaves as it found
 // them, epochs that only grow) and a body of `bytes`, zero at first too.
+//
+// A call that is being captured into a graph takes one of the capture's own instead (per
+// stream, so that it is not shared by branches): the graph holds its address, and may run
+// at any time beside calls and graphs that came from the same stream.  The graph, and
+// what is instantiated from it, owns that one; the last of them to go gives it back, for
+// later captures to take.
 enum ScratchKind {
   kPlain = 0,  // the body holds nothing between calls
   kTagged = 1  // the body holds (value, epoch) pairs of the recurrence only
 };
+struct SeqSpace;
 class Scratch {
  public:
   static constexpr size_t kHead = 4096;
@@ -70,10 +77,12 @@ class Scratch {
   void* body() const { return static_cast<char*>(head()) + kHead; }
 
  private:
-  struct SeqSpace* sp_ = nullptr;
+  int open_captured(int dev, pv_stream_t stream, ScratchKind kind, size_t need, unsigned long long capture,
+                    cudaGraph_t graph);
+  SeqSpace* sp_ = nullptr;
 };
 
-int release_scratch();  // frees every Scratch (pv_release_workspace)
+int release_scratch();  // frees every Scratch that no graph owns (pv_release_workspace)
 
 // ------------------------------------------------------------ device side
 
