@@ -350,9 +350,23 @@ extern "C" int pv_attention_backward(const pv_attention_params* params, const pv
   a.sides_row = side_rows + 128;
   const size_t sides = static_cast<size_t>(a.sides_row) * (2 * a.H + 3);
   const size_t parts = a.head_parts > 1 ? static_cast<size_t>(2) * a.head_parts * nk * a.Hk * a.D : 0;
-  if ((st = scratch.open(dev, stream, kPlain, sizeof(float) * (sides + parts))) != PV_OK) return st;
+  // Float16: the blocks that look for a frame's largest gradients and values, and what they leave.
+  const bool bf16 = params->dtype == PV_BF16, range = !bf16 && nq && nk;
+  if (range) {
+    int64_t most = 0;
+    for (int f = 0; f < a.frames; ++f)
+      most = std::max<int64_t>(most, static_cast<int64_t>(a.q0[f + 1] - a.q0[f]) * a.H + static_cast<int64_t>(a.k0[f + 1] - a.k0[f]) * a.Hk);
+    a.norm_parts = static_cast<int>(std::min<int64_t>(std::max(1, std::min(256, 4 * sms / a.frames)), (most + 63) / 64));
+  }
+  const size_t ups = range ? static_cast<size_t>(a.frames) * (2 * a.norm_parts + 1) : 0;
+  if ((st = scratch.open(dev, stream, kPlain, sizeof(float) * (sides + parts + ups))) != PV_OK) return st;
   a.sides = static_cast<float*>(scratch.body());
   a.part_o = a.sides + sides;
+  if (range) {
+    a.norms = reinterpret_cast<float2*>(a.part_o + parts);
+    a.up = reinterpret_cast<float*>(a.norms + static_cast<size_t>(a.frames) * a.norm_parts);
+    a.norms_done = static_cast<unsigned int*>(scratch.head()) + kHeadFrames;
+  }
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   AttnMaps m{};
   if (nq && ((st = make_map(&m.q, a.q, params->dtype, a.D, a.H, 1, nq, 128)) != PV_OK ||
@@ -369,7 +383,7 @@ extern "C" int pv_attention_backward(const pv_attention_params* params, const pv
   const int q_tiles = list_tiles(a, a.k0, [&](int f) { return (a.q0[f + 1] - a.q0[f] + 127) / 128; });
   const int k_tiles = list_tiles(b, a.q0, [&](int f) { return (a.k0[f + 1] - a.k0[f] + 127) / 128; });
   if (q_tiles < 0 || k_tiles < 0) return PV_ERR_TOO_LARGE;
-  const bool bf16 = params->dtype == PV_BF16;
+  if (range && (st = attn_backward_up_half(a, cs)) != PV_OK) return st;
   if ((st = (bf16 ? attn_backward_dq_bf16 : attn_backward_dq_half)(a, m, dim3(q_tiles * a.heads), cs)) != PV_OK) return st;
   return (bf16 ? attn_backward_dkv_bf16 : attn_backward_dkv_half)(b, m, dim3(k_tiles * b.heads), cs);
 }

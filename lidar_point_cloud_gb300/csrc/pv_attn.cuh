@@ -24,6 +24,12 @@ struct AttnArgs {
   // delta (negated), [3] positions.
   float* sides;
   long long sides_row;
+  // Backward, float16: per frame, what the scores' gradients are scaled by on top of the
+  // probabilities' factor, found by norm_parts blocks a frame.  Null for bfloat16.
+  float* up;       // [frames]
+  float2* norms;   // [frames, norm_parts]: largest squared norms of rows of dout and v
+  unsigned int* norms_done;  // [frames], zero between launches
+  int norm_parts;
   const float* slopes;
   const int32_t* qpos;
   const int32_t* kpos;
@@ -67,6 +73,7 @@ using Storage = __nv_bfloat16;
 #endif
 int attn_forward_bf16(const AttnArgs& a, const AttnMaps& m, dim3 grid, cudaStream_t s);
 int attn_forward_half(const AttnArgs& a, const AttnMaps& m, dim3 grid, cudaStream_t s);
+int attn_backward_up_half(const AttnArgs& a, cudaStream_t s);  // float16: `up`, first
 int attn_backward_dq_bf16(const AttnArgs& a, const AttnMaps& m, dim3 grid, cudaStream_t s);   // and the sides
 int attn_backward_dq_half(const AttnArgs& a, const AttnMaps& m, dim3 grid, cudaStream_t s);
 int attn_backward_dkv_bf16(const AttnArgs& a, const AttnMaps& m, dim3 grid, cudaStream_t s);  // after it

@@ -41,7 +41,10 @@
 // turns for want of tensor memory.
 //
 // P and dS are held 16 times their values in the storage type: float16 runs out
-// of exponent below 2^-14, where the probabilities of some thousand keys lie.
+// of exponent below 2^-14, where the probabilities of some thousand keys lie.  How large
+// dS is goes by dout, too, which a loss scale moves anywhere, and float16 ends at 65,504:
+// there dS has a frame's own power of two, by |dP - delta| <= 2 |dout| |v| for the largest rows
+// of the frame, so that 2^15 bounds it.  One small kernel reads dout and v for that.
 
 #include "pv_attn.cuh"
 #include "pv_tc.cuh"
@@ -63,7 +66,7 @@ constexpr int kOther = 128;  // rows of a step
 constexpr int kCols = kOther / kGroups;  // columns of a thread
 constexpr int kSides = 3;    // slots of what belongs to the other side's rows
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kUp = 4.0f;  // log2 of the factor on P and dS
+constexpr float kUp = 4.0f;  // log2 of the factor on P (and, in bfloat16, dS)
 constexpr float kDown = 0.0625f;
 
 template <int kBlocks>
@@ -89,8 +92,9 @@ struct Rows {
   float pos[3][4];         // negated
   float slope[4], mul;     // exponent = mul * (score + slope * distance) + off
   float cap_in;            // score = tanh of half this times the raw one, if capped
-  float off[4], delta[4];  // dq: the rows' own (delta negated); dk, dv: the columns', in shared memory
-  float total[4];          // dq: sums of 16 P (dP - delta)
+  float off[4], delta[4];  // dq: the rows' own (delta negated, times `up`); dk, dv: the columns', in shared memory
+  float up;                // float16: dS is `up` times 16 times its value
+  float total[4];          // dq: sums of 16 P (dP - delta), times `up`
   int lo[4], hi[4];        // of the thread's first column, columns seen: lo <= column < hi
 };
 
@@ -183,7 +187,10 @@ __device__ __forceinline__ void gradients(uint32_t at, const float* side, Rows& 
       const int r = row_of(h, x);
       float2 d = make_float2(row.delta[r], row.delta[r]);
       if (kDkv) d = *reinterpret_cast<const float2*>(side + kOther + col_of(x));
-      add2(g[h][x], g[h][x + 1], g[h][x], g[h][x + 1], d.x, d.y);
+      if (std::is_same<T, __half>::value)
+        fma2(g[h][x], g[h][x + 1], g[h][x], g[h][x + 1], row.up, row.up, d.x, d.y);
+      else
+        add2(g[h][x], g[h][x + 1], g[h][x], g[h][x + 1], d.x, d.y);
       // (A hidden place has e = 0, but what stands at it need not be finite.)
       const bool seen0 = !kMask || (col_of(x) >= row.lo[r] && col_of(x) < row.hi[r]);
       const bool seen1 = !kMask || (col_of(x + 1) >= row.lo[r] && col_of(x + 1) < row.hi[r]);
@@ -478,6 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       math_sync();
     }
     Rows row{};
+    row.up = !kBf16 && a.up ? a.up[f] : 1.0f;
     row.mul = (kCap ? a.cap : a.scale) * kLog2e;
     row.cap_in = kCap ? 2.0f * a.scale * kLog2e / a.cap : 0.0f;
     // A place is seen if its column is at least `from` and below `to`.
@@ -497,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!kDkv) {
         if (in) row.off[x] = fmaf(-kLog2e, a.lse[static_cast<long long>(own_head) * a.queries + at], kUp);
-        row.delta[x] = -sm.guess[rx];
+        row.delta[x] = -sm.guess[rx] * row.up;
       }
       if (kSlopes && in) {
         if (!kDkv) row.slope[x] = -a.slopes[own_head] * kLog2e / row.mul;
@@ -564,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool any = steps > 0;
     if (any && ok) ok = warp_wait(&sm.acc_full, 0, given_up);
     tc_after();
-    // dq: the sum of P (dP - delta) is what delta is off by.
+    // dq: the sum of P (dP - delta) is what delta is off by (here `up` times that).
     float total = 0.0f;
     if (!kDkv) {
 #pragma unroll
@@ -578,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (live && wg == 0) {
         float* const side = a.sides + own_head * a.sides_row + a.side0[f] + own;
         side[0] = fmaf(-kLog2e, a.lse[static_cast<long long>(own_head) * a.queries + own_row], kUp);
-        side[a.H * a.sides_row] = -(sm.guess[r] + total);
+        side[a.H * a.sides_row] = -fmaf(sm.guess[r], row.up, total);
         if (own_head == 0)
           for (int c = 0; c < a.axes; ++c)
             side[(2 * a.H + c) * a.sides_row] = static_cast<float>(a.qpos[own_row * a.qpos_stride + c]);
@@ -591,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool parts = kDkv && a.head_parts > 1;
     float* part = parts ? a.part_o + (((static_cast<long long>(head % a.head_parts) * 2 + which) * a.keys + own_row) * a.Hk + own_head) * a.D
                         : nullptr;
-    const float k1 = (kDkv && which ? 1.0f : a.scale) * kDown * bad;
+    const float k1 = (kDkv && which ? 1.0f : a.scale / row.up) * kDown * bad;
     const uint32_t acc = mine + 256 + (kDkv && which ? 64 * kBlocks : 0);
     for (int x = (kDkv ? wg >> 1 : wg) * 16; x < a.Dn; x += kDkv ? 32 : 64) {
       uint32_t c[16], d[16];
@@ -638,6 +646,92 @@ __global__ void __launch_bounds__(kThreads, 1)
   allow_next_grid();
 }
 
+#ifdef PV_ATTN_HALF
+// A frame's `up` (block: frame blockIdx.y, every gridDim.x-th stretch of its rows' heads, as
+// many lanes a head as it has pieces of 16 bytes).  Rows that are not finite do not count: they
+// spoil their own gradients, not the frame's.  Bound by its loads' latency: 33 MB (8,192 tokens
+// of 8 heads of 128) take 15 us from DRAM, a few hundred tokens 6 us; the gradients of
+// 12,289 capped tokens take 24 us more in all with it (1,646 -> 1,670 us with the forward pass).
+constexpr int kNormThreads = 256;
+
+template <int kLanes>
+__global__ void __launch_bounds__(kNormThreads) pv_attn_up_kernel(const __grid_constant__ AttnArgs a) {
+  __shared__ float2 warps[kNormThreads / 32];
+  __shared__ bool last;
+  wait_prior_grid();
+  const int f = blockIdx.y, lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+  constexpr int kRows = kNormThreads / kLanes;
+  auto largest = [&](const View& view, int row0, int rows, int heads) {
+    const int step = gridDim.x * kRows, step_t = step / heads, step_h = step - step_t * heads;
+    const int first = blockIdx.x * kRows + group;
+    long long t = first / heads;
+    int h = first - static_cast<int>(t) * heads;
+    float most = 0.0f;
+    constexpr int kAhead = 4;
+    for (long long i = static_cast<long long>(blockIdx.x) * kRows; i < static_cast<long long>(rows) * heads; i += kAhead * step) {
+      uint4 raw[kAhead] = {};
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x) {
+        if (t < rows && lane * 8 < a.D)
+          raw[x] = *reinterpret_cast<const uint4*>(view.data + (row0 + t) * view.row + h * view.head + lane * 16);
+        t += step_t;
+        h += step_h;
+        if (h >= heads) h -= heads, ++t;
+      }
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x) {
+        float v[8], s = 0.0f;
+        Pack<Storage>::open(raw[x], v);
+#pragma unroll
+        for (int y = 0; y < 8; ++y) s = fmaf(v[y], v[y], s);
+#pragma unroll
+        for (int o = kLanes / 2; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+        if (s < INFINITY) most = fmaxf(most, s);
+      }
+    }
+    return most;
+  };
+  auto block_most = [&](float2 m) {  // for thread 0
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      m.x = fmaxf(m.x, __shfl_xor_sync(0xFFFFFFFFu, m.x, o));
+      m.y = fmaxf(m.y, __shfl_xor_sync(0xFFFFFFFFu, m.y, o));
+    }
+    __syncthreads();
+    if (threadIdx.x % 32 == 0) warps[threadIdx.x / 32] = m;
+    __syncthreads();
+    for (int w = 0; w < kNormThreads / 32; ++w) m = make_float2(fmaxf(m.x, warps[w].x), fmaxf(m.y, warps[w].y));
+    return m;
+  };
+  const float2 mine = block_most(make_float2(largest(a.dout, a.q0[f], a.q0[f + 1] - a.q0[f], a.H),
+                                             largest(a.v, a.k0[f], a.k0[f + 1] - a.k0[f], a.Hk)));
+  float2* const parts = a.norms + static_cast<long long>(f) * gridDim.x;
+  if (threadIdx.x == 0) {
+    parts[blockIdx.x] = mine;
+    __threadfence();
+    last = atomicAdd(a.norms_done + f, 1u) == gridDim.x - 1;
+  }
+  __syncthreads();
+  if (last) {
+    __threadfence();
+    float2 m = make_float2(0.0f, 0.0f);
+    for (int p = threadIdx.x; p < static_cast<int>(gridDim.x); p += kNormThreads) {
+      const float2 x = __ldcg(parts + p);
+      m = make_float2(fmaxf(m.x, x.x), fmaxf(m.y, x.y));
+    }
+    m = block_most(m);
+    if (threadIdx.x == 0) {
+      int e = 11;  // nothing that is not 0: a factor of 1
+      const float bound = 2.0f * sqrtf(m.x) * sqrtf(m.y);
+      if (bound > 0.0f) frexpf(bound, &e);  // bound < 2^e
+      a.up[f] = ldexpf(1.0f, 15 - e - static_cast<int>(kUp));
+      a.norms_done[f] = 0;
+    }
+  }
+  allow_next_grid();
+}
+#endif
+
 // dk and dv of a key head whose query heads were cut into parts: the parts' sum, in order.
 template <typename T>
 __global__ void __launch_bounds__(256) pv_attn_bwd_join_kernel(const __grid_constant__ AttnArgs a) {
@@ -679,6 +773,15 @@ int with_scores(const AttnArgs& a, const AttnMaps& m, dim3 grid, cudaStream_t s)
 }
 
 }  // namespace
+
+#ifdef PV_ATTN_HALF
+int attn_backward_up_half(const AttnArgs& a, cudaStream_t s) {
+  const dim3 grid(a.norm_parts, a.frames);
+  if (a.D > 64) return launch_pdl(pv_attn_up_kernel<16>, grid, kNormThreads, 0, s, a);
+  return a.D > 32 ? launch_pdl(pv_attn_up_kernel<8>, grid, kNormThreads, 0, s, a)
+                  : launch_pdl(pv_attn_up_kernel<4>, grid, kNormThreads, 0, s, a);
+}
+#endif
 
 int PV_ATTN_NAME(attn_backward_dq)(const AttnArgs& a, const AttnMaps& m, dim3 grid, cudaStream_t s) {
   return a.D > 64 ? with_scores<2, false>(a, m, grid, s) : with_scores<1, false>(a, m, grid, s);

@@ -67,10 +67,12 @@ enum ScratchKind {
   kPlain = 0,  // the body holds nothing between calls
   kTagged = 1  // the body holds (value, epoch) pairs of the recurrence only
 };
+constexpr int kHeadFrames = 64;
+static_assert(4 * (kHeadFrames + PV_MAX_FRAMES) <= 4096, "the head holds the frames' counters");
 struct SeqSpace;
 class Scratch {
  public:
-  static constexpr size_t kHead = 4096;
+  static constexpr size_t kHead = 4096;  // words from kHeadFrames on: a counter a frame
   int open(int dev, pv_stream_t stream, ScratchKind kind, size_t bytes);
   ~Scratch();
   void* head() const;
