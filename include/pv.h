@@ -381,8 +381,8 @@ int pv_qk_norm_rope_backward(const pv_rope_params* params, const pv_heads* dout_
  *                 query's softmax sum, or NULL if no backward pass follows.
  * Rows of other frames never reach a result, whatever they hold; hidden keys of
  * the same frame have to be finite.
- * Scores and lse are 32-bit: a probability is off by some 2^-23 times its score
- * and its lse, which shows beside the outputs' type once slopes times distances
+ * Scores and lse are 32-bit: a probability is off by some 2^-22 times its score
+ * and its lse (and, with a cap, by some 2^-17), which shows beside the outputs' type once slopes times distances
  * to the nearest keys reach the thousands.
  */
 typedef struct pv_attention_params {

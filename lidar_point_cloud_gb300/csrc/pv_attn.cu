@@ -65,7 +65,9 @@ AttnArgs args_of(const pv_attention_params* p) {
   a.qpos_stride = p->q_position_stride;
   a.kpos_stride = p->k_position_stride;
   a.scale = p->scale;
-  a.cap = p->cap;
+  // Caps past 1e34 or below 1e-30 cap like these (and their products with the scale and
+  // with log2(e) stay finite).
+  a.cap = p->cap > 0.0f ? std::min(std::max(p->cap, 1e-30f), 1e34f) : 0.0f;
   a.axes = p->slopes ? p->axes : 0;
   a.causal = p->causal != 0;
   a.H = p->q_heads;

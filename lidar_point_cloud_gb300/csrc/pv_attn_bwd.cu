@@ -108,7 +108,7 @@ __device__ __forceinline__ constexpr int col_of(int x) { return (x >> 2) * 8 + (
 // for acc2 too, and what the slope took from 16 P, for the sum of P dP, goes to `rest`
 // as half pairs (a small share, of which the rounding does not show).  One operation
 // after the other over all elements: an element's chain is long, 32 of them hide it.
-template <typename T, bool kDkv, bool kCap, bool kSlopes, bool kMask>
+template <typename T, bool kDkv, int kCap, bool kSlopes, bool kMask>
 __device__ __forceinline__ void probabilities(uint32_t at, const float* side, int axes, const Rows& row, float (*u)[kElems],
                                               uint32_t (*rest)[kElems / 2]) {
   tmem_ld_16x256b_x4(at, reinterpret_cast<uint32_t*>(u[0]));
@@ -121,7 +121,7 @@ __device__ __forceinline__ void probabilities(uint32_t at, const float* side, in
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int x = 0; x < kElems; ++x) {
-        u[h][x] = tanh_half(u[h][x] * row.cap_in);
+        u[h][x] = capped<kCap>(u[h][x] * row.cap_in);
         steep[h][x] = fmaf(-u[h][x], u[h][x], 1.0f);
       }
   }
@@ -170,7 +170,7 @@ __device__ __forceinline__ void probabilities(uint32_t at, const float* side, in
 }
 
 // dP at column `at` to 16 dS there.
-template <typename T, bool kDkv, bool kCap, bool kMask>
+template <typename T, bool kDkv, int kCap, bool kMask>
 __device__ __forceinline__ void gradients(uint32_t at, const float* side, Rows& row, const float (*e)[kElems],
                                           const uint32_t (*rest)[kElems / 2]) {
   float g[2][kElems];
@@ -216,7 +216,7 @@ __device__ __forceinline__ void gradients(uint32_t at, const float* side, Rows& 
 // The cap and the slopes are compile-time choices: code that a launch does not run
 // still costs it instruction fetches (2 x 4096 tokens, 64-element heads, forward and
 // backward: 411 us with both as branches, 375 us so).
-template <typename T, int kBlocks, bool kDkv, bool kCap, bool kSlopes>
+template <typename T, int kBlocks, bool kDkv, int kCap, bool kSlopes>
 __global__ void __launch_bounds__(kThreads, 1)
     pv_attn_bwd_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap mq,
                        const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
@@ -756,7 +756,7 @@ __global__ void __launch_bounds__(256) pv_attn_bwd_join_kernel(const __grid_cons
   allow_next_grid();
 }
 
-template <int kBlocks, bool kDkv, bool kCap, bool kSlopes>
+template <int kBlocks, bool kDkv, int kCap, bool kSlopes>
 int launch_bwd(const AttnArgs& a, const AttnMaps& m, dim3 grid, cudaStream_t s) {
   if (grid.x == 0) return PV_OK;
   auto kernel = pv_attn_bwd_kernel<Storage, kBlocks, kDkv, kCap, kSlopes>;
@@ -767,9 +767,11 @@ int launch_bwd(const AttnArgs& a, const AttnMaps& m, dim3 grid, cudaStream_t s) 
 
 template <int kBlocks, bool kDkv>
 int with_scores(const AttnArgs& a, const AttnMaps& m, dim3 grid, cudaStream_t s) {
+  if (a.cap > kSmallCap)
+    return a.slopes ? launch_bwd<kBlocks, kDkv, kAny, true>(a, m, grid, s) : launch_bwd<kBlocks, kDkv, kAny, false>(a, m, grid, s);
   if (a.cap > 0.0f)
-    return a.slopes ? launch_bwd<kBlocks, kDkv, true, true>(a, m, grid, s) : launch_bwd<kBlocks, kDkv, true, false>(a, m, grid, s);
-  return a.slopes ? launch_bwd<kBlocks, kDkv, false, true>(a, m, grid, s) : launch_bwd<kBlocks, kDkv, false, false>(a, m, grid, s);
+    return a.slopes ? launch_bwd<kBlocks, kDkv, kSmall, true>(a, m, grid, s) : launch_bwd<kBlocks, kDkv, kSmall, false>(a, m, grid, s);
+  return a.slopes ? launch_bwd<kBlocks, kDkv, kNoCap, true>(a, m, grid, s) : launch_bwd<kBlocks, kDkv, kNoCap, false>(a, m, grid, s);
 }
 
 }  // namespace

@@ -75,7 +75,7 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return Pack<T>::two(a, b);
 }
 
-template <typename T, int kBlocks, bool kCap, bool kSlopes>
+template <typename T, int kBlocks, int kCap, bool kSlopes>
 __global__ void __launch_bounds__(kThreads, 1)
     pv_attn_fwd_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap mq,
                        const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_wait_ld<64>(reinterpret_cast<uint32_t*>(u[1]));
         if (kCap) {
 #pragma unroll
-          for (int x = 0; x < 128; ++x) u[x >> 6][x & 63] = tanh_half(u[x >> 6][x & 63] * cap_in);
+          for (int x = 0; x < 128; ++x) u[x >> 6][x & 63] = capped<kCap>(u[x >> 6][x & 63] * cap_in);
         }
         {
           if (!(ok = warp_wait(&sm.pos_full[n % kPosSlots], (n / kPosSlots) & 1, given_up))) break;
@@ -515,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_wait_ld<kRows>(ur);
         if (kCap) {
 #pragma unroll
-          for (int x = 0; x < kRows; ++x) u[x] = tanh_half(u[x] * cap_in);
+          for (int x = 0; x < kRows; ++x) u[x] = capped<kCap>(u[x] * cap_in);
         }
         if ((j + 1) * kRows > clear) {
           const int seen = lim - j * kRows;
@@ -689,7 +689,7 @@ int launch_join(const AttnArgs& a, cudaStream_t s) {
   return launch_pdl(pv_attn_join_kernel<Storage, kLanes>, dim3(static_cast<unsigned>((threads + 127) / 128)), 128, 0, s, a);
 }
 
-template <int kBlocks, bool kCap, bool kSlopes>
+template <int kBlocks, int kCap, bool kSlopes>
 int launch_fwd(const AttnArgs& a, const AttnMaps& m, dim3 grid, cudaStream_t s) {
   auto kernel = pv_attn_fwd_kernel<Storage, kBlocks, kCap, kSlopes>;
   const int smem = static_cast<int>(sizeof(Smem<kBlocks>)) + 1024;
@@ -699,8 +699,9 @@ int launch_fwd(const AttnArgs& a, const AttnMaps& m, dim3 grid, cudaStream_t s) 
 
 template <int kBlocks>
 int with_scores(const AttnArgs& a, const AttnMaps& m, dim3 grid, cudaStream_t s) {
-  if (a.cap > 0.0f) return a.slopes ? launch_fwd<kBlocks, true, true>(a, m, grid, s) : launch_fwd<kBlocks, true, false>(a, m, grid, s);
-  return a.slopes ? launch_fwd<kBlocks, false, true>(a, m, grid, s) : launch_fwd<kBlocks, false, false>(a, m, grid, s);
+  if (a.cap > kSmallCap) return a.slopes ? launch_fwd<kBlocks, kAny, true>(a, m, grid, s) : launch_fwd<kBlocks, kAny, false>(a, m, grid, s);
+  if (a.cap > 0.0f) return a.slopes ? launch_fwd<kBlocks, kSmall, true>(a, m, grid, s) : launch_fwd<kBlocks, kSmall, false>(a, m, grid, s);
+  return a.slopes ? launch_fwd<kBlocks, kNoCap, true>(a, m, grid, s) : launch_fwd<kBlocks, kNoCap, false>(a, m, grid, s);
 }
 
 }  // namespace
