@@ -73,8 +73,9 @@ typedef enum pv_status {
   PV_ERR_INTERNAL = -7,    /* device: a consistency check failed (a point index read
                               from the pillar table was out of range); the workspace is
                               fully reset by the next call on the same stream */
-  PV_ERR_TOO_LARGE = -8    /* pv_voxelize_static only: more points or a larger
-                              max_points than its fixed scratch holds */
+  PV_ERR_TOO_LARGE = -8    /* pv_voxelize_static: more points or a larger max_points
+                              than its fixed scratch holds; operators on voxel tokens:
+                              more rows, or blocks of work, than their indexes hold */
 } pv_status;
 
 /* Largest max_points accepted. */
@@ -370,7 +371,8 @@ int pv_qk_norm_rope_backward(const pv_rope_params* params, const pv_heads* dout_
  * a query with no visible key gives 0 (its lse is -inf, its gradients 0).
  * Query head h reads key head h / (q_heads / k_heads).
  *   frames        1 .. PV_MAX_FRAMES; q_offsets and k_offsets HOST [frames + 1]:
- *                 0, then never decreasing (empty frames allowed), below 2^31.
+ *                 0, then never decreasing (empty frames allowed), up to
+ *                 PV_ATTENTION_MAX_ROWS (more: PV_ERR_TOO_LARGE).
  *   head_dim      a multiple of 8, 8 .. 128; dtype PV_BF16 or PV_F16.
  *   scale, cap    finite, scale > 0, cap >= 0 (0: no cap).
  *   slopes        device float32 [q_heads] or NULL; then q_positions and
@@ -385,6 +387,7 @@ int pv_qk_norm_rope_backward(const pv_rope_params* params, const pv_heads* dout_
  * and its lse (and, with a cap, by some 2^-17), which shows beside the outputs' type once slopes times distances
  * to the nearest keys reach the thousands.
  */
+#define PV_ATTENTION_MAX_ROWS ((INT64_C(1) << 31) - 4096)
 typedef struct pv_attention_params {
   int frames;
   const int64_t* q_offsets;
@@ -418,7 +421,7 @@ int pv_attention_backward(const pv_attention_params* params, const pv_heads* dou
  * its first if `reverse`.
  *   x, gate, out_h  device [rows, channels] of dtype, row strides in elements
  *                 (x_stride, gate_stride, h_stride >= channels); element aligned.
- *   frames, offsets   as above (HOST).  channels 1 .. 2^20.
+ *   frames, offsets   as above (HOST), below 2^31.  channels 1 .. 2^20.
  *   h0            device float32 [frames, channels], or NULL for zeros.
  *   out_last      device float32 [frames, channels]: the state after each
  *                 frame's last step (h0 for an empty frame), or NULL.

@@ -31,6 +31,8 @@ int check_params(const pv_attention_params* p, int* dev, const void* some) {
   int st;
   if ((st = check_offsets(p->q_offsets, p->frames)) != PV_OK || (st = check_offsets(p->k_offsets, p->frames)) != PV_OK)
     return st;
+  if (p->q_offsets[p->frames] > PV_ATTENTION_MAX_ROWS || p->k_offsets[p->frames] > PV_ATTENTION_MAX_ROWS)
+    return PV_ERR_TOO_LARGE;
   if (p->q_heads < 1 || p->k_heads < 1 || p->q_heads > 4096 || p->q_heads % p->k_heads) return PV_ERR_INVALID;
   if (p->head_dim < 8 || p->head_dim > 128 || p->head_dim % 8) return PV_ERR_INVALID;
   if (!(p->scale > 0.0f) || !std::isfinite(p->scale) || !(p->cap >= 0.0f) || !std::isfinite(p->cap)) return PV_ERR_INVALID;

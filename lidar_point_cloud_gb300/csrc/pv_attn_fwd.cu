@@ -90,14 +90,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tile = blockIdx.x / a.heads, place = frame_of(a.tile0, a.frames, tile), f = a.order[place];
   const int nq = a.q0[f + 1] - a.q0[f], nk = a.k0[f + 1] - a.k0[f];
   const int pack = 1 << a.pack_log2;
-  const int mblocks = (((nq << a.pack_log2) + 2 * kRows - 1) / (2 * kRows));
+  const int per_block = 2 * kRows >> a.pack_log2;  // queries of a block
+  const int mblocks = (nq + per_block - 1) / per_block;
   const int local = tile - a.tile0[place];
   // Later rows see more keys under a causal mask: they go first.
   const int mb = mblocks - 1 - local % mblocks, split = local / mblocks;
   const int hb = blockIdx.x - tile * a.heads;  // block of `pack` heads
   const int kh = (hb << a.pack_log2) / a.G;
   // Keys that query i sees: all below this.
-  auto limit = [&](int i) { return a.causal ? max(min(max(i + nk - nq + 1, a.prefix[f]), nk), 0) : nk; };
+  auto limit = [&](int i) { return a.causal ? max(min(max(i - nq + nk + 1, a.prefix[f]), nk), 0) : nk; };
   const int js = split * a.chunk;
   int first[2], last_j[2];
 #pragma unroll

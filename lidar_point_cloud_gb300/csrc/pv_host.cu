@@ -856,7 +856,7 @@ const char* pv_status_string(int status) {
     case PV_ERR_CAPACITY: return "PV_ERR_CAPACITY: pillar table full";
     case PV_ERR_TIMEOUT: return "PV_ERR_TIMEOUT: a bounded device wait gave up";
     case PV_ERR_INTERNAL: return "PV_ERR_INTERNAL: device consistency check failed";
-    case PV_ERR_TOO_LARGE: return "PV_ERR_TOO_LARGE: beyond the limits of the allocation-free entry point";
+    case PV_ERR_TOO_LARGE: return "PV_ERR_TOO_LARGE: beyond the limits of this call";
     default: return status >= 0 ? "pillar count" : "unknown status";
   }
 }

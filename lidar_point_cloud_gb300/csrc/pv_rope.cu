@@ -53,6 +53,11 @@ struct RopeArgs {
   float* dwk;
 };
 
+// (Rows come close to 2^31: the sum takes 64 bits.)
+__host__ __device__ __forceinline__ int tiles_of(const RopeArgs& a) {
+  return static_cast<int>((static_cast<long long>(a.rows) + a.tile - 1) / a.tile);
+}
+
 // Two pairs turned, two operations an instruction where the signs allow.
 __device__ __forceinline__ void turn(float* x, float* y, float c0, float c1, float s0, float s1) {
   float a0, a1, b0, b1;
@@ -194,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 2) pv_rope_backward_kernel(const Rop
   const bool on = sub * V < half;
   const float inv = 1.0f / static_cast<float>(a.D);
   wait_prior_grid();
-  const int tiles = (a.rows + a.tile - 1) / a.tile;
+  const int tiles = tiles_of(a);
   float* sums = table;
   for (int side = 0; side < 2; ++side) {
     const View& in = side ? a.k : a.q;
@@ -429,7 +434,7 @@ extern "C" int pv_qk_norm_rope(const pv_rope_params* params, const pv_heads* q, 
   a.oq = view_of(out_q, elem);
   a.ok = view_of(out_k, elem);
   a.tile = tile_tokens(a, kPerSm * sms);
-  const int blocks = (a.rows + a.tile - 1) / a.tile;
+  const int blocks = tiles_of(a);
   switch (params->dtype) {
     case PV_F32: return launch(pv_rope_kernel<float>, blocks, a, stream);
     case PV_BF16: return launch(pv_rope_kernel<__nv_bfloat16>, blocks, a, stream);
@@ -467,8 +472,7 @@ extern "C" int pv_qk_norm_rope_backward(const pv_rope_params* params, const pv_h
   a.dwk = dk_weight;
   const int most = std::min(kMaxBlocks, kPerSmBack * sms);
   a.tile = tile_tokens(a, most);
-  const int tiles = (a.rows + a.tile - 1) / a.tile;
-  const int blocks = std::max(1, std::min(most, tiles));
+  const int blocks = std::max(1, std::min(most, tiles_of(a)));
   Scratch scratch;
   if ((st = scratch.open(dev, stream, kPlain, sizeof(float) * 2 * a.D * static_cast<size_t>(blocks))) != PV_OK)
     return st;
