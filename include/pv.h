@@ -418,7 +418,8 @@ int pv_attention_backward(const pv_attention_params* params, const pv_heads* dou
  * Gated linear recurrence along each frame, every channel by itself:
  *   z = 1 / (1 + exp(-gate)),  h[t] = (1 - z[t]) h[t-1] + z[t] x[t],
  * from h0[b], read from the frame's first row to its last, or from its last to
- * its first if `reverse`.
+ * its first if `reverse`.  What is not finite goes through this as it stands: an
+ * infinite state stays infinite until z is 1 in 32 bits.
  *   x, gate, out_h  device [rows, channels] of dtype, row strides in elements
  *                 (x_stride, gate_stride, h_stride >= channels); element aligned.
  *   frames, offsets   as above (HOST), below 2^31.  channels 1 .. 2^20.

@@ -135,13 +135,30 @@ __device__ __forceinline__ void vmul(float* r, const float* a, const float* b) {
     r[0] = a[0] * b[0];
 }
 
+// r = a - b.
+template <int V>
+__device__ __forceinline__ void vsub(float* r, const float* a, const float* b) {
+  const float minus[2] = {-1.0f, -1.0f};
+  vfma<V>(r, b, minus, a);
+}
+// a = 1 - z.
+template <int V>
+__device__ __forceinline__ void keep(float* a, const float* z) {
+  const float one[2] = {1.0f, 1.0f};
+  vsub<V>(a, one, z);
+}
+
+// The product of two factors that states are kept by, which is 0 only if one of them is:
+// an infinite state stays infinite however many steps a map spans.
+constexpr float kLeast = 1.401298464e-45f;  // the least number above 0
+__device__ __forceinline__ float kept(float a, float b) { return fmaxf(a * b, fminf(fminf(a, b), kLeast)); }
+
 template <typename T, int V>
 struct Lane;  // V neighbouring channels of one row
 template <>
 struct Lane<float, 1> {
   using Raw = float;
   static __device__ __forceinline__ Raw closed() { return __uint_as_float(0xFF800000u); }  // a gate of -inf
-  static __device__ __forceinline__ Raw minus(Raw r) { return -r; }
   static __device__ __forceinline__ void open(Raw r, float* f) { f[0] = r; }
   static __device__ __forceinline__ Raw close(const float* f) { return f[0]; }
 };
@@ -149,7 +166,6 @@ template <typename T>
 struct Lane<T, 1> {
   using Raw = T;
   static __device__ __forceinline__ Raw closed() { return Pack<T>::one(__uint_as_float(0xFF800000u)); }
-  static __device__ __forceinline__ Raw minus(Raw r) { return -r; }
   static __device__ __forceinline__ void open(Raw r, float* f) { f[0] = Pack<T>::to(r); }
   static __device__ __forceinline__ Raw close(const float* f) { return Pack<T>::one(f[0]); }
 };
@@ -157,7 +173,6 @@ template <>
 struct Lane<__nv_bfloat16, 2> {
   using Raw = uint32_t;
   static __device__ __forceinline__ Raw closed() { return 0xFF80FF80u; }
-  static __device__ __forceinline__ Raw minus(Raw r) { return r ^ 0x80008000u; }
   static __device__ __forceinline__ void open(Raw r, float* f) {
     f[0] = __uint_as_float(r << 16);
     f[1] = __uint_as_float(r & 0xFFFF0000u);
@@ -168,7 +183,6 @@ template <>
 struct Lane<__half, 2> {
   using Raw = uint32_t;
   static __device__ __forceinline__ Raw closed() { return 0xFC00FC00u; }
-  static __device__ __forceinline__ Raw minus(Raw r) { return r ^ 0x80008000u; }
   static __device__ __forceinline__ void open(Raw r, float* f) {
     const float2 d = __half22float2(*reinterpret_cast<const __half2*>(&r));
     f[0] = d.x;
@@ -352,35 +366,44 @@ __global__ void __launch_bounds__(kThreads, 2) pv_scan_kernel(const __grid_const
     stage_wait();
     const Raw* in = words + at * (kIn * kSteps * kThreads);
     auto word = [&](int tensor, int j, float* f) { L::open(in[(tensor * kSteps + j) * kThreads], f); };
-    auto minus_x = [&](int j, float* f) { L::open(L::minus(in[j * kThreads]), f); };
-    // The gates negated, and the inputs: with a step's state as (-z) s + s, then
-    // (-z) (-x) on top, every operation is a multiply-add of what is at hand (two channels
-    // an instruction), exact at both ends of z.
-    float nz[kSteps][V];
+    // A step is (1 - z) s + z x as it stands (s + z (x - s) would make no number of an
+    // infinite s, as would s - z s), two channels an instruction.
+    float z[kSteps][V];
 #pragma unroll
     for (int j = 0; j < kSteps; ++j) {
-      word(1, j, nz[j]);
+      word(1, j, z[j]);
 #pragma unroll
-      for (int v = 0; v < V; ++v) nz[j][v] = -sigmoid<T>(nz[j][v]);
+      for (int v = 0; v < V; ++v) z[j][v] = sigmoid<T>(z[j][v]);
     }
     float A[V], B[V], Cb[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = 0.0f, Cb[v] = 0.0f;
 #pragma unroll
     for (int j = 0; j < kSteps; ++j) {
-      float x[V];
-      minus_x(j, x);
-      vfma<V>(A, nz[j], A, A);
-      vfma<V>(B, nz[j], B, B);
-      vfma<V>(B, nz[j], x, B);
+      float x[V], k[V];
+      word(0, j, x);
+      keep<V>(k, z[j]);
+      vmul<V>(x, z[j], x);
+      vmul<V>(A, k, A);
+      vfma<V>(B, k, B, x);
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if (A[v] == 0.0f) {  // as in `kept`, all at once: seldom
+        float most = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j) most = fmaxf(most, z[j][v]);
+        if (most < 1.0f) A[v] = kLeast;
+      }
     }
     if (kBack) {
 #pragma unroll
       for (int j = kSteps - 1; j >= 0; --j) {
-        float d[V];
+        float d[V], k[V];
         word(2, j, d);
+        keep<V>(k, z[j]);
         vadd<V>(d, d, Cb);
-        vfma<V>(Cb, nz[j], d, d);
+        vmul<V>(Cb, k, d);
       }
     }
     float* const mine = all + seg * kRows * width + cl * V;
@@ -404,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 2) pv_scan_kernel(const __grid_const
           p[0] = TA;
           p[width] = TB;
           TB = fmaf(sa, TB, sb);
-          TA *= sa;
+          TA = kept(sa, TA);
         }
       } else {
         // Forward along the tile from the state that the forward pass left, and
@@ -423,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 2) pv_scan_kernel(const __grid_const
           pe[0] = TA;
           pe[2 * width] = TB;
           TB = fmaf(sa, TB, sc);
-          TA *= sa;
+          TA = kept(sa, TA);
         }
       }
     }
@@ -447,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 2) pv_scan_kernel(const __grid_const
 #pragma unroll 5
       for (int j = 0; j < ahead; ++j) {
         GB = fmaf(fetch[j][0][threadIdx.x], GB, fetch[j][1][threadIdx.x]);
-        GA *= fetch[j][0][threadIdx.x];
+        GA = kept(fetch[j][0][threadIdx.x], GA);
       }
       if (group) start = take(base_word, base_at, epoch);
       const float s = fmaf(GA, start, GB), after = fmaf(TA, s, TB);
@@ -469,10 +492,11 @@ __global__ void __launch_bounds__(kThreads, 2) pv_scan_kernel(const __grid_const
       auto run = [&](auto whole) {
 #pragma unroll
         for (int j = 0; j < kSteps; ++j, po += so) {
-          float x[V];
-          minus_x(j, x);
-          vfma<V>(s, nz[j], s, s);
-          vfma<V>(s, nz[j], x, s);
+          float x[V], k[V];
+          word(0, j, x);
+          keep<V>(k, z[j]);
+          vmul<V>(x, z[j], x);
+          vfma<V>(s, k, s, x);
           if (decltype(whole)::value || j < now.n) __stcs(po, L::close(s));
         }
       };
@@ -481,16 +505,17 @@ __global__ void __launch_bounds__(kThreads, 2) pv_scan_kernel(const __grid_const
       else
         run(std::false_type{});
     } else {
-      float diff[kSteps][V];  // h[t-1] - x[t]
+      float diff[kSteps][V];  // x[t] - h[t-1]
 #pragma unroll
       for (int v = 0; v < V; ++v) s[v] = mine[width + v];
 #pragma unroll
       for (int j = 0; j < kSteps; ++j) {
-        float x[V];
-        minus_x(j, x);
-        vadd<V>(diff[j], s, x);
-        vfma<V>(s, nz[j], s, s);
-        vfma<V>(s, nz[j], x, s);
+        float x[V], k[V];
+        word(0, j, x);
+        vsub<V>(diff[j], x, s);
+        keep<V>(k, z[j]);
+        vmul<V>(x, z[j], x);
+        vfma<V>(s, k, s, x);
       }
 #pragma unroll
       for (int v = 0; v < V; ++v) s[v] = fmaf(mine[v], carry[cl * V + v], mine[2 * width + v]);
@@ -500,15 +525,16 @@ __global__ void __launch_bounds__(kThreads, 2) pv_scan_kernel(const __grid_const
       auto run = [&](auto whole) {
 #pragma unroll
         for (int j = kSteps - 1; j >= 0; --j, po -= so, pq -= sq) {
-          float d[V], gx[V], gg[V];
+          float d[V], k[V], gx[V], gg[V];
           word(2, j, d);
           vadd<V>(d, d, s);
-          vmul<V>(gx, d, nz[j]);  // -e z
-          vfma<V>(s, nz[j], d, d);
-          vmul<V>(gg, nz[j], diff[j]);
+          vmul<V>(gx, d, z[j]);  // e z
+          keep<V>(k, z[j]);
+          vmul<V>(s, k, d);
+          vmul<V>(gg, z[j], diff[j]);
           vmul<V>(gg, gg, s);  // e z (1 - z) (x - h)
           if (decltype(whole)::value || j < now.n) {
-            __stcs(po, L::minus(L::close(gx)));
+            __stcs(po, L::close(gx));
             __stcs(pq, L::close(gg));
           }
         }
