@@ -444,8 +444,8 @@ typedef struct pv_scan_params {
 int pv_gated_scan(const pv_scan_params* params, const float* h0, void* out_h, int64_t h_stride, float* out_last,
                   float* out_states, pv_stream_t stream);
 
-/* Rows of out_states for these offsets, channels, dtype (from params; strides
- * matter too, the data pointers do not), or a negative status. */
+/* Rows of out_states for these offsets, channels, dtype (from params; strides and
+ * data pointers do not matter), or a negative status. */
 int64_t pv_gated_scan_states(const pv_scan_params* params);
 
 /* Its backward pass: from the gradients of h ([rows, channels], stride

@@ -561,14 +561,20 @@ struct Shape {
 // Two 16-bit channels share a 32-bit word where every row begins on one.
 bool paired(const void* p, int64_t stride) { return stride % 2 == 0 && aligned(p, 4); }
 
+// How the steps are cut into tiles goes by the offsets, the number of channels and the type
+// alone, since the states that a forward call leaves are handed to a backward call whose
+// tensors may lie otherwise: an even number of 16-bit channels has the tiles of lanes of
+// two channels, also where alignment leaves a lane only one.
 int shape_of(const pv_scan_params* p, bool pairs, Shape* s) {
   s->elem = dtype_size(p->dtype);
-  s->vec = s->elem == 2 && pairs ? 2 : 1;
-  const int64_t words = (p->channels + s->vec - 1) / s->vec;
+  const int per_lane = s->elem == 2 && p->channels % 2 == 0 ? 2 : 1;
+  s->vec = pairs ? per_lane : 1;
+  const int64_t words = (p->channels + per_lane - 1) / per_lane;
   s->lanes_log2 = 0;
   while ((1 << s->lanes_log2) < 32 && (int64_t(1) << s->lanes_log2) < words) ++s->lanes_log2;
   s->steps = (kThreads >> s->lanes_log2) * kSteps;
-  s->slabs = static_cast<int>((words + (1 << s->lanes_log2) - 1) >> s->lanes_log2);
+  const int64_t width = int64_t(s->vec) << s->lanes_log2;
+  s->slabs = static_cast<int>((p->channels + width - 1) / width);
   s->tiles = 0;
   for (int b = 0; b < p->frames; ++b) {
     const int64_t t = (p->offsets[b + 1] - p->offsets[b] + s->steps - 1) / s->steps;
@@ -679,11 +685,9 @@ int start(const pv_scan_params* p, const Shape& sh, ScanArgs& a, int dev, pv_str
 extern "C" int64_t pv_gated_scan_states(const pv_scan_params* params) {
   int st = check_params(params);
   if (st != PV_OK) return st;
-  // The shortest tile that any of the calls on these sizes takes: one channel
-  // a lane.  (Whether two channels share a lane goes by alignment.)
-  Shape one, two;
-  if ((st = shape_of(params, false, &one)) != PV_OK || (st = shape_of(params, true, &two)) != PV_OK) return st;
-  return std::max(one.tiles, two.tiles);
+  Shape sh;
+  if ((st = shape_of(params, true, &sh)) != PV_OK) return st;
+  return sh.tiles;
 }
 
 extern "C" int pv_gated_scan(const pv_scan_params* params, const float* h0, void* out_h, int64_t h_stride,
@@ -702,11 +706,8 @@ extern "C" int pv_gated_scan(const pv_scan_params* params, const float* h0, void
   if ((h0 && !on_device(h0, 4, dev)) || (out_last && !on_device(out_last, 4, dev)) ||
       (rows && out_states && !on_device(out_states, 4, dev)))
     return PV_ERR_INVALID;
-  // The states' layout is part of what is handed to the backward call, so with
-  // states the tiles go by the shape alone: channels in pairs if C is even.
-  const bool pairs = C % 2 == 0 && paired(params->x, params->x_stride) && paired(params->gate, params->gate_stride) &&
+  const bool pairs = paired(params->x, params->x_stride) && paired(params->gate, params->gate_stride) &&
                      paired(out_h, h_stride);
-  if (out_states && C % 2 == 0 && elem == 2 && !pairs) return PV_ERR_INVALID;
   Shape sh;
   if ((st = shape_of(params, pairs, &sh)) != PV_OK) return st;
   ScanArgs a{};
@@ -734,9 +735,8 @@ extern "C" int pv_gated_scan_backward(const pv_scan_params* params, const void* 
                params->x_stride < C || params->gate_stride < C || dh_stride < C || dx_stride < C || dgate_stride < C))
     return PV_ERR_INVALID;
   if ((dlast && !on_device(dlast, 4, dev)) || (dh0 && !on_device(dh0, 4, dev))) return PV_ERR_INVALID;
-  const bool pairs = C % 2 == 0 && paired(params->x, params->x_stride) && paired(params->gate, params->gate_stride) &&
+  const bool pairs = paired(params->x, params->x_stride) && paired(params->gate, params->gate_stride) &&
                      paired(dh, dh_stride) && paired(dx, dx_stride) && paired(dgate, dgate_stride);
-  if (C % 2 == 0 && elem == 2 && !pairs) return PV_ERR_INVALID;
   Shape sh;
   if ((st = shape_of(params, pairs, &sh)) != PV_OK) return st;
   ScanArgs a{};
