@@ -421,7 +421,8 @@ int pv_attention_backward(const pv_attention_params* params, const pv_heads* dou
  * its first if `reverse`.  What is not finite goes through this as it stands: an
  * infinite state stays infinite until z is 1 in 32 bits.
  *   x, gate, out_h  device [rows, channels] of dtype, row strides in elements
- *                 (x_stride, gate_stride, h_stride >= channels); element aligned.
+ *                 (x_stride, gate_stride, h_stride >= channels; 0 for one row of x
+ *                 or gate seen as many); element aligned.
  *   frames, offsets   as above (HOST), below 2^31.  channels 1 .. 2^20.
  *   h0            device float32 [frames, channels], or NULL for zeros.
  *   out_last      device float32 [frames, channels]: the state after each
@@ -450,7 +451,7 @@ int64_t pv_gated_scan_states(const pv_scan_params* params);
 
 /* Its backward pass: from the gradients of h ([rows, channels], stride
  * dh_stride) and of the last states (float32 [frames, channels], NULL: zeros)
- * the gradients of x and gate (strides dx_stride, dgate_stride) and of h0
+ * the gradients of x and gate (strides dx_stride, dgate_stride) and of h0; dh_stride may be 0
  * (float32 [frames, channels] or NULL).  `states` is the forward call's. */
 int pv_gated_scan_backward(const pv_scan_params* params, const void* dh, int64_t dh_stride, const float* dlast,
                            const float* states, void* dx, int64_t dx_stride, void* dgate, int64_t dgate_stride,

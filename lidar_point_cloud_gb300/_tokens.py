@@ -63,6 +63,12 @@ def _heads(t, name: str, like=None, heads: Optional[int] = None, apart: bool = F
     return h
 
 
+def _gradient(t):
+    """A gradient with a dense last dimension: that of a plain sum is one element
+    expanded over everything, and is written out."""
+    return t.contiguous() if t.dim() and t.numel() and t.stride(-1) == 0 else t
+
+
 def _dense(like):
     torch = _torch()
     if like.is_contiguous():
@@ -183,6 +189,7 @@ def qk_norm_rope_backward(dout_q, dout_k, q, k, q_weight, k_weight, positions, i
         with _on(stream, q):
             return qk_norm_rope_backward(dout_q, dout_k, q, k, q_weight, k_weight, positions, inv_freq, eps)
     torch = _torch()
+    dout_q, dout_k = _gradient(dout_q), _gradient(dout_k)
     hq, hk = _heads(q, "q"), _heads(k, "k", q, 1)
     p = _rope_params(q, k, q_weight, k_weight, positions, inv_freq, eps)
     (dq, hdq), (dk, hdk) = _new(q), _new(k)
@@ -356,6 +363,7 @@ def gated_scan_backward(dh, dlast, x, gate, states, offsets, reverse: bool = Fal
     C, dev = x.shape[1], x.get_device()
     state = (p.frames, C)
     lib = load()
+    dh = _gradient(dh)
     dhp, dhs = _rows(dh, "dh", x)
     dx, dgate = _dense(x), _dense(x)
     torch = _torch()

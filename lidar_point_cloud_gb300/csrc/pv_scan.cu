@@ -591,6 +591,9 @@ int check_params(const pv_scan_params* p) {
   return PV_OK;
 }
 
+// A row stride of 0 is one row seen as many, for what is read.
+bool readable(int64_t stride, int64_t channels) { return stride >= channels || stride == 0; }
+
 bool on_device(const void* p, size_t align, int dev) { return p && aligned(p, align) && device_of(p) == dev; }
 
 template <typename T, int V, bool kBack>
@@ -701,7 +704,7 @@ extern "C" int pv_gated_scan(const pv_scan_params* params, const float* h0, void
   const int dev = device_of(any);
   if (dev < 0) return PV_ERR_INVALID;
   if (rows && (!on_device(params->x, elem, dev) || !on_device(params->gate, elem, dev) ||
-               !on_device(out_h, elem, dev) || params->x_stride < C || params->gate_stride < C || h_stride < C))
+               !on_device(out_h, elem, dev) || !readable(params->x_stride, C) || !readable(params->gate_stride, C) || h_stride < C))
     return PV_ERR_INVALID;
   if ((h0 && !on_device(h0, 4, dev)) || (out_last && !on_device(out_last, 4, dev)) ||
       (rows && out_states && !on_device(out_states, 4, dev)))
@@ -732,7 +735,8 @@ extern "C" int pv_gated_scan_backward(const pv_scan_params* params, const void* 
   if (dev < 0) return PV_ERR_INVALID;
   if (rows && (!on_device(params->x, elem, dev) || !on_device(params->gate, elem, dev) || !on_device(dh, elem, dev) ||
                !on_device(dx, elem, dev) || !on_device(dgate, elem, dev) || !on_device(states, 4, dev) ||
-               params->x_stride < C || params->gate_stride < C || dh_stride < C || dx_stride < C || dgate_stride < C))
+               !readable(params->x_stride, C) || !readable(params->gate_stride, C) || !readable(dh_stride, C) ||
+               dx_stride < C || dgate_stride < C))
     return PV_ERR_INVALID;
   if ((dlast && !on_device(dlast, 4, dev)) || (dh0 && !on_device(dh0, 4, dev))) return PV_ERR_INVALID;
   const bool pairs = paired(params->x, params->x_stride) && paired(params->gate, params->gate_stride) &&
