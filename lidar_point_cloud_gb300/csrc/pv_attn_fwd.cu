@@ -75,6 +75,9 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return Pack<T>::two(a, b);
 }
 
+// The logarithm of a row's sum (-inf if it sees nothing, no number if its sum is none).
+__device__ __forceinline__ float log_sum(float top, float sum) { return sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2; }
+
 template <typename T, int kBlocks, int kCap, bool kSlopes>
 __global__ void __launch_bounds__(kThreads, 1)
     pv_attn_fwd_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap mq,
@@ -578,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (any && ok) ok = warp_wait(&sm.o_full[t], 0, given_up);
     tc_after();
     const bool parts = a.part_o != nullptr;
-    float by = parts ? 1.0f : row_sum > 0.0f ? 1.0f / row_sum : 0.0f;
+    float by = parts ? 1.0f : row_sum == 0.0f ? 0.0f : 1.0f / row_sum;
     if (!ok || *given_up) by = __int_as_float(0x7FFFFFFF);  // a wait ran out: nothing here is an answer
     char* out = a.o.data + qrow * a.o.row + h * a.o.head;
     float* part = parts ? a.part_o + ((static_cast<long long>(split) * a.queries + qrow) * a.H + h) * a.D : nullptr;
@@ -608,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (parts)
         a.part_ml[(static_cast<long long>(split) * a.queries + qrow) * a.H + h] = make_float2(row_top, row_sum);
       else if (a.lse)
-        a.lse[at] = row_sum > 0.0f ? (row_top + log2f(row_sum)) * kLn2 : -INFINITY;
+        a.lse[at] = log_sum(row_top, row_sum);
     }
     tc_before();
   }
@@ -675,12 +678,12 @@ __global__ void __launch_bounds__(128) pv_attn_join_kernel(const __grid_constant
       }
     }
   }
-  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
   if (on)
     *reinterpret_cast<uint2*>(a.o.data + row * a.o.row + h * a.o.head + lane * 8) =
         make_uint2(pack2<T>(v[0] * inv, v[1] * inv), pack2<T>(v[2] * inv, v[3] * inv));
   if (any && a.lse && lane == 0)
-    a.lse[static_cast<long long>(h) * a.queries + row] = sum > 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+    a.lse[static_cast<long long>(h) * a.queries + row] = log_sum(top, sum);
   allow_next_grid();
 }
 
