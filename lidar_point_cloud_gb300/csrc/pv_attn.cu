@@ -246,7 +246,7 @@ int pvs::make_map(CUtensorMap* map, const View& v, int dtype, int D, int heads, 
 }
 
 extern "C" int pv_attention(const pv_attention_params* params, const pv_heads* q, const pv_heads* k, const pv_heads* v,
-                            const pv_heads* out, float* lse, pv_stream_t stream) {
+                            const pv_heads* out, float* lse, pv_stream_t stream) try {
   if (!params || !params->q_offsets || !out || !q) return PV_ERR_INVALID;
   int dev = 0, st;
   if ((st = check_offsets(params->q_offsets, params->frames)) != PV_OK) return st;
@@ -300,11 +300,13 @@ extern "C" int pv_attention(const pv_attention_params* params, const pv_heads* q
   }
   const bool bf16 = params->dtype == PV_BF16;
   return (bf16 ? attn_forward_bf16 : attn_forward_half)(a, m, dim3(tiles * heads), reinterpret_cast<cudaStream_t>(stream));
+} catch (...) {
+  return caught();
 }
 
 extern "C" int pv_attention_backward(const pv_attention_params* params, const pv_heads* dout, const pv_heads* q,
                                      const pv_heads* k, const pv_heads* v, const pv_heads* out, const float* lse,
-                                     const pv_heads* dq, const pv_heads* dk, const pv_heads* dv, pv_stream_t stream) {
+                                     const pv_heads* dq, const pv_heads* dk, const pv_heads* dv, pv_stream_t stream) try {
   if (!params || !params->q_offsets || !params->k_offsets || !dq || !dk || !dv) return PV_ERR_INVALID;
   int dev = 0, st;
   if ((st = check_offsets(params->q_offsets, params->frames)) != PV_OK ||
@@ -390,4 +392,6 @@ extern "C" int pv_attention_backward(const pv_attention_params* params, const pv
   if (range && (st = attn_backward_up_half(a, cs)) != PV_OK) return st;
   if ((st = (bf16 ? attn_backward_dq_bf16 : attn_backward_dq_half)(a, m, dim3(q_tiles * a.heads), cs)) != PV_OK) return st;
   return (bf16 ? attn_backward_dkv_bf16 : attn_backward_dkv_half)(b, m, dim3(k_tiles * b.heads), cs);
+} catch (...) {
+  return caught();
 }

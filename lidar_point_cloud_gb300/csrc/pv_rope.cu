@@ -414,7 +414,7 @@ int launch(K kernel, int blocks, const RopeArgs& a, pv_stream_t stream) {
 }  // namespace
 
 extern "C" int pv_qk_norm_rope(const pv_rope_params* params, const pv_heads* q, const pv_heads* k,
-                               const pv_heads* out_q, const pv_heads* out_k, pv_stream_t stream) {
+                               const pv_heads* out_q, const pv_heads* out_k, pv_stream_t stream) try {
   int dev = 0, st = check_params(params, &dev);
   if (st != PV_OK) return st;
   const int elem = dtype_size(params->dtype);
@@ -440,11 +440,13 @@ extern "C" int pv_qk_norm_rope(const pv_rope_params* params, const pv_heads* q, 
     case PV_BF16: return launch(pv_rope_kernel<__nv_bfloat16>, blocks, a, stream);
     default: return launch(pv_rope_kernel<__half>, blocks, a, stream);
   }
+} catch (...) {
+  return caught();
 }
 
 extern "C" int pv_qk_norm_rope_backward(const pv_rope_params* params, const pv_heads* dout_q, const pv_heads* dout_k,
                                         const pv_heads* q, const pv_heads* k, const pv_heads* dq, const pv_heads* dk,
-                                        float* dq_weight, float* dk_weight, pv_stream_t stream) {
+                                        float* dq_weight, float* dk_weight, pv_stream_t stream) try {
   int dev = 0, st = check_params(params, &dev);
   if (st != PV_OK) return st;
   const int elem = dtype_size(params->dtype);
@@ -483,4 +485,6 @@ extern "C" int pv_qk_norm_rope_backward(const pv_rope_params* params, const pv_h
     case PV_BF16: return launch(pv_rope_backward_kernel<__nv_bfloat16>, blocks, a, stream);
     default: return launch(pv_rope_backward_kernel<__half>, blocks, a, stream);
   }
+} catch (...) {
+  return caught();
 }

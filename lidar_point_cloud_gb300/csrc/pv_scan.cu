@@ -694,7 +694,7 @@ extern "C" int64_t pv_gated_scan_states(const pv_scan_params* params) {
 }
 
 extern "C" int pv_gated_scan(const pv_scan_params* params, const float* h0, void* out_h, int64_t h_stride,
-                             float* out_last, float* out_states, pv_stream_t stream) {
+                             float* out_last, float* out_states, pv_stream_t stream) try {
   int st = check_params(params);
   if (st != PV_OK) return st;
   const int64_t rows = params->offsets[params->frames], C = params->channels;
@@ -720,11 +720,13 @@ extern "C" int pv_gated_scan(const pv_scan_params* params, const float* h0, void
   a.last = out_last;
   a.states = out_states;
   return start<false>(params, sh, a, dev, stream);
+} catch (...) {
+  return caught();
 }
 
 extern "C" int pv_gated_scan_backward(const pv_scan_params* params, const void* dh, int64_t dh_stride,
                                       const float* dlast, const float* states, void* dx, int64_t dx_stride,
-                                      void* dgate, int64_t dgate_stride, float* dh0, pv_stream_t stream) {
+                                      void* dgate, int64_t dgate_stride, float* dh0, pv_stream_t stream) try {
   int st = check_params(params);
   if (st != PV_OK) return st;
   const int64_t rows = params->offsets[params->frames], C = params->channels;
@@ -754,4 +756,6 @@ extern "C" int pv_gated_scan_backward(const pv_scan_params* params, const void* 
   a.last = dh0;
   a.states = const_cast<float*>(states);
   return start<true>(params, sh, a, dev, stream);
+} catch (...) {
+  return caught();
 }

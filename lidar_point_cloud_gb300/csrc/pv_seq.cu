@@ -6,6 +6,7 @@
 #include <atomic>
 #include <list>
 #include <map>
+#include <memory>
 #include <new>
 #include <tuple>
 
@@ -81,6 +82,16 @@ int sm_count(int dev) {
   return g_sms[dev];
 }
 
+int caught() noexcept {
+  try {
+    throw;
+  } catch (const std::bad_alloc&) {
+    return PV_ERR_ALLOC;
+  } catch (...) {
+    return PV_ERR_CUDA;
+  }
+}
+
 int check_offsets(const int64_t* off, int n) {
   if (!off || n < 1 || n > PV_MAX_FRAMES || off[0] != 0) return PV_ERR_INVALID;
   for (int i = 0; i < n; ++i)
@@ -116,8 +127,7 @@ int Scratch::open(int dev, pv_stream_t stream, ScratchKind kind, size_t bytes) {
   {
     std::lock_guard<std::mutex> lk(g_seq_mu);
     SeqSpace*& sp = g_seq[std::make_tuple(dev, stream, static_cast<int>(kind))];
-    if (!sp) sp = new (std::nothrow) SeqSpace();
-    if (!sp) return PV_ERR_ALLOC;
+    if (!sp) sp = new SeqSpace();
     sp->device = dev;
     sp->mu.lock();
     sp_ = sp;
@@ -159,19 +169,19 @@ int Scratch::open_captured(int dev, pv_stream_t stream, ScratchKind kind, size_t
   }
   RelaxedCapture relaxed;
   if (!idle) {
-    idle = new (std::nothrow) SeqSpace();
-    if (!idle) return PV_ERR_ALLOC;
+    auto space = std::make_unique<SeqSpace>();
+    g_captured.push_back(space.get());
     void* mem = nullptr;
     const int st = zeroed_now(&mem, need);
     if (st != PV_OK) {
-      delete idle;
+      g_captured.pop_back();
       return st;
     }
+    idle = space.release();
     idle->device = dev;
     idle->mem = static_cast<unsigned char*>(mem);
     idle->cap = need;
     idle->kind = kind;
-    g_captured.push_back(idle);
   }
   cudaUserObject_t owner = nullptr;
   if (cudaUserObjectCreate(&owner, idle, give_back, 1, cudaUserObjectNoDestructorSync) != cudaSuccess) {
@@ -202,6 +212,7 @@ int release_scratch() {
   int st = PV_OK;
   for (auto& kv : g_seq) {
     SeqSpace* sp = kv.second;
+    if (!sp) continue;  // the host had no memory for it
     DeviceScope scope(sp->device);
     if (!scope.ok() || cudaDeviceSynchronize() != cudaSuccess) st = PV_ERR_CUDA;
     sp->mu.lock();  // wait for a call that is still enqueueing

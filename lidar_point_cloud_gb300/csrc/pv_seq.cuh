@@ -35,6 +35,10 @@ int check_heads(const pv_heads* h, int64_t rows, int heads, int elem, int dev);
 // The same for what a call writes: its rows and heads do not share memory by a stride of 0.
 int check_out_heads(const pv_heads* h, int64_t rows, int heads, int elem, int dev);
 
+// The status of the exception that is being handled.  The entries are called from C: each
+// ends in a handler that returns this (maps, lists and locks may throw).
+int caught() noexcept;
+
 // Makes `dev` current for a scope.
 class DeviceScope {
  public:
