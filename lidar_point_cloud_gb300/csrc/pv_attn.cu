@@ -364,13 +364,13 @@ extern "C" int pv_attention_backward(const pv_attention_params* params, const pv
       most = std::max<int64_t>(most, static_cast<int64_t>(a.q0[f + 1] - a.q0[f]) * a.H + static_cast<int64_t>(a.k0[f + 1] - a.k0[f]) * a.Hk);
     a.norm_parts = static_cast<int>(std::min<int64_t>(std::max(1, std::min(256, 4 * sms / a.frames)), (most + 63) / 64));
   }
-  const size_t ups = range ? static_cast<size_t>(a.frames) * (2 * a.norm_parts + 1) : 0;
+  const size_t ups = range ? static_cast<size_t>(a.frames) * 2 * (a.norm_parts + 1) : 0;
   if ((st = scratch.open(dev, stream, kPlain, sizeof(float) * (sides + parts + ups))) != PV_OK) return st;
   a.sides = static_cast<float*>(scratch.body());
   a.part_o = a.sides + sides;
   if (range) {
     a.norms = reinterpret_cast<float2*>(a.part_o + parts);
-    a.up = reinterpret_cast<float*>(a.norms + static_cast<size_t>(a.frames) * a.norm_parts);
+    a.up = a.norms + static_cast<size_t>(a.frames) * a.norm_parts;
     a.norms_done = static_cast<unsigned int*>(scratch.head()) + kHeadFrames;
   }
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);

@@ -24,9 +24,10 @@ struct AttnArgs {
   // delta (negated), [3] positions.
   float* sides;
   long long sides_row;
-  // Backward, float16: per frame, what the scores' gradients are scaled by on top of the
-  // probabilities' factor, found by norm_parts blocks a frame.  Null for bfloat16.
-  float* up;       // [frames]
+  // Backward, float16: per frame, what dk's score gradients are scaled by on top of the
+  // probabilities' factor, and the largest norm of a row of v, found by norm_parts blocks a
+  // frame.  Null for bfloat16.
+  float2* up;      // [frames]
   float2* norms;   // [frames, norm_parts]: largest squared norms of rows of dout and v
   unsigned int* norms_done;  // [frames], zero between launches
   int norm_parts;

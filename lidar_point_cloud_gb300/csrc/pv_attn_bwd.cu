@@ -43,8 +43,9 @@
 // P and dS are held 16 times their values in the storage type: float16 runs out
 // of exponent below 2^-14, where the probabilities of some thousand keys lie.  How large
 // dS is goes by dout, too, which a loss scale moves anywhere, and float16 ends at 65,504:
-// there dS has a frame's own power of two, by |dP - delta| <= 2 |dout| |v| for the largest rows
-// of the frame, so that 2^15 bounds it.  One small kernel reads dout and v for that.
+// there dS has a power of two by |dP - delta| <= 2 |dout| |v|, so that 2^15 bounds it: for dq the
+// row's own, with the largest v of the frame, for dk, whose sums go over the queries, the
+// frame's, with the largest dout, too.  One small kernel reads dout and v for that.
 
 #include "pv_attn.cuh"
 #include "pv_tc.cuh"
@@ -78,6 +79,7 @@ struct Smem {
   alignas(16) float side[kSides][5][kOther];  // lse (as an offset of the exponent), delta (negated), positions
   float rest[kGroups][kOwn];      // dq: each warpgroup's sum of P (dP - delta)
   float guess[kOwn];              // dq: do.o of the rounded o
+  float up[kOwn];                 // dq, float16: the rows' factors
   uint64_t own_full, dirty[2], clean[2], full[2][kSlots], empty[2][kSlots], s_full, dp_full, p_full, ds_full, acc_full, side_full[kSides],
       side_empty[kSides];
   uint32_t tmem;
@@ -93,10 +95,18 @@ struct Rows {
   float slope[4], mul;     // exponent = mul * (score + slope * distance) + off
   float cap_in;            // score = tanh of half this times the raw one, if capped
   float off[4], delta[4];  // dq: the rows' own (delta negated, times `up`); dk, dv: the columns', in shared memory
-  float up;                // float16: dS is `up` times 16 times its value
+  float up[4];             // float16: dS is `up` times 16 times its value
   float total[4];          // dq: sums of 16 P (dP - delta), times `up`
   int lo[4], hi[4];        // of the thread's first column, columns seen: lo <= column < hi
 };
+
+// The power of two for gradients of rows of these norms; 1 where they are 0 or not finite.
+__device__ __forceinline__ float factor(float dout, float v) {
+  const float bound = 2.0f * dout * v;
+  int e = 15 - static_cast<int>(kUp);
+  if (bound > 0.0f && bound < INFINITY) frexpf(bound, &e);  // bound < 2^e
+  return ldexpf(1.0f, 15 - static_cast<int>(kUp) - e);
+}
 
 constexpr int kElems = kCols / 2;  // of two of the four rows: registers of one 16-lane fragment
 __device__ __forceinline__ constexpr int row_of(int h, int x) { return 2 * h + ((x >> 1) & 1); }
@@ -188,7 +198,7 @@ __device__ __forceinline__ void gradients(uint32_t at, const float* side, Rows& 
       float2 d = make_float2(row.delta[r], row.delta[r]);
       if (kDkv) d = *reinterpret_cast<const float2*>(side + kOther + col_of(x));
       if (std::is_same<T, __half>::value)
-        fma2(g[h][x], g[h][x + 1], g[h][x], g[h][x + 1], row.up, row.up, d.x, d.y);
+        fma2(g[h][x], g[h][x + 1], g[h][x], g[h][x + 1], row.up[kDkv ? 0 : r], row.up[kDkv ? 0 : r], d.x, d.y);
       else
         add2(g[h][x], g[h][x + 1], g[h][x], g[h][x + 1], d.x, d.y);
       // (A hidden place has e = 0, but what stands at it need not be finite.)
@@ -468,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const long long own_row = (kDkv ? a.k0[f] : a.q0[f]) + own;
     if (!kDkv) {
       if (wg == 0) {
-        float delta = 0.0f;
+        float delta = 0.0f, norm = 0.0f;
         if (live) {
           const char* o = a.o.data + own_row * a.o.row + own_head * a.o.head;
           const char* g = a.dout.data + own_row * a.dout.row + own_head * a.dout.head;
@@ -478,14 +488,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             Pack<T>::load(g + d * 2, y);
 #pragma unroll
             for (int e = 0; e < 8; ++e) delta = fmaf(x[e], y[e], delta);
+            if (!kBf16) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) norm = fmaf(y[e], y[e], norm);
+            }
           }
         }
         sm.guess[r] = delta;
+        if (!kBf16) sm.up[r] = a.up ? factor(sqrtf(norm), a.up[f].y) : 1.0f;
       }
       math_sync();
     }
     Rows row{};
-    row.up = !kBf16 && a.up ? a.up[f] : 1.0f;
+    const float up_frame = !kBf16 && a.up ? a.up[f].x : 1.0f;
+    if (kDkv) row.up[0] = up_frame;
     row.mul = (kCap ? a.cap : a.scale) * kLog2e;
     row.cap_in = kCap ? 2.0f * a.scale * kLog2e / a.cap : 0.0f;
     // A place is seen if its column is at least `from` and below `to`.
@@ -505,7 +521,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!kDkv) {
         if (in) row.off[x] = fmaf(-kLog2e, a.lse[static_cast<long long>(own_head) * a.queries + at], kUp);
-        row.delta[x] = -sm.guess[rx] * row.up;
+        if (!kBf16) row.up[x] = sm.up[rx];
+        row.delta[x] = kBf16 ? -sm.guess[rx] : -sm.guess[rx] * row.up[x];
       }
       if (kSlopes && in) {
         if (!kDkv) row.slope[x] = -a.slopes[own_head] * kLog2e / row.mul;
@@ -586,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (live && wg == 0) {
         float* const side = a.sides + own_head * a.sides_row + a.side0[f] + own;
         side[0] = fmaf(-kLog2e, a.lse[static_cast<long long>(own_head) * a.queries + own_row], kUp);
-        side[a.H * a.sides_row] = -fmaf(sm.guess[r], row.up, total);
+        side[a.H * a.sides_row] = kBf16 ? -(sm.guess[r] + total) : -fmaf(sm.guess[r], up_frame, total * (up_frame / sm.up[r]));
         if (own_head == 0)
           for (int c = 0; c < a.axes; ++c)
             side[(2 * a.H + c) * a.sides_row] = static_cast<float>(a.qpos[own_row * a.qpos_stride + c]);
@@ -599,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool parts = kDkv && a.head_parts > 1;
     float* part = parts ? a.part_o + (((static_cast<long long>(head % a.head_parts) * 2 + which) * a.keys + own_row) * a.Hk + own_head) * a.D
                         : nullptr;
-    const float k1 = (kDkv && which ? 1.0f : a.scale / row.up) * kDown * bad;
+    const float k1 = (kDkv && which ? 1.0f : kBf16 ? a.scale : a.scale / (kDkv ? up_frame : sm.up[r])) * kDown * bad;
     const uint32_t acc = mine + 256 + (kDkv && which ? 64 * kBlocks : 0);
     for (int x = (kDkv ? wg >> 1 : wg) * 16; x < a.Dn; x += kDkv ? 32 : 64) {
       uint32_t c[16], d[16];
@@ -721,10 +738,7 @@ __global__ void __launch_bounds__(kNormThreads) pv_attn_up_kernel(const __grid_c
     }
     m = block_most(m);
     if (threadIdx.x == 0) {
-      int e = 11;  // nothing that is not 0: a factor of 1
-      const float bound = 2.0f * sqrtf(m.x) * sqrtf(m.y);
-      if (bound > 0.0f) frexpf(bound, &e);  // bound < 2^e
-      a.up[f] = ldexpf(1.0f, 15 - e - static_cast<int>(kUp));
+      a.up[f] = make_float2(factor(sqrtf(m.x), sqrtf(m.y)), sqrtf(m.y));
       a.norms_done[f] = 0;
     }
   }

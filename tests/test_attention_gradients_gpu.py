@@ -76,3 +76,17 @@ def test_a_gradient_row_that_overflowed_leaves_the_other_queries_alone(dtype):
     keep = torch.arange(60, device="cuda") != 17
     assert torch.equal(dq[keep], dq2[keep]) and not torch.isfinite(dq2[17]).any()
     assert not torch.isfinite(dk2).any() and not torch.isfinite(dv2).any()
+
+
+@pytest.mark.parametrize("cap", [0.0, 10.0])
+def test_rows_of_very_different_gradients(cap):
+    # A few loud rows beside quiet ones, 2^24 apart: the quiet rows' dq is as good as theirs alone would be.
+    # Two roundings to float16 of 2^-12 and sums that average them out: 2^-9 of a row's norm leaves room.
+    t = make([60], [90], 2, 1, 64, torch.float16, loud=2.0)
+    loud = torch.zeros(60, dtype=torch.bool, device="cuda")
+    loud[[3, 17, 40]] = True
+    t["dout"] = (t["dout"].float() * torch.where(loud, 2.0 ** 13, 2.0 ** -11)[:, None, None]).half()
+    _, _, (dq, _, _) = check(t, cap=cap)
+    want = ref.attention(t["q"], t["k"], t["v"], t["qo"], t["ko"], cap=cap, dout=t["dout"], **t["how"])[0]["dq"]
+    off = ((dq.double() - want).norm(dim=-1) - 2.0 ** -25 * 8).clamp_min(0)  # (64 roundings of numbers near 2^-14)
+    assert (off / want.norm(dim=-1)).max() < 2.0 ** -9
