@@ -40,9 +40,11 @@
 // 607 us.  Tensor cores 34 and 46 %, issue slots 51 to 61 %: products and arithmetic take
 // turns for want of tensor memory.
 //
-// P and dS are held 16 times their values in the storage type: float16 runs out
-// of exponent below 2^-14, where the probabilities of some thousand keys lie.  How large
-// dS is goes by dout, too, which a loss scale moves anywhere, and float16 ends at 65,504:
+// P and dS are held 2^kUp times their values in the storage type.  Float16 runs out of
+// exponent below 2^-14, where the probabilities of some thousand keys lie, and ends at
+// 65,504: a factor of 1,024 keeps P whole down to 2^-24, and leaves room for one of 60 (of a
+// score so large that 32 bits hold it badly).  How large
+// dS is goes by dout, too, which a loss scale moves anywhere:
 // there dS has a power of two by |dP - delta| <= 2 |dout| |v|, so that 2^15 bounds it: for dq the
 // row's own, with the largest v of the frame, for dk, whose sums go over the queries, the
 // frame's, with the largest dout, too.  One small kernel reads dout and v for that.
@@ -67,8 +69,9 @@ constexpr int kOther = 128;  // rows of a step
 constexpr int kCols = kOther / kGroups;  // columns of a thread
 constexpr int kSides = 3;    // slots of what belongs to the other side's rows
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kUp = 4.0f;  // log2 of the factor on P (and, in bfloat16, dS)
-constexpr float kDown = 0.0625f;
+constexpr bool kHalf = std::is_same<Storage, __half>::value;
+constexpr float kUp = kHalf ? 10.0f : 4.0f;  // log2 of the factor on P (and, in bfloat16, dS)
+constexpr float kDown = kHalf ? 0x1p-10f : 0x1p-4f;
 
 template <int kBlocks>
 struct Smem {
@@ -95,8 +98,8 @@ struct Rows {
   float slope[4], mul;     // exponent = mul * (score + slope * distance) + off
   float cap_in;            // score = tanh of half this times the raw one, if capped
   float off[4], delta[4];  // dq: the rows' own (delta negated, times `up`); dk, dv: the columns', in shared memory
-  float up[4];             // float16: dS is `up` times 16 times its value
-  float total[4];          // dq: sums of 16 P (dP - delta), times `up`
+  float up[4];             // float16: dS is `up` times 2^kUp times its value
+  float total[4];          // dq: sums of 2^kUp P (dP - delta), times `up`
   int lo[4], hi[4];        // of the thread's first column, columns seen: lo <= column < hi
 };
 
@@ -112,10 +115,10 @@ constexpr int kElems = kCols / 2;  // of two of the four rows: registers of one 
 __device__ __forceinline__ constexpr int row_of(int h, int x) { return 2 * h + ((x >> 1) & 1); }
 __device__ __forceinline__ constexpr int col_of(int x) { return (x >> 2) * 8 + (x & 1); }
 
-// 32 rows' scores of 32 columns, from column `at` of tensor memory on, to 16 P there, in
+// 32 rows' scores of 32 columns, from column `at` of tensor memory on, to P there, in
 // the storage type.  `side` points to what belongs to the thread's first column.
-// u keeps what dS is made of: 16 P times the cap's slope; with a cap, dq takes that
-// for acc2 too, and what the slope took from 16 P, for the sum of P dP, goes to `rest`
+// u keeps what dS is made of: P times the cap's slope; with a cap, dq takes that
+// for acc2 too, and what the slope took from P, for the sum of P dP, goes to `rest`
 // as half pairs (a small share, of which the rounding does not show).  One operation
 // after the other over all elements: an element's chain is long, 32 of them hide it.
 template <typename T, bool kDkv, int kCap, bool kSlopes, bool kMask>
@@ -179,7 +182,7 @@ __device__ __forceinline__ void probabilities(uint32_t at, const float* side, in
   }
 }
 
-// dP at column `at` to 16 dS there.
+// dP at column `at` to dS there.
 template <typename T, bool kDkv, int kCap, bool kMask>
 __device__ __forceinline__ void gradients(uint32_t at, const float* side, Rows& row, const float (*e)[kElems],
                                           const uint32_t (*rest)[kElems / 2]) {

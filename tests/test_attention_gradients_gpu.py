@@ -90,3 +90,17 @@ def test_rows_of_very_different_gradients(cap):
     want = ref.attention(t["q"], t["k"], t["v"], t["qo"], t["ko"], cap=cap, dout=t["dout"], **t["how"])[0]["dq"]
     off = ((dq.double() - want).norm(dim=-1) - 2.0 ** -25 * 8).clamp_min(0)  # (64 roundings of numbers near 2^-14)
     assert (off / want.norm(dim=-1)).max() < 2.0 ** -9
+
+
+def test_probabilities_of_millions_of_keys():
+    # Queries that see every key alike: dv of every key is the mean of dout's rows, times queries
+    # over keys.  A probability of 2^-23 and the result are each rounded by 2^-12 at most.
+    n, rows, D = 8_400_001, 4096, 8
+    k, q = torch.zeros((n, 1, D), dtype=torch.float16, device="cuda"), torch.zeros((rows, 1, D), dtype=torch.float16, device="cuda")
+    v = torch.randn((n, 1, D), device="cuda").half()
+    do = torch.full((rows, 1, D), 512.0, dtype=torch.float16, device="cuda")
+    o, lse = pv.attention(q, k, v, [0, rows], [0, n], return_lse=True)
+    _, _, dv = pv.attention_backward(do, q, k, v, o, lse, [0, rows], [0, n])
+    want = 512.0 * rows / n
+    # (32 bits add 2^-22 times lse, 16, to a probability.)
+    assert float((dv.double() / want - 1.0).abs().max()) < 2 * 2.0 ** -12 + 16 * 2.0 ** -21
