@@ -306,7 +306,9 @@ int pv_voxelize_static(const float* points, int64_t num_points, const float poin
  * check their arguments on the host as pv_voxelize does: a status is returned
  * and nothing is enqueued.  Row offsets are HOST arrays, read before the call
  * returns.  Sums, softmax statistics, norms and recurrent states are held in
- * 32 bits; outputs are rounded once.  Outputs do not overlap inputs unless a
+ * 32 bits.  Outputs are rounded once; in attention the tensor cores take the
+ * probabilities, and backward the scores' gradients, rounded to the tensors' type, too:
+ * a result's norm is then off by some 1.2 units of that type instead of 0.9.  Outputs do not overlap inputs unless a
  * call says so.
  */
 typedef enum pv_dtype { PV_F32 = 0, PV_BF16 = 1, PV_F16 = 2 } pv_dtype;

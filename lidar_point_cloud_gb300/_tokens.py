@@ -2,7 +2,8 @@
 
 A batch of frames (:func:`voxelize_batch`) is a ragged sequence of tokens, one
 row per voxel, frame b the rows ``offsets[b]:offsets[b + 1]``; ``offsets`` is a
-host sequence of ints, as ``frame_offsets`` of the voxelizer is.  The work is
+host sequence of ints (not the voxelizer's ``frame_offsets``, which count points: the
+tokens of each frame are counted in the coordinates' first column).  The work is
 done by libpv.so (``include/pv.h``, "Operators on voxel tokens"); this file
 checks dtypes, devices and shapes and allocates outputs.  There is no CPU
 fallback.  Nothing here records autograd history: a backward pass is a call of
@@ -251,6 +252,9 @@ def attention(q, k, v, q_offsets, k_offsets, scale: Optional[float] = None, cap:
     ``j <= i + nk - nq`` or ``j < prefix[frame]``.  A query that sees no key
     gives 0.  Returns out [queries, H, D], with ``return_lse`` also the float32
     [H, queries] logarithms of the softmax sums for :func:`attention_backward`.
+    Sums are held in 32 bits; the probabilities are rounded to q's type for the
+    product with v, as the tensor cores take them.  Tensors expanded over their
+    rows are copied.
     """
     if stream is not None:
         with _on(stream, q):
@@ -273,7 +277,9 @@ def attention_backward(dout, q, k, v, out, lse, q_offsets, k_offsets, scale: Opt
                        slopes=None, q_positions=None, k_positions=None, causal: bool = False, prefix=None,
                        stream=None):
     """Gradients (dq, dk, dv) of :func:`attention` from that of its output,
-    its inputs, ``out`` and ``lse``; the other arguments as there."""
+    its inputs, ``out`` and ``lse``; the other arguments as there.  Probabilities
+    and the scores' gradients are rounded to q's type for the products (in
+    float16 scaled so that they neither overflow nor run out of exponent)."""
     if stream is not None:
         with _on(stream, q):
             return attention_backward(dout, q, k, v, out, lse, q_offsets, k_offsets, scale, cap, slopes, q_positions,

@@ -36,9 +36,10 @@
 // the four that dq needs least, and no more exponentials.
 //
 // Measured: 4 ragged frames of up to 4,000, 8 heads of 64, distances, bf16: dq 207 us,
-// dk and dv 202 us; 12,289 causal tokens, capped, 8 heads over 2 of 128, f16: 590 and
-// 607 us.  Tensor cores 34 and 46 %, issue slots 51 to 61 %: products and arithmetic take
-// turns for want of tensor memory.
+// dk and dv 202 us; 12,289 causal tokens, capped, 8 heads over 2 of 128, f16: 600 and
+// 615 us.  Tensor cores 34 and 45 %, issue slots 50 to 61 %: products and arithmetic take
+// turns.  At 128 elements that is for want of tensor memory; heads of 64 or less leave 128
+// columns of it, where a second S would fit, which is not done.
 //
 // P and dS are held 2^kUp times their values in the storage type.  Float16 runs out of
 // exponent below 2^-14, where the probabilities of some thousand keys lie, and ends at

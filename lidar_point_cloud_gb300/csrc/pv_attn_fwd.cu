@@ -25,8 +25,9 @@
 // Probabilities are rounded to the storage type for the second product, as the
 // tensor cores take it; their sum is taken before rounding, in 32 bits.
 //
-// Measured: 24,571 causal tokens, 8 heads over 2 of 128, bf16, 743 us, 1,665 TFLOP/s:
-// bound by the tensor cores.  8 ragged frames of up to 6,000, 8 heads of 64: 414 us,
+// Measured: 24,571 causal tokens, 8 heads over 2 of 128, bf16, 743 us by itself (1,665
+// TFLOP/s), 795 to 820 us in a row, at the power limit (1,510 to 1,560): bound by the tensor
+// cores.  8 ragged frames of up to 6,000, 8 heads of 64: 414 us,
 // with distances 594 us: bound by the arithmetic between the products (two warps a
 // scheduler, 53 % of issue slots; four softmax warpgroups have too few registers, and
 // loading the scores in two or four pieces hides nothing: 601 and 660 us).  A cap is two more

@@ -31,11 +31,12 @@
 // h[t-1] is rebuilt inside the tile and x, gate and dh are read once.
 //
 // Bound by memory: forward 2 reads and 1 write per element, backward 3 and 2.
-// Measured at 204,057 steps of 512 channels in 32 frames, bf16: forward 150 us,
-// backward 250 us, 4.2 TB/s of these bytes; half of the issue slots, the barriers of
+// Measured at 204,057 steps of 512 channels in 32 frames, bf16: forward 151 us,
+// backward 255 us, 4.1 TB/s of these bytes; half of the issue slots, the barriers of
 // a tile the largest stall.  Two blocks a multiprocessor: three (forward, 85 registers
-// a thread) wait more for one another (425 us for both passes against 408), as do
-// blocks of 128 threads (420) and as many blocks as chains (462).
+// a thread) waited more for one another (425 us for both passes against 408, when a step
+// was s - z s + z x, which loses infinite states), as did blocks of 128 threads (420) and
+// as many blocks as chains (462).
 
 #include "pv_seq.cuh"
 
@@ -653,8 +654,8 @@ int start(const pv_scan_params* p, const Shape& sh, ScanArgs& a, int dev, pv_str
   int frames = 0;
   for (int b = 0; b < p->frames; ++b) frames += p->offsets[b + 1] > p->offsets[b];
   // Groups shorten a chain whose tiles are worked on side by side, and cost their maps'
-  // publishing and joining: half as many tiles as one chain has in flight.  (Forward and
-  // backward, bf16, 512 channels, groups of 1 and 8: 32 frames of up to 9,000 steps,
+  // publishing and joining: half as many tiles as one chain has in flight.  (As above, forward
+  // and backward, bf16, 512 channels, groups of 1 and 8: 32 frames of up to 9,000 steps,
   // 256 chains, 427 and 448 us; one frame of 60,000, 8 chains, 457 and 214 us.)
   const int64_t chains = std::max<int64_t>(1, static_cast<int64_t>(frames) * sh.slabs);
   a.group_log2 = 0;
