@@ -195,7 +195,7 @@ def qk_norm_rope_backward(dout_q, dout_k, q, k, q_weight, k_weight, positions, i
     p = _rope_params(q, k, q_weight, k_weight, positions, inv_freq, eps)
     (dq, hdq), (dk, hdk) = _new(q), _new(k)
     D = q.shape[2]
-    dw = torch.empty((2, D), dtype=torch.float32, device=q.device)
+    dw = (torch.empty if k.shape[1] else torch.zeros)((2, D), dtype=torch.float32, device=q.device)
     at = dw.data_ptr()
     _check(load().pv_qk_norm_rope_backward(p, _heads(dout_q, "dout_q", q), _heads(dout_k, "dout_k", k), hq, hk, hdq, hdk,
                                            at, at + 4 * D, _stream(q)), "pv_qk_norm_rope_backward")
