@@ -31,6 +31,12 @@ def _dtype(t, name: str, wide: bool = True) -> int:
     return code
 
 
+def _strides(t, shape):
+    """Those of rows and heads (0 where there is one only: torch gives it any) and of head_dim."""
+    row, head, one = t.stride()
+    return row if shape[0] > 1 else 0, head if shape[1] > 1 else 0, one
+
+
 def _heads(t, name: str, like=None, heads: Optional[int] = None, apart: bool = False) -> Heads:
     """[rows, heads, head_dim] as the library reads it: any strides that are
     multiples of 16 bytes, the last dimension dense.  `like`: the tensor whose
@@ -48,11 +54,11 @@ def _heads(t, name: str, like=None, heads: Optional[int] = None, apart: bool = F
             raise TypeError(f"{name} must have the dtype and device of the other tensors")
         if shape[2] != like.shape[2] or (heads is None and shape != like.shape):
             raise ValueError(f"{name} has the wrong shape {tuple(shape)}")
-    row, head, one = t.stride()
+    row, head, one = _strides(t, shape)
     copy = apart and row == 0 and shape[0] > 1
     if copy:
         t = t.contiguous()
-        row, head, one = t.stride()
+        row, head, one = _strides(t, shape)
     at = t.data_ptr()
     size = t.element_size()
     if (at | row * size | head * size) & 15 or one != 1 or row < 0:
@@ -80,7 +86,7 @@ def _dense(like):
 def _new(like):
     """A dense tensor like this one, and how the library reads it."""
     t = _dense(like)
-    row, head, _ = t.stride()
+    row, head, _ = _strides(t, t.shape)
     return t, Heads(t.data_ptr(), row, head)
 
 

@@ -1,4 +1,5 @@
-"""Attention on tensors expanded over their rows, as the gradient of a sum over rows is."""
+"""Attention on tensors expanded over their rows, as the gradient of a sum over rows is, or over their
+heads, and on single rows and heads."""
 
 from __future__ import annotations
 
@@ -72,3 +73,27 @@ def test_the_library_refuses_what_its_tiles_cannot_read():
         pv.qk_norm_rope(t["q"], t["q"], w, w, pos, pv.rope_frequencies(64, device="cuda"),
                         out=(o, o[:, :1].expand(-1, 2, -1)))
     del alive
+
+
+def test_strides_of_a_single_row_or_head_do_not_matter():
+    t = make([33], [50], 1, 1, 64, torch.bfloat16)
+    want = run(t)
+    odd = {n: (x.as_strided(x.shape, (64, 1, 1)) if isinstance(x, torch.Tensor) else x) for n, x in t.items()}
+    assert all(torch.equal(a, b) for a, b in zip(run(odd), want))
+    one = make([1], [1], 4, 2, 64, torch.bfloat16)
+    want = run(one)
+    for n in ("q", "k", "v", "dout"):
+        one[n] = one[n].as_strided(one[n].shape, (3, 64, 1))
+    assert all(torch.equal(a, b) for a, b in zip(run(one), want))
+
+
+def test_heads_expanded_from_one():
+    # The gradient of out.sum(1), and queries that all heads share.
+    t = make([130, 70], [90, 60], 4, 2, 64, torch.float16)
+    for names in (("dout",), ("q",), ("q", "k", "v", "dout")):
+        u = dict(t)
+        for n in names:
+            u[n] = t[n][:, :1].expand(-1, t[n].shape[1], -1)
+        dense = {n: (x.contiguous() if isinstance(x, torch.Tensor) else x) for n, x in u.items()}
+        for a, b in zip(run(u), run(dense)):
+            assert (a.float() - b.float()).abs().max() <= 2.0 ** -9 * b[b.isfinite()].float().abs().max()
