@@ -144,6 +144,6 @@ def test_what_a_destroyed_graph_held_is_used_again():
         gc.collect()
         torch.cuda.synchronize()
         torch.cuda.empty_cache()
-        time.sleep(0.05)  # the space is given back by a thread of the driver's
+        time.sleep(0.05)  # the space is given back by a thread of CUDA's
         free.append(torch.cuda.mem_get_info()[0])
     assert free[3] - free[-1] < 150 << 20
