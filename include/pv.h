@@ -475,9 +475,10 @@ int pv_gated_scan_backward(const pv_scan_params* params, const void* dh, int64_t
  *   state, last   device float32 [frames, heads, head_dim, head_dim] (of k, then of v), 16-byte
  *                 aligned, or NULL; apart from one another.
  * The state is held in 32 bits, and so is what is added to it.  The tensor cores take
- * scores (in two parts where no frame has more than 128 tokens) and, once for each 128 tokens, the
+ * scores (in two parts in frames of up to 128 tokens) and, once for each 128 tokens, the
  * state rounded to bfloat16 for the outputs.  Rows of other
- * frames never reach a result; what is not finite may come out as NaN.
+ * frames never reach a result; what is not finite may come out as NaN.  How a frame of more than 128 tokens is cut,
+ * and so the roundings of its results, goes by the frames of the call; a shorter one has the same bits in every call.
  */
 typedef struct pv_linear_params {
   int frames;

@@ -500,10 +500,14 @@ struct OutSmem {
 // Columns of tensor memory: two buffers of scores, the output's terms (scores; the chunk's state, the segment's).
 constexpr int kP = 0, kO = 256, kZ = 320;
 
-// kRest: scores are taken in two bfloat16 parts, for calls whose frames have one chunk each.  There few terms
-// make a row, and one's rounding shows (a single token's output is one score times v); in longer frames
-// two parts turn 1.41 times the output's own rounding into 1.2 and take 8 ragged frames of up to 6,000 from 58 to 63 us.
-template <int kBlocks, bool kRest>
+// Scores are taken in two bfloat16 parts in frames of one chunk.  There few terms make a row, and one's
+// rounding shows (a single token's output is one score times v); in longer frames two parts turn 1.41 times the output's own
+// rounding into 1.2 and take 8 ragged frames of up to 6,000 from 58 to 63 us.  It goes by the frame, so that what a
+// frame gives does not depend on the frames beside it; calls whose frames are all alike have a kernel without the question
+// (asked in every block, the same 8 frames take 60 us).
+enum Scores { kOnePart, kTwoParts, kByFrame };
+
+template <int kBlocks, int kScores>
 __global__ void __launch_bounds__(kOutThreads, 1)
     pv_linear_out_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ Maps maps) {
   using S = OutSmem<kBlocks>;
@@ -515,6 +519,7 @@ __global__ void __launch_bounds__(kOutThreads, 1)
   const Run& run = a.run[blockIdx.y];
   const Place at = place_of(a, run);
   const int count = at.count;
+  const bool two = kScores == kTwoParts || (kScores == kByFrame && at.chunks == 1);
   // From the segment's last chunk to its first: what the states' kernel read and wrote last is still in the L2 cache
   // (24,571 tokens, 8 heads of 128: 86 us from the first to the last, 84 like this).
   auto nth = [&](int i) { return count - 1 - i; };
@@ -615,7 +620,7 @@ __global__ void __launch_bounds__(kOutThreads, 1)
           for (int x = 0; x < kRows / 16; ++x) {
             const uint32_t at_p = p + (x >> 1) * 32 + (x & 1) * 8, at_c = c + x * (2048 >> 4);
             mma_ts(tm + kO, at_p, at_c, word_o, x > 0);
-            if constexpr (kRest) mma_ts(tm + kO, at_p + 16, at_c, word_o, true);
+            if (two) mma_ts(tm + kO, at_p + 16, at_c, word_o, true);
           }
           mma_commit(&sm.o_full);
           mma_commit(&sm.c_empty[slot]);
@@ -636,7 +641,7 @@ __global__ void __launch_bounds__(kOutThreads, 1)
 #pragma unroll 1
       for (int j = 0; j < 4; ++j) {
         // (Where the block's 32 scores were: what they are rounded to and, if it is taken, what that leaves.)
-        uint32_t out[kRest ? 32 : 16];
+        uint32_t out[kScores == kOnePart ? 16 : 32];
         float v[32];
         if (at.reverse ? j < diagonal : j > diagonal) {
 #pragma unroll
@@ -676,16 +681,17 @@ __global__ void __launch_bounds__(kOutThreads, 1)
             }
           }
         }
-        if constexpr (kRest) {
+        if constexpr (kScores != kOnePart) {
+          if (two) {
 #pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            const float r0 = __uint_as_float(out[x] << 16), r1 = __uint_as_float(out[x] & 0xFFFF0000u);
-            out[16 + x] = Pack<T>::two(v[2 * x] - r0, v[2 * x + 1] - r1);
+            for (int x = 0; x < 16; ++x) {
+              const float r0 = __uint_as_float(out[x] << 16), r1 = __uint_as_float(out[x] & 0xFFFF0000u);
+              out[16 + x] = Pack<T>::two(v[2 * x] - r0, v[2 * x + 1] - r1);
+            }
+            tmem_st32(own + 32 * j, out);
           }
-          tmem_st32(own + 32 * j, out);
-        } else {
-          tmem_st16(own + 32 * j, out);
         }
+        if (!two) tmem_st16(own + 32 * j, out);
       }
       ok = ok && warp_wait_for(&sm.c_full[slot], (i / S::kStages) & 1, given_up);
       if (len < kRows) {
@@ -882,22 +888,32 @@ int chunk_of(const LinArgs& a, int runs, int sms) {
   return best;
 }
 
+template <int kBlocks, int kScores>
+int launch_out(const LinArgs& a, const Maps& m, dim3 grid, cudaStream_t s) {
+  const int smem = static_cast<int>(sizeof(OutSmem<kBlocks>)) + 1024, st = allow_smem(pv_linear_out_kernel<kBlocks, kScores>, smem);
+  return st != PV_OK ? st : launch_pdl(pv_linear_out_kernel<kBlocks, kScores>, grid, kOutThreads, smem, s, a, m);
+}
+
 template <int kBlocks>
-int launch_runs(const LinArgs& a, const Maps& m, int segments, bool some, bool rest, int runs, cudaStream_t s) {
+int launch_runs(const LinArgs& a, const Maps& m, int segments, int runs, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>(segments) * a.H * a.halves, runs);
-  const int first = static_cast<int>(sizeof(StateSmem<kBlocks>)) + 1024, second = static_cast<int>(sizeof(OutSmem<kBlocks>)) + 1024;
+  const int smem = static_cast<int>(sizeof(StateSmem<kBlocks>)) + 1024;
   int st;
-  if ((st = allow_smem(pv_linear_states_kernel<kBlocks>, first)) != PV_OK ||
-      (st = rest ? allow_smem(pv_linear_out_kernel<kBlocks, true>, second) : allow_smem(pv_linear_out_kernel<kBlocks, false>, second)) != PV_OK)
+  if ((st = allow_smem(pv_linear_states_kernel<kBlocks>, smem)) != PV_OK ||
+      (st = launch_pdl(pv_linear_states_kernel<kBlocks>, grid, kStateThreads, smem, s, a, m)) != PV_OK)
     return st;
-  if ((st = launch_pdl(pv_linear_states_kernel<kBlocks>, grid, kStateThreads, first, s, a, m)) != PV_OK) return st;
   if (!a.whole) {
     const dim3 joins(static_cast<unsigned>(a.frames) * a.H * a.halves * (64 * kBlocks * kCols / 4 / 256), runs);
     if ((st = launch_pdl(pv_linear_join_kernel<kBlocks>, joins, 256, 0, s, a)) != PV_OK) return st;
   }
-  if (!some) return PV_OK;
-  return rest ? launch_pdl(pv_linear_out_kernel<kBlocks, true>, grid, kOutThreads, second, s, a, m)
-              : launch_pdl(pv_linear_out_kernel<kBlocks, false>, grid, kOutThreads, second, s, a, m);
+  bool shorts = false, longs = false;  // frames of one chunk, of several
+  for (int f = 0; f < a.frames; ++f) {
+    const int chunks = a.chunk0[f + 1] - a.chunk0[f];
+    shorts = shorts || chunks == 1, longs = longs || chunks > 1;
+  }
+  if (!shorts && !longs) return PV_OK;  // no rows
+  return !shorts ? launch_out<kBlocks, kOnePart>(a, m, grid, s)
+                 : longs ? launch_out<kBlocks, kByFrame>(a, m, grid, s) : launch_out<kBlocks, kTwoParts>(a, m, grid, s);
 }
 
 int go(LinArgs& a, const Maps& m, int runs, int dev, pv_stream_t stream) {
@@ -925,11 +941,8 @@ int go(LinArgs& a, const Maps& m, int runs, int dev, pv_stream_t stream) {
   a.starts = reinterpret_cast<unsigned char*>(a.segs + runs * a.seg_run);
   a.states = a.starts + 2 * runs * a.seg_run;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const bool some = a.off[a.frames] > 0;
-  bool rest = true;
-  for (int f = 0; f < a.frames; ++f) rest = rest && a.chunk0[f + 1] - a.chunk0[f] <= 1;
-  return a.D > 64 ? launch_runs<2>(a, m, static_cast<int>(segments), some, rest, runs, s)
-                  : launch_runs<1>(a, m, static_cast<int>(segments), some, rest, runs, s);
+  return a.D > 64 ? launch_runs<2>(a, m, static_cast<int>(segments), runs, s)
+                  : launch_runs<1>(a, m, static_cast<int>(segments), runs, s);
 }
 
 int maps_of(Maps* m, const LinArgs& a, std::initializer_list<const pv_heads*> tensors) {
