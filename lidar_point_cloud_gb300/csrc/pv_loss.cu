@@ -190,8 +190,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (++slot == kStages) slot = 0, parity ^= 1;
         }
       }
-      // (The second block waits for the first one at the end.)
-      if (rank == 0) bars_drain(sm.full, kStages, sent);
+      // (The first block's barriers tell when both blocks' loads have landed, but not of loads that it has not come to
+      // itself, if it has given up; those of the second block have landed, too, when the products are done with them.)
+      bars_drain(rank == 0 ? sm.full : sm.empty, kStages, sent);
     }
     __syncwarp();
   } else if (warp == kEpilogues) {
@@ -225,12 +226,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if constexpr (kMode == kProbs) wait_prior_grid();
     const int quarter = warp >> 2, row = rank * kHalf + (warp & 3) * 32 + lane;
     const uint32_t acc_empty[2] = {in_first(&sm.acc_empty[0]), in_first(&sm.acc_empty[1])};
+    // A warp whose wait has run out gives nothing back, and all that it writes from there on is NaN: the products stop
+    // at the accumulator that it keeps, and no other warp, of either block, finds another tile's in the place of its own.
+    bool ok = true;
     auto release = [&](int buf) {
       __syncwarp();
-      if (lane == 0) bar_arrive_at(acc_empty[buf]);
+      if (ok && lane == 0) bar_arrive_at(acc_empty[buf]);
     };
     const uint32_t own = tm + (static_cast<uint32_t>((warp & 3) * 32) << 16) + quarter * kOwn;
-    bool ok = true;
     for (int n = 0, i; (i = nth_tile<kMode>(a, pair, pairs, n)) >= 0; ++n) {
       const Tile t = tile_of<kMode>(a, i);
       const int buf = n & 1;
@@ -290,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c = 0; c < kOwn; ++c) v[c] = 0.0f;
           }
-          if (!ok) v[0] = NAN, r.x = 1.0f;
+          if (!ok) r.x = 1.0f, r.z = NAN;  // (and with it every exponential)
           if (lane == 0) tma_stores_read();
           __syncwarp();
 #pragma unroll
@@ -327,12 +330,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           // By TMA, as the probabilities are: rows by themselves would be written in pieces of 16 bytes
           // (40 rows, 214,272 classes of 512, backward: 233 us with rows stored by their threads, 163 like this).
           if (quarter * kOwn < t.n) {
-            const float by = *a.mult;
+            const float by = ok ? *a.mult : NAN;
             float v[kOwn];
             tmem_read64(own + buf * kN, v);
             tc_before();
             release(buf);
-            if (!ok) v[0] = NAN;
             if (lane == 0) tma_stores_read();
             __syncwarp();
 #pragma unroll
@@ -482,7 +484,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       float z[kFew];
       tmem_read32(tm + (static_cast<uint32_t>(warp * 32) << 16) + (n & 1) * kFew, z);
       tc_before();
-      warp_arrive(&sm.acc_empty[n & 1]);
+      if (ok) warp_arrive(&sm.acc_empty[n & 1]);
       if (i * 128 + warp * 32 + lane < a.V) {
 #pragma unroll
         for (int j = 0; j < kFew; ++j) {
