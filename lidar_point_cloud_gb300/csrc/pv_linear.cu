@@ -137,6 +137,8 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatil
   }
   return true;
 }
+// (A warp whose wait has run out neither writes what others read nor arrives for them: several warps' arrivals end a
+// barrier's phase, and those who still read would find another chunk's numbers in the place of their own.)
 __device__ __forceinline__ bool warp_wait_for(uint64_t* bar, uint32_t parity, volatile int* given_up) {
   return __all_sync(0xFFFFFFFFu, wait_for(bar, parity, given_up));
 }
@@ -350,6 +352,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
       const int step = to_end && i + 1 == at.count && !run.end_step ? 1 : 0;  // steps short of the next token
       ok = ok && warp_wait_for(&sm.full[slot], parity, given_up);
       if (i > 1) ok = ok && warp_wait_for(&sm.d_full[buf], ((i >> 1) - 1) & 1, given_up);
+      if (!ok) break;
       unsigned char* const c = sm.bc[slot] + kBlocks * kTile;
 #pragma unroll
       for (int x = 0; x < kRows; x += 64) {
@@ -449,7 +452,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
         }
       }
       tc_before();
-      warp_arrive(&sm.d_free[i & 1]);
+      if (ok) warp_arrive(&sm.d_free[i & 1]);
     }
     if (a.whole && to_end && own < a.D) {
       const float2 w = decay_exact(ld, static_cast<float>(at.n - (run.end_step ? 0 : 1)));
@@ -637,6 +640,7 @@ __global__ void __launch_bounds__(kOutThreads, 1)
     for (int i = turn; i < count; i += 2) {
       const int len = at.len_of(nth(i)), slot = i % S::kStages;
       ok = ok && warp_wait_for(&sm.p_full[turn], (i >> 1) & 1, given_up);
+      if (!ok) break;
       tc_after();
 #pragma unroll 1
       for (int j = 0; j < 4; ++j) {
@@ -693,7 +697,9 @@ __global__ void __launch_bounds__(kOutThreads, 1)
         }
         if (!two) tmem_st16(own + 32 * j, out);
       }
+      tc_wait_st();
       ok = ok && warp_wait_for(&sm.c_full[slot], (i / S::kStages) & 1, given_up);
+      if (!ok) break;
       if (len < kRows) {
         // Rows past the frame's end are another frame's: whatever they hold must not meet the zeros
         // of these places.
@@ -701,7 +707,6 @@ __global__ void __launch_bounds__(kOutThreads, 1)
           *reinterpret_cast<uint4*>(sm.in[slot] + kC + y * 16) = make_uint4(0, 0, 0, 0);
         fence_to_async();
       }
-      tc_wait_st();
       tc_before();
       warp_arrive(&sm.p_ready[turn]);
     }
@@ -723,7 +728,7 @@ __global__ void __launch_bounds__(kOutThreads, 1)
         tmem_read3x16(mine + kO + j, mine + kZ + j, mine + kZ + kCols + j, o, u, v);
         if (j + 16 == kCols / 2) {
           tc_before();
-          warp_arrive(&sm.o_free);
+          if (ok) warp_arrive(&sm.o_free);
         }
 #pragma unroll
         for (int x = 0; x < 16; x += 2) {

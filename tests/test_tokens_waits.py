@@ -28,7 +28,7 @@ def lines(source):
         return [x.split("//")[0] for x in f.read().splitlines()]
 
 
-@pytest.mark.parametrize("source,arrivals", [("pv_loss.cu", 2)])
+@pytest.mark.parametrize("source,arrivals", [("pv_loss.cu", 2), ("pv_linear.cu", 4)])
 def test_a_warp_arrives_only_for_what_it_has_seen(source, arrivals):
     found, stopped = 0, False
     for n, line in enumerate(lines(source)):
