@@ -772,7 +772,7 @@ struct StepArgs {
 // the states in DRAM, less than the host's part of the call.
 template <typename U>
 __global__ void __launch_bounds__(256) pv_linear_step_kernel(const __grid_constant__ StepArgs a) {
-  __shared__ float q[128], k[128], v[128];
+  __shared__ alignas(16) float q[128], k[128], v[128];  // (v is read in fours)
   __shared__ float4 sums[256];
   wait_prior_grid();
   const int i = blockIdx.x / a.H, h = blockIdx.x - i * a.H, D = a.D;
