@@ -539,7 +539,8 @@ int pv_rms_norm(const pv_norm_params* params, void* y, int64_t y_stride, void* h
 
 /* The same with y in 8 bits, for products in them: y is cut into groups of channels (group =
  * 32, 64 or 128; 0: a whole row is one), scale = max |y| / 448 over a group (never
- * below the smallest normal binary32, so that zeros stay zeros), value = e4m3(y / scale).  values: device
+ * below the smallest normal binary32, so that zeros stay zeros), value = e4m3(y / scale), y, scale and
+ * the quotient rounded to 32 bits.  values: device
  * bytes [rows, channels]; scales: device float32 [rows, ceil(channels / group)]; both
  * dense.  A group that holds an infinity or NaN has a scale that is none either. */
 int pv_rms_norm_8bit(const pv_norm_params* params, int group, void* values, float* scales, void* h, int64_t h_stride,

@@ -12,7 +12,7 @@
 // blocks are persistent, so that the weight is read once a block and its gradient is
 // summed in registers, then block by block in a fixed order by a second kernel.
 // In a row through the Python entries: 96,001 rows of 512 in bfloat16, forward 63 us (6.3 TB/s of its bytes), backward 64
-// with the join (6.1 TB/s); 24,571 rows of 1,024 to 8 bits 32 us (5.6 TB/s).
+// with the join (6.1 TB/s); 24,571 rows of 1,024 to 8 bits 34 us (5.1 TB/s).
 
 #include "pv_seq.cuh"
 
@@ -108,6 +108,36 @@ __device__ __forceinline__ void join_row(float* v, int lanes, float (*shared)[kT
       v[i] = kMax ? max_nan(v[i], u) : v[i] + u;
     }
 }
+
+// What y is divided by to 8 bits: scale = most / 448, rounded once (never 0, so that rows of zeros are zeros; what is not finite
+// stays so), and 1 / scale in two parts, so that y low + y high gives the e4m3 values that y / scale rounded to 32 bits has.
+//   scale: 1 / 448 in two parts is good to 2^-47, and no quotient by 448 comes as near to the middle of two floats (7 times
+//     the distance is a whole number of 2^-25 of the value, and not 0).
+//   high is below 1 / scale by less than 2^-21 of it (so that low is not negative, and zeros keep their sign); what is left, e, the sum e + e^2,
+//     low and its product with y are rounded, each off by less than 2^-24 2^-21: together by less than d = 2^-43 of the quotient.
+//   Rounded to 32 bits this falls on the other side of a border b 2^x of two e4m3 values (16 <= b < 32) than the quotient
+//     does only if the quotient is within d of the middle of the border and the next float, (b +- 2^-20) 2^x (below b = 16 b - 2^-21).  With
+//     S the scale's 24 bits as a whole number, its distance from there is |N -+ S 2^-20| / (b S), N a whole number: at least
+//     64 2^-20 / 2^29 = 2^-43 where S is 64 or more from a multiple of 2^20 (S 2^-21 likewise, b S being half as large).
+// One scale in 2^12 is not, and is divided by, as are those of sizes at which a product here may fall short of 2^-126.
+// (24,571 x 1,024 bfloat16, groups of 128: 31.5 us with products by a rounded reciprocal, which take one value in some 10^6 to the
+// wrong side, 34.4 like this, 43.6 with a division each; a scale for each row: 30.4, 30.5 and 38.5.)
+struct Quotients {
+  float scale, high, low;
+  bool quick;
+  __device__ __forceinline__ explicit Quotients(float most) {
+    constexpr double k = 1.0 / 448.0;
+    constexpr float kHigh = static_cast<float>(k), kLow = static_cast<float>(k - static_cast<double>(kHigh));
+    constexpr uint32_t kFrom = (127u - 90) << 23, kTo = (127u + 90) << 23;  // 2^-90, 2^90
+    scale = fmaf(most, kHigh, most * kLow);
+    quick = __float_as_uint(most) - kFrom < kTo - kFrom && ((__float_as_uint(scale) + 128) & 0xFFFFF) > 256;
+    if (!quick) scale = max_nan(most / 448.0f, 1.17549435e-38f);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(high) : "f"(scale));  // (good to 2^-23)
+    high *= 1.0f - 0x1p-22f;
+    const float e = fmaf(-scale, high, 1.0f);
+    low = high * fmaf(e, e, e);
+  }
+};
 
 // Channels c .. c + 8 as they lie in memory, opened where they are used.
 template <typename T, bool kVec>
@@ -251,14 +281,23 @@ __global__ void __launch_bounds__(kThreads, kVec && kThreads == 256 ? kBlocks<T,
       auto put = [&](int j, const float* y, float most) {
         const int p = j * lanes + lane, c = p * kV;
         if (!on || c >= a.C) return;
-        // Never 0, so that rows of zeros are zeros; whatever is not finite stays so.
-        const float scale = max_nan(most * (1.0f / 448.0f), 1.17549435e-38f), inv = 1.0f / scale;
+        unsigned short b[kV / 2];
+        const Quotients by(most);
+        const float scale = by.scale;
         if ((p & ((1 << a.group_lanes_log2) - 1)) == 0 && (a.groups > 1 || p == 0))
           a.scales[row * a.groups + (a.groups > 1 ? p >> a.group_lanes_log2 : 0)] = scale;
-        unsigned short b[kV / 2];
+        if (by.quick) {
 #pragma unroll
-        for (int i = 0; i < kV; i += 2)
-          b[i / 2] = __nv_cvt_float2_to_fp8x2(make_float2(y[i] * inv, y[i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+          for (int i = 0; i < kV; i += 2) {
+            float q0, q1;
+            mul2(q0, q1, y[i], y[i + 1], by.low, by.low);
+            fma2(q0, q1, y[i], y[i + 1], by.high, by.high, q0, q1);
+            b[i / 2] = __nv_cvt_float2_to_fp8x2(make_float2(q0, q1), __NV_SATFINITE, __NV_E4M3);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < kV; i += 2) b[i / 2] = __nv_cvt_float2_to_fp8x2(make_float2(y[i] / scale, y[i + 1] / scale), __NV_SATFINITE, __NV_E4M3);
+        }
         unsigned char* out = reinterpret_cast<unsigned char*>(a.y + row * a.y_row) + c;
         if constexpr (kVec) {
           *reinterpret_cast<uint2*>(out) = make_uint2(b[0] | static_cast<uint32_t>(b[1]) << 16, b[2] | static_cast<uint32_t>(b[3]) << 16);
