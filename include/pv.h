@@ -586,7 +586,8 @@ int pv_cross_entropy(const pv_loss_params* params, float* loss, float* lse, pv_s
  * and lse (float32 [rows]; dlse NULL: zeros; what dloss holds for a negative target is not
  * looked at) and the forward call's lse.  With G[t][v] = (dloss + dlse) softmax(z) - dloss
  * [v = target]: dx = G weight, dweight = G^T x.  The tensor cores take G rounded to dtype, its
- * factors divided by the largest one.  Where both factors of a row are 0, its G is 0 whatever its
+ * factors divided by the largest one of the call; PV_F16 holds it to within 2^-39 of that at best, which shows
+ * in rows whose factors are smaller by many powers of two.  Where both factors of a row are 0, its G is 0 whatever its
  * logits are; its x, which is multiplied with that, has to be finite all the same.  Sums are taken in 32 bits in a fixed order; both results are
  * written whole. */
 int pv_cross_entropy_backward(const pv_loss_params* params, const float* dloss, const float* dlse, const float* lse, void* dx,

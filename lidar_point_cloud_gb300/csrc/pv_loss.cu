@@ -21,10 +21,12 @@
 // vocabulary in pieces: G of a piece in the tensors' type (so that the tensor cores can
 // take it), then its products, dx summed over the pieces in 32 bits.
 //
-// What G is rounded to: its factors are divided by the largest |dloss| (and times 2^14 in float16,
-// whose exponents end at 2^-24), which the results are multiplied with.  So the usual
+// What G is rounded to: its factors are divided by the largest |dloss + dlse| or |dloss| of the call (and times 2^14 in
+// float16, whose exponents end at 2^-24), which the results are multiplied with.  So the usual
 // mean over rows gives factors of exactly 1, a target's gradient near -1 loses little, and
-// float16 holds probabilities down to 2^-28 whole.
+// float16 holds probabilities down to 2^-28 whole in rows of the largest weight.  A row of a weight 2^-n of it has them
+// whole down to 2^(n - 28) only, and from there on to within 2^-39 of the largest weight: both products take the same G, and the one over
+// rows needs one scale for all of them.
 
 #include "pv_attn.cuh"
 #include "pv_tc.cuh"
