@@ -29,9 +29,9 @@
 // What bounds it: products of 64 and 128 columns out of shared memory (50 + 0.48 N cycles for N columns, 128
 // rows and 16 of the depth, whatever their order: some 1,300 to 2,600 cycles a chunk in each kernel), the
 // chain product - decay - product - output beside them, and some 5 us at the beginning of each kernel.
-// Measured: 8 ragged frames of up to 6,000 tokens, 8 heads of 64: 58 us (states 24, join 4, outputs 28); 24,571
-// tokens, 8 heads of 128: 84 us (36, 5, 42).  One kernel that carries the state from chunk to chunk beside the outputs:
-// 65 and 83 us, but 91 instead of 84 for a training step, whose chains it cannot cut as finely.
+// Measured: 8 ragged frames of up to 6,000 tokens, 8 heads of 64: 57 us (states 24, join 4, outputs 28); 24,571
+// tokens, 8 heads of 128: 84 us (36, 5, 42); a training step on 4 frames of up to 4,000, 83.  One kernel that carries the state from
+// chunk to chunk beside the outputs: 65, 83 and 91 us; it cannot cut the chains as finely, and is as quick only for the long frame.
 
 #include "pv_attn.cuh"
 #include "pv_tc.cuh"
@@ -94,8 +94,8 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return m;
 }
 
-// e^(d x) as the sum of two numbers, good to some 2^-27 (a state goes through one a chunk, and an error
-// of 2^-22 in each would add up).  y = d x = n ln 2 + r with r in two parts; e^r = 1 + r + q, q =
+// e^(d x) as the sum of two numbers, good to 2^-25.3 (q's three roundings; 2^-26 is the most that was seen.  A state goes
+// through one a chunk, and an error of 2^-22 in each would add up).  y = d x = n ln 2 + r with r in two parts; e^r = 1 + r + q, q =
 // r^2 / 2 + r^3 / 6 + ..., at most 0.071, by its series; the sum's rounding is kept.
 __device__ __forceinline__ float2 decay_exact(float d, float x) {
   constexpr double kLn2 = 0.69314718055994530942;
