@@ -515,7 +515,8 @@ int pv_linear_attention_step(const pv_linear_step_params* params, const pv_heads
  * Root-mean-square norm of rows, with the residual's addition in front of it:
  *   h = x + residual, rounded to dtype (it is what the next layer adds to);
  *   y = h / sqrt(mean(h^2) + eps) * weight          (over the channels).
- *   rows          0 <= rows < 2^31;  channels  1 .. 16384.
+ *   rows          0 <= rows < 2^31;  channels  1 .. 16384.  A row whose squares' sum passes 32 bits (some 1e38)
+ *                 is 0, one that holds NaN or an infinity has NaN.
  *   x, residual   device [rows, channels] of dtype (PV_F32, PV_BF16, PV_F16), row
  *                 strides in elements >= channels, or 0 (one row seen as many); any
  *                 alignment (rows of a multiple of 8 channels on 16-byte boundaries are read in
@@ -565,7 +566,7 @@ int pv_rms_norm_backward(const pv_norm_params* params, const void* dy, int64_t d
  *                 PV_F16, on 16-byte boundaries, row strides (elements) multiples of 8, >= channels.
  *   targets       device int64 [rows].
  *   loss, lse     device float32 [rows].
- * Logits, sums and losses are held in 32 bits.
+ * Logits, sums and losses are held in 32 bits; a row with a logit that is +inf or NaN has NaN.
  */
 #define PV_LOSS_MAX_ROWS (INT64_C(1) << 26)
 #define PV_LOSS_MAX_CLASSES (INT64_C(1) << 26)

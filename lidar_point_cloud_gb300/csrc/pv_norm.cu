@@ -173,7 +173,8 @@ struct Row8 {
 // 8 bits 56 with 5, 49 with 4 and loads ahead; 96,001 x 512 62 with 3 and 66 with loads ahead, to 8 bits 62 with 4, 56 with 3 and loads
 // ahead; 17,000 x 3,000 74 with 2, 64 with loads ahead, to 8 bits 92 and 73.  32 bits: 60,000 x 512 83 with 2,
 // 91 with 3 blocks.  Backward, 16 bits: 96,001 x 512 78 with 3, 64 with 2 and loads ahead; 25,000 x 2,048 95 with 1, 72 with
-// loads ahead, but 4,000 x 16,384 in 512 threads 145 without, 200 with.  32 bits: 60,000 x 512 85 with 3, 74 with 2 blocks and 86 with loads ahead.
+// loads ahead, but 4,000 x 16,384 in 512 threads, whose rows and sums of the weight's gradient do not fit into 128 registers as it
+// is (356 bytes a thread spilled, 464 with 32 bits), 145 without, 200 with.  32 bits: 60,000 x 512 85 with 3, 74 with 2 blocks and 86 with loads ahead.
 template <typename T, int kP, int kForm>
 constexpr int kBlocks = kP == 4 ? 2 : kP == 2 ? (sizeof(T) == 4 ? 2 : 3) : kForm == kPlainOut ? 6 : 4;
 template <typename T, int kP, bool kVec, int kForm>

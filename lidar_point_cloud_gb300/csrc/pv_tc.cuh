@@ -1,4 +1,4 @@
-// Thin wrappers of the sm_103a instructions that the attention kernels use:
+// Thin wrappers of the sm_103a instructions that the attention, linear attention and cross entropy kernels use:
 // mbarriers with bounded waits, TMA tile loads, tensor memory, tcgen05.mma.
 
 #pragma once
@@ -153,7 +153,7 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* r) {
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(addr));
 }
-// 32, 64 or 128 columns of the thread's lane, waited for in the same statement: whatever
+// 32 or 64 columns of the thread's lane, or 16 in two or three places, waited for in the same statement: whatever
 // the compiler does with the registers, moving them or spilling them, comes after the wait.
 __device__ __forceinline__ void tmem_read32(uint32_t addr, float* r) {
   asm volatile(
