@@ -515,7 +515,7 @@ int pv_linear_attention_step(const pv_linear_step_params* params, const pv_heads
  * Root-mean-square norm of rows, with the residual's addition in front of it:
  *   h = x + residual, rounded to dtype (it is what the next layer adds to);
  *   y = h / sqrt(mean(h^2) + eps) * weight          (over the channels).
- *   rows          0 <= rows < 2^31;  channels  1 .. 16384.  A row whose squares' sum passes 32 bits (some 1e38)
+ *   rows          0 <= rows < 2^31;  channels  1 .. 16384.  A row whose squares' sum passes 32 bits (some 3e38)
  *                 is 0, one that holds NaN or an infinity has NaN.
  *   x, residual   device [rows, channels] of dtype (PV_F32, PV_BF16, PV_F16), row
  *                 strides in elements >= channels, or 0 (one row seen as many); any
